@@ -76,7 +76,12 @@ typedef struct CUstream_st *gqa_stream_t;
  * kev PR #202 ("Measurements") loads its models in fp32 with TF32 off: GQA_F32_TC
  * uses no TF32; its split operands carry twice TF32's 11 significant bits.
  */
-typedef enum { GQA_F32 = 0, GQA_BF16 = 1, GQA_F32_TC = 2 } gqa_dtype_t;
+typedef enum {
+  GQA_F32 = 0,
+  GQA_BF16 = 1,
+  GQA_F32_TC = 2,
+  GQA_E4M3 = 3 /* cache pages only: float8 e4m3 codes with one fp32 scale per row of d */
+} gqa_dtype_t;
 
 typedef enum { GQA_MASK_CAUSAL = 0, GQA_MASK_PREFIX_BRANCH = 1 } gqa_mask_t;
 
@@ -393,6 +398,185 @@ int gqa_attn_fwd_static_ws(const void *q, const void *k, const void *v, void *ou
                            int mask_kind, int64_t q_pos_offset,
                            const int32_t *segment_ids_q, const int32_t *segment_ids_kv,
                            gqa_stream_t stream);
+
+/*
+ * Decoding from a cache.  The shared state of system1-omni issue #27 (item 3: the state
+ * is computed once, then one branch per question) is what a decoder keeps: its keys and
+ * values stay in a cache, the next tokens' rotated keys and their values are appended,
+ * and one token, or a tree of drafted ones, attends to all of it.  The entry points
+ * below are the four steps: rotary positions, the cache's write and read, and the
+ * attention of drafted tokens over it.  They differ from those above in three ways:
+ * inputs may be strided, lengths live on the device, and device-side errors go to a
+ * status word that belongs to the cache.
+ *
+ * gqa_rows_t: a [B, H, L, d] tensor (d = 256) whose rows of d elements are contiguous.
+ *   The strides count elements; data and every stride of a dimension longer than one
+ *   are multiples of 16 bytes.  The output of a projection ([B, L, H, d]) is one such
+ *   view.
+ */
+typedef struct {
+  void *data;
+  int64_t stride_b, stride_h, stride_l;
+  int32_t H;
+} gqa_rows_t;
+
+/*
+ * gqa_cache_t: a pool of pages that sequences share out through their page tables.
+ *   k, v              device, [n_pages][Hkv][page_size][d] of dtype, 16-byte aligned;
+ *                     stride_page, stride_head and stride_token (elements, the same for
+ *                     k and v, multiples of 16 bytes) allow other orders of the first
+ *                     three dimensions.
+ *   k_scale, v_scale  device fp32 [n_pages][Hkv][page_size], dense: the value of a
+ *                     GQA_E4M3 row is code * scale.  NULL for the other dtypes.
+ *   status            device, one int32 word that the owner zeroes when it makes the
+ *                     pool, or NULL.  The calls record the first device-side error in
+ *                     it (GQA_ERR_DEVICE_BOUNDS: a page index outside 0 .. n_pages - 1
+ *                     or a length outside the page table; GQA_ERR_DEVICE_TIMEOUT) and
+ *                     never clear it; read it with gqa_attn_status(status, stream).
+ *                     What a bad index or length names is neither read nor written.
+ *   Hkv, page_size    key/value heads; tokens per page, a power of two in 8 .. 1024.
+ *   dtype             GQA_F32, GQA_BF16 or GQA_E4M3.
+ * A page table is device int32 [B][max_pages], dense: token j of sequence b is slot
+ * j % page_size of page page_table[b][j / page_size].  Entries past a sequence's last
+ * token are not read.  Sequences may share pages that nothing writes.
+ */
+typedef struct {
+  void *k, *v;
+  float *k_scale, *v_scale;
+  int32_t *status;
+  int64_t stride_page, stride_head, stride_token, n_pages;
+  int32_t Hkv, page_size, dtype;
+} gqa_cache_t;
+
+typedef enum { GQA_ROPE_HALF = 0, GQA_ROPE_INTERLEAVED = 1 } gqa_rope_layout_t;
+typedef enum {
+  GQA_ROPE_PLAIN = 0,
+  GQA_ROPE_LINEAR = 1,
+  GQA_ROPE_NTK = 2,
+  GQA_ROPE_YARN = 3
+} gqa_rope_scaling_t;
+
+/*
+ * gqa_rope_t: the rotation of a [.., d] row at position p.  Pair i < rot / 2 of the
+ * first `rot` columns -- (x[i], x[i + rot / 2]) with GQA_ROPE_HALF, (x[2 i], x[2 i + 1])
+ * with GQA_ROPE_INTERLEAVED -- turns by the angle a = p * f_i:
+ *     y1 = m (x1 cos a - x2 sin a),   y2 = m (x2 cos a + x1 sin a);
+ * the other columns are left as they are.
+ *   turns      device, rot / 2 words from gqa_attn_rope_turns: f_i / (2 pi) as a binary
+ *              fraction of 64 bits.  p * turns modulo 2^64 is then the angle's exact
+ *              fraction of a turn, so far positions lose nothing.
+ *   magnitude  m; rot: a multiple of 16 in 16 .. 256; layout: gqa_rope_layout_t.
+ *   positions  device int32 [B][L] with row stride positions_stride_b (0: one row for
+ *              all sequences), any values; or NULL: token l of sequence b is at
+ *              pos_offset + l (gqa_attn_cache_write: at its own place in the sequence
+ *              plus pos_offset).
+ */
+typedef struct {
+  const uint64_t *turns;
+  const int32_t *positions;
+  int64_t positions_stride_b, pos_offset;
+  float magnitude;
+  int32_t rot, layout;
+} gqa_rope_t;
+
+/*
+ * gqa_attn_rope_freqs: writes f_i, i < rot / 2, to inv_freq (host) and m to *magnitude.
+ *   GQA_ROPE_PLAIN   f_i = base^(-2 i / rot)
+ *   GQA_ROPE_LINEAR  f_i / factor: positions interpolated
+ *   GQA_ROPE_NTK     base * factor^(rot / (rot - 2)) in place of base: the slowest pair
+ *                    slows by factor, the fastest by nothing
+ *   GQA_ROPE_YARN    by parts: f_i g + f_i / factor (1 - g) with g = clamp((r_i -
+ *                    beta_slow) / (beta_fast - beta_slow), 0, 1), r_i = original_length
+ *                    f_i / (2 pi) the pair's turns over the length trained on, and
+ *                    m = 0.1 ln(factor) + 1 (the YaRN paper, Peng et al. 2023, section 3)
+ *   m = 1 but for GQA_ROPE_YARN.  GQA_ERR_INVALID_ARG: a null pointer, base <= 1, factor
+ *   < 1, original_length < 1 or beta_fast <= beta_slow (GQA_ROPE_YARN), rot of 2 with
+ *   GQA_ROPE_NTK, or rot not an even number in 2 .. 256.  Host-only.
+ * gqa_attn_rope_turns: the n words of `turns` (host) for any finite frequencies inv_freq
+ *   (host; computed above or the user's own).  GQA_ERR_INVALID_ARG for a null pointer, n <
+ *   1 or a frequency that is not finite.  Host-only; the caller copies them to the device.
+ */
+int gqa_attn_rope_freqs(int rot, double base, int scaling, double factor, int64_t original_length, double beta_fast,
+                        double beta_slow, double *inv_freq, double *magnitude);
+int gqa_attn_rope_turns(const double *inv_freq, int n, uint64_t *turns);
+
+/*
+ * gqa_attn_rope: rotates the rows of x (and of x2, when it is not NULL: q and k in one
+ * launch) into out (and out2), of the same dtype (GQA_F32 or GQA_BF16; fp32 arithmetic,
+ * one rounding).  With inverse != 0 it turns by -a with the same m, which is the
+ * gradient of the rotation: dx = the inverse rotation of dy.  out may be x itself.
+ * Enqueues one kernel on `stream`; B or L of 0 enqueues nothing.  Errors:
+ * GQA_ERR_INVALID_ARG (a null pointer, a negative size, H < 1, another dtype or layout,
+ * rot out of its range), GQA_ERR_UNSUPPORTED (d != 256), GQA_ERR_MISALIGNED (data or a
+ * stride not a multiple of 16 bytes), GQA_ERR_LAUNCH.
+ */
+int gqa_attn_rope(const gqa_rows_t *x, const gqa_rows_t *out, const gqa_rows_t *x2, const gqa_rows_t *out2, int B,
+                  int64_t L, int d, int dtype, const gqa_rope_t *rope, int inverse, gqa_stream_t stream);
+
+/*
+ * gqa_attn_cache_write: appends L tokens of each of B sequences to the cache.
+ *   k, v        views of H = Hkv heads, dtype GQA_F32 or GQA_BF16.
+ *   page_table  [B][max_pages]; start: device int32 [B], the tokens a sequence holds
+ *               already: its token i goes to place start[b] + i.
+ *   lens        device int32 [B], tokens of each sequence to write (values above L count
+ *               as L, below 0 as 0), or NULL: L of each.
+ *   rope        the keys are rotated in fp32 before they are rounded; NULL: stored as they
+ *               are.  rope->positions NULL: position = start[b] + i + pos_offset.  Drafted
+ *               tokens of a tree share positions: give them.
+ * GQA_F32 and GQA_BF16 pages get the value rounded once.  GQA_E4M3 pages get, per row, the
+ * scale 2^ceil(log2(amax / 448)) with amax the largest finite |x| of the row (scale 1 when
+ * amax is 0; the exponent kept in -120 .. 120), and the codes of x / scale, rounded to
+ * nearest even; a power of two makes the division exact, and costs a float format no
+ * precision.  Infinities become +-448, NaN stays NaN.
+ * No two tokens of a call may go to the same slot.  Slots that no token goes to are left as
+ * they were.  A token whose place is outside the page table, or whose page index is outside
+ * the pool, is skipped and recorded in cache->status.  Enqueues one kernel.  Errors as
+ * gqa_attn_rope, and GQA_ERR_INVALID_ARG for scales that do not fit the dtype, k or v with
+ * other heads than the cache, a page_size or max_pages out of range.
+ *
+ * gqa_attn_cache_read: the first lens[b] tokens of each sequence as dense k_out and v_out
+ * [B, Hkv, max_len, d] of dtype_out (GQA_F32 or GQA_BF16, one rounding), zeros behind them
+ * and for a bad page index (recorded); lens above max_len count as max_len, below 0 as 0.
+ * Enqueues one kernel.  Errors as above.
+ */
+int gqa_attn_cache_write(const gqa_cache_t *cache, const gqa_rows_t *k, const gqa_rows_t *v,
+                         const int32_t *page_table, int64_t max_pages, const int32_t *start, const int32_t *lens,
+                         int B, int64_t L, int d, int dtype, const gqa_rope_t *rope, gqa_stream_t stream);
+int gqa_attn_cache_read(const gqa_cache_t *cache, const int32_t *page_table, int64_t max_pages, const int32_t *lens,
+                        void *k_out, void *v_out, int B, int64_t max_len, int d, int dtype_out, gqa_stream_t stream);
+
+/*
+ * gqa_attn_fwd_tree: attention of T drafted tokens per sequence over the cache.  T = 1 is
+ * one decoding step.  Sequence b holds context_lens[b] tokens and, behind them, its first
+ * tree_lens[b] drafted ones, whose keys and values are in the cache already.  Drafted token
+ * t sees the whole context and the drafted tokens u < tree_lens[b] with tree_mask[t][u]:
+ *     out[b,h,t] = sum_j softmax_j(<q[b,h,t], k[b,g,j]> / 16) v[b,g,j],  lse as gqa_attn_fwd.
+ *   q             view of Hq heads and T tokens, dtype GQA_F32 or GQA_BF16; Hq / Hkv in
+ *                 {1, 2, 4, 8, 16}.
+ *   page_table, max_pages, context_lens  as above (context_lens: device int32 [B], 0 or
+ *                 more; context and drafted tokens fit the page table).
+ *   tree_lens     device int32 [B], or NULL: T of each.  Tokens t >= tree_lens[b] are
+ *                 padding: no visible key.
+ *   tree_mask     device bytes [T][T], or [B][T][T] with mask_stride_b = T * T (0: one mask
+ *                 for all); not 0 = visible, and nothing else is implied: a row's own token
+ *                 too has to be named.  NULL: a chain, token t sees u <= t.
+ *   out, lse      device, written whole: [B, Hq, T, d] of dtype and [B, Hq, T] fp32.  A row
+ *                 with no visible key gets out = 0 and lse = -inf.
+ *   workspace     device, >= gqa_attn_tree_workspace_bytes(...), 16-byte aligned,
+ *                 overwritten; calls that share one must be ordered on one stream.
+ * What a row's mask hides does not reach the row, NaN and infinities among it.  Work is cut
+ * evenly over the SMs whatever the lengths; partial results are merged in a fixed order, so
+ * equal calls give equal bits.  GQA_BF16 queries over GQA_BF16 or GQA_E4M3 pages run on the
+ * tensor cores, the other pairs of types on the FP32 pipe.  Errors: as gqa_attn_cache_write, GQA_ERR_UNSUPPORTED
+ * (d, Hq / Hkv, T > 1024), GQA_ERR_WORKSPACE.
+ * gqa_attn_tree_workspace_bytes returns 0 for a shape that the call rejects.  Host-only.
+ */
+size_t gqa_attn_tree_workspace_bytes(int B, int Hq, int Hkv, int64_t T, int64_t max_pages, int page_size, int d,
+                                     int dtype, int cache_dtype);
+int gqa_attn_fwd_tree(const gqa_rows_t *q, const gqa_cache_t *cache, const int32_t *page_table, int64_t max_pages,
+                      const int32_t *context_lens, const int32_t *tree_lens, const uint8_t *tree_mask,
+                      int64_t mask_stride_b, void *out, float *lse, int B, int64_t T, int d, int dtype,
+                      void *workspace, size_t workspace_bytes, gqa_stream_t stream);
 
 /* Static, human-readable text for a gqa_status_t; never NULL. */
 const char *gqa_attn_strerror(int status);

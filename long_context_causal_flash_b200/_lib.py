@@ -15,7 +15,7 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(
     HERE, "libgqa_attn_debug_bounds.so" if os.environ.get("GQA_ATTN_DEBUG_BOUNDS") == "1" else "libgqa_attn.so")
 
-GQA_F32, GQA_BF16, GQA_F32_TC = 0, 1, 2
+GQA_F32, GQA_BF16, GQA_F32_TC, GQA_E4M3 = 0, 1, 2, 3
 GQA_MASK_CAUSAL, GQA_MASK_PREFIX_BRANCH = 0, 1
 GQA_OK = 0
 GQA_ERR_INVALID_ARG = -1
@@ -69,8 +69,41 @@ SIGNATURES = {
     "gqa_attn_selftest_wait": (_c.c_int, [_c.c_void_p, _c.c_size_t, _c.c_int64, _c.c_void_p]),
     "gqa_attn_selftest_bounds": (_c.c_int, [_c.c_void_p, _c.c_size_t, _c.c_int, _c.c_void_p]),
     "gqa_attn_probe_ffma2": (_c.c_int, [_c.c_void_p, _c.c_int, _c.c_int, _c.c_int, _c.c_void_p]),
+    "gqa_attn_rope_freqs": (_c.c_int, [_c.c_int, _c.c_double, _c.c_int, _c.c_double, _c.c_int64, _c.c_double,
+                                       _c.c_double, _c.c_void_p, _c.c_void_p]),
+    "gqa_attn_rope_turns": (_c.c_int, [_c.c_void_p, _c.c_int, _c.c_void_p]),
+    "gqa_attn_rope": (_c.c_int, [_c.c_void_p] * 4 + [_c.c_int, _c.c_int64, _c.c_int, _c.c_int, _c.c_void_p, _c.c_int,
+                                                     _c.c_void_p]),
+    "gqa_attn_cache_write": (_c.c_int, [_c.c_void_p] * 4 + [_c.c_int64, _c.c_void_p, _c.c_void_p, _c.c_int, _c.c_int64,
+                                                            _c.c_int, _c.c_int, _c.c_void_p, _c.c_void_p]),
+    "gqa_attn_cache_read": (_c.c_int, [_c.c_void_p, _c.c_void_p, _c.c_int64, _c.c_void_p, _c.c_void_p, _c.c_void_p,
+                                       _c.c_int, _c.c_int64, _c.c_int, _c.c_int, _c.c_void_p]),
+    "gqa_attn_tree_workspace_bytes": (_c.c_size_t, [_c.c_int, _c.c_int, _c.c_int, _c.c_int64, _c.c_int64, _c.c_int,
+                                                    _c.c_int, _c.c_int, _c.c_int]),
+    "gqa_attn_fwd_tree": (_c.c_int, [_c.c_void_p, _c.c_void_p, _c.c_void_p, _c.c_int64, _c.c_void_p, _c.c_void_p,
+                                     _c.c_void_p, _c.c_int64, _c.c_void_p, _c.c_void_p, _c.c_int, _c.c_int64, _c.c_int,
+                                     _c.c_int, _c.c_void_p, _c.c_size_t, _c.c_void_p]),
     "gqa_attn_strerror": (_c.c_char_p, [_c.c_int]),
 }
+
+
+# The structures of include/gqa_attn.h, field by field.
+class Rows(ctypes.Structure):
+    _fields_ = [("data", _c.c_void_p), ("stride_b", _c.c_int64), ("stride_h", _c.c_int64), ("stride_l", _c.c_int64),
+                ("H", _c.c_int32)]
+
+
+class Cache(ctypes.Structure):
+    _fields_ = [("k", _c.c_void_p), ("v", _c.c_void_p), ("k_scale", _c.c_void_p), ("v_scale", _c.c_void_p),
+                ("status", _c.c_void_p), ("stride_page", _c.c_int64), ("stride_head", _c.c_int64),
+                ("stride_token", _c.c_int64), ("n_pages", _c.c_int64), ("Hkv", _c.c_int32), ("page_size", _c.c_int32),
+                ("dtype", _c.c_int32)]
+
+
+class Rope(ctypes.Structure):
+    _fields_ = [("turns", _c.c_void_p), ("positions", _c.c_void_p), ("positions_stride_b", _c.c_int64),
+                ("pos_offset", _c.c_int64), ("magnitude", _c.c_float), ("rot", _c.c_int32), ("layout", _c.c_int32)]
+
 
 _lib = None
 

@@ -116,6 +116,8 @@ int test_skip_fill() {
   return -1;
 }
 
+}  // namespace
+
 int64_t wait_budget_ns() {
   static int64_t budget = -1;
   if (budget < 0) {
@@ -128,7 +130,6 @@ int64_t wait_budget_ns() {
   return budget;
 }
 
-}  // namespace
 }  // namespace gqa
 
 using namespace gqa;

@@ -1,0 +1,155 @@
+// Device helpers shared by the decoding kernels (rotary positions, the paged cache, the
+// attention over it): 16-column loads and stores, e4m3 rows and page lookups.
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_fp8.h>
+
+#include "common.cuh"
+
+namespace gqa {
+
+// Element strides of a [B, H, L, d] view (gqa_rows_t).
+struct RowsView {
+  char* p;
+  int64_t sb, sh, sl;
+  int H;
+};
+
+// gqa_cache_t as the kernels take it; page_shift = log2(page_size).
+struct CacheView {
+  char *k, *v;
+  float *ks, *vs;
+  int32_t* status;
+  int64_t sp, sh, st, n_pages;
+  int Hkv, page_shift, dtype;
+};
+
+// gqa_rope_t without the frequencies' host part; turns == null: no rotation.
+struct RopeView {
+  const uint64_t* turns;
+  const int32_t* positions;
+  int64_t pos_sb, pos_offset;
+  float magnitude;
+  int rot, interleaved;
+};
+
+#if defined(__CUDACC__)
+
+// A row of 256 columns is the work of 16 threads, `unit` 0 .. 15, each with 16 columns.
+// A rotated unit (unit < rot / 16) holds pairs 8 unit .. 8 unit + 7: with the half layout
+// columns 8 unit + (0..7) and rot / 2 + 8 unit + (0..7), else columns 16 unit + (0..15).
+// c0 / c1 are the first columns of its two groups of eight.
+__device__ __forceinline__ void unit_columns(int unit, int rot, int interleaved, int* c0, int* c1) {
+  if (!interleaved && unit < rot / 16) {
+    *c0 = 8 * unit;
+    *c1 = rot / 2 + 8 * unit;
+  } else {
+    *c0 = 16 * unit;
+    *c1 = 16 * unit + 8;
+  }
+}
+
+__device__ __forceinline__ void load8(const float* p, float* x) {
+  const float4 a = *reinterpret_cast<const float4*>(p), b = *reinterpret_cast<const float4*>(p + 4);
+  x[0] = a.x, x[1] = a.y, x[2] = a.z, x[3] = a.w, x[4] = b.x, x[5] = b.y, x[6] = b.z, x[7] = b.w;
+}
+__device__ __forceinline__ void unpack8(uint4 u, float* x) {
+  const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    x[2 * i] = __uint_as_float(w[i] << 16);
+    x[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+  }
+}
+__device__ __forceinline__ void load8(const __nv_bfloat16* p, float* x) {
+  unpack8(*reinterpret_cast<const uint4*>(p), x);
+}
+__device__ __forceinline__ void store8(float* p, const float* x) {
+  *reinterpret_cast<float4*>(p) = make_float4(x[0], x[1], x[2], x[3]);
+  *reinterpret_cast<float4*>(p + 4) = make_float4(x[4], x[5], x[6], x[7]);
+}
+__device__ __forceinline__ void store8(__nv_bfloat16* p, const float* x) {
+  __nv_bfloat162 h[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) h[i] = __floats2bfloat162_rn(x[2 * i], x[2 * i + 1]);
+  *reinterpret_cast<uint4*>(p) = *reinterpret_cast<const uint4*>(h);
+}
+
+// Four e4m3 codes of a word as floats (exact), and the codes of four floats (nearest
+// even, saturating; NaN stays NaN).
+__device__ __forceinline__ void e4m3_decode4(uint32_t w, float* x) {
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2(__nv_fp8x2_storage_t((w >> (16 * i)) & 0xffffu), __NV_E4M3);
+    const float2 f = __half22float2(__half2(h));
+    x[2 * i] = f.x;
+    x[2 * i + 1] = f.y;
+  }
+}
+__device__ __forceinline__ uint32_t e4m3_encode4(const float* x) {
+  const uint32_t a = __nv_cvt_float2_to_fp8x2(make_float2(x[0], x[1]), __NV_SATFINITE, __NV_E4M3);
+  const uint32_t b = __nv_cvt_float2_to_fp8x2(make_float2(x[2], x[3]), __NV_SATFINITE, __NV_E4M3);
+  return a | (b << 16);
+}
+
+// The scale of a quantised row: the least power of two s with amax / s <= 448 = 1.75 * 2^8,
+// found in the bits of amax = f * 2^e, f in [1, 2): e - 8, and one more when f > 1.75.  The
+// exponent stays in -120 .. 120, so the scale and its reciprocal are normal numbers; a row
+// of zeros gets 1.
+__device__ __forceinline__ float e4m3_row_scale(float amax) {
+  if (!(amax > 0.f)) return 1.f;
+  const uint32_t bits = __float_as_uint(amax);
+  int e = int(bits >> 23) - 127 - 8 + ((bits & 0x7fffffu) > 0x600000u ? 1 : 0);
+  e = max(-120, min(120, e));
+  return __uint_as_float(uint32_t(e + 127) << 23);
+}
+
+// Page index of token `j`; -1 when the table or the pool does not hold it (recorded).
+__device__ __forceinline__ int page_of(const CacheView& c, const int32_t* table, int64_t max_pages, int64_t j) {
+  const int64_t slot = j >> c.page_shift;
+  int page = -1;
+  if (j >= 0 && slot < max_pages) page = __ldg(table + slot);
+  if (page < 0 || page >= c.n_pages) {
+    set_status(c.status, GQA_ERR_DEVICE_BOUNDS);
+    return -1;
+  }
+  return page;
+}
+
+// cos and sin of the eight pairs of a rotated unit at position p, times m.  p * turns
+// modulo 2^64 is the angle as a fraction of a turn, exact; its upper 32 bits, as a signed
+// number of 2^-32 turns in [-1/2, 1/2), go to fp32 and sincospi.
+__device__ __forceinline__ void unit_angles(const uint64_t* turns, int unit, int64_t p, float m, float sign, float* co,
+                                            float* si) {
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const uint64_t frac = uint64_t(p) * __ldg(reinterpret_cast<const unsigned long long*>(turns) + 8 * unit + i);
+    const float half_turns = float(int32_t(uint32_t(frac >> 32))) * 4.656612873077393e-10f;  // 2^-31
+    float s, c;
+    sincospif(half_turns, &s, &c);
+    co[i] = c * m;
+    si[i] = s * m * sign;
+  }
+}
+
+// Turns the 16 columns of a rotated unit (x[0..7], x[8..15] as loaded from c0 and c1).
+// Two branches of fixed indexes: one loop with computed ones would put x in local memory.
+__device__ __forceinline__ void turn_pair(float& x1, float& x2, float co, float si) {
+  const float a = x1, b = x2;
+  x1 = a * co - b * si;
+  x2 = b * co + a * si;
+}
+__device__ __forceinline__ void turn_unit(float* x, int interleaved, const float* co, const float* si) {
+  if (interleaved) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) turn_pair(x[2 * i], x[2 * i + 1], co[i], si[i]);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) turn_pair(x[i], x[8 + i], co[i], si[i]);
+  }
+}
+
+#endif  // __CUDACC__
+
+}  // namespace gqa

@@ -96,4 +96,19 @@ int launch_merge_splits(const float* o_part, const float* lse_part, void* out, f
 int launch_merge_pair(const float* o_a, const float* lse_a, const void* o_b, const float* lse_b, bool b_bf16,
                       void* o_out, float* lse_out, bool out_bf16, int64_t rows, cudaStream_t stream);
 
+// Decoding (decode.cuh): rotary positions and the paged cache.  B L tokens of 0 launch nothing.
+struct RowsView;
+struct CacheView;
+struct RopeView;
+int launch_rope(const RowsView& x, const RowsView& y, const RowsView& x2, const RowsView& y2, int B, int64_t L,
+                bool bf16, const RopeView& r, bool inverse, cudaStream_t stream);
+int launch_cache_write(const CacheView& c, const RowsView& k, const RowsView& v, const int32_t* table,
+                       int64_t max_pages, const int32_t* start, const int32_t* lens, int B, int64_t L, bool bf16,
+                       const RopeView& r, cudaStream_t stream);
+int launch_cache_read(const CacheView& c, const int32_t* table, int64_t max_pages, const int32_t* lens, void* k_out,
+                      void* v_out, int B, int64_t max_len, bool bf16, cudaStream_t stream);
+
+// Budget of a bounded device-side wait (GQA_ATTN_WAIT_BUDGET_NS).
+int64_t wait_budget_ns();
+
 }  // namespace gqa

@@ -15,6 +15,7 @@ Contents
 ``backward``   the gradients (dq, dk, dv) of the attention definition in float64.
 ``context``    attention against one key block of a sharded sequence, and the merge
                of partial results by their log-sum-exp.
+``decode``     rotary positions, quantised cache rows and the attention of drafted tokens.
 
 Sources (the three pages this build follows):
 
@@ -29,7 +30,8 @@ Sources (the three pages this build follows):
   kernel) and the code review.
 
 Every function here is pinned by tests in ``tests/test_oracle.py``,
-``tests/test_oracle_backward.py`` and ``tests/test_oracle_context.py`` against
+``tests/test_oracle_backward.py``, ``tests/test_oracle_context.py`` and
+``tests/test_oracle_decode.py`` against
 library routines, closed forms, invariants and the figures the pages print.
 """
 
@@ -43,4 +45,4 @@ from .exact import (  # noqa: F401
 from .plan import SKIP, PARTIAL, FULL, tile_plan  # noqa: F401
 from .backward import attention_backward  # noqa: F401
 from .context import attention_block, attention_block_backward, merge_partials  # noqa: F401
-from . import memory  # noqa: F401
+from . import decode, memory  # noqa: F401

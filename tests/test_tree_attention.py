@@ -1,0 +1,370 @@
+"""Attention of drafted tokens over the paged cache on the GPU against the float64 definition.
+
+Tolerances.  fp32 queries: the repository's bars for unit-variance inputs (out 2e-5, LSE
+1e-5), scaled by the size of the values where those are larger.  bf16 queries: products
+of bf16 (and e4m3) numbers are exact in fp32, so scores are off by the fp32 sums only, or, where a query is taken
+apart into two e4m3 pieces, by 2^-10 steps of a row scaled to 448: 2^-18.8 of its
+largest element times sum |k| / 16, below 2e-4 for these inputs, which bounds the LSE.
+Each probability is rounded to at least 8 bits, off by at most 2^-8 of itself, and so is the output: out is
+off by at most 2^-8 (|out| + sum p |v| / sum p) plus the scores' share, 2 x 2e-4 of
+that sum.
+"""
+
+import numpy as np
+import pytest
+import torch
+
+import long_context_causal_flash_b200 as gqa
+from long_context_causal_flash_b200 import cache, rotary
+from oracle import decode
+
+pytestmark = pytest.mark.gpu
+
+E4M3 = torch.float8_e4m3fn
+F32, BF16 = torch.float32, torch.bfloat16
+PAIRS = [(F32, F32), (BF16, BF16), (BF16, E4M3), (F32, BF16), (F32, E4M3), (BF16, F32)]
+IDS = ["f32", "bf16", "bf16_e4m3", "f32_bf16", "f32_e4m3", "bf16_f32"]
+
+
+def _tree(T, seed):
+    rng = np.random.default_rng(seed)
+    mask = np.eye(T, dtype=bool)
+    for t in range(1, T):
+        mask[t] |= mask[rng.integers(0, t)]
+    return mask
+
+
+class Problem:
+    """Filled pages (garbage, NaN by default, in every slot that no sequence holds) and what they stand for."""
+
+    def __init__(self, dev, B, Hq, Hkv, T, ctx, page, dtype, kind, seed=0, drafted=None, garbage=0xff, gain=1.0):
+        g = torch.Generator().manual_seed(seed)
+        self.ctx = list(ctx)
+        self.drafted = list(drafted) if drafted is not None else [T] * B
+        per = max(1, -(-(max(self.ctx) + T) // page))
+        n = B * per + 2
+        self.pool = cache.PagedCache.empty(n, Hkv, page, kind, dev)
+        for t in (self.pool.k, self.pool.v):
+            t.view(torch.uint8).fill_(garbage)
+        if kind == E4M3:
+            for t in (self.pool.k_scale, self.pool.v_scale):
+                t.fill_(float("nan"))
+        self.table = torch.randperm(n, generator=g)[: B * per].view(B, per).to(torch.int32)
+        L = max(c + d for c, d in zip(self.ctx, self.drafted))
+        self.k, self.v = (torch.randn((B, Hkv, max(L, 1), 256), generator=g).to(BF16) * gain for _ in range(2))
+        lens = torch.tensor([c + d for c, d in zip(self.ctx, self.drafted)], dtype=torch.int32)
+        self.table = self.table.to(dev)
+        cache.write(self.pool, self.k.to(dev), self.v.to(dev), self.table,
+                    torch.zeros(B, dtype=torch.int32, device=dev), lens=lens.to(dev))
+        if kind == E4M3:
+            self.k, self.v = (torch.as_tensor(y * s[..., None]) for y, s in map(decode.quantise, (self.k, self.v)))
+        self.q = torch.randn((B, Hq, T, 256), generator=g).to(dtype)
+        self.dev, self.ctx_dev = dev, torch.tensor(self.ctx, dtype=torch.int32, device=dev)
+        self.drafted_dev = torch.tensor(self.drafted, dtype=torch.int32, device=dev) if drafted is not None else None
+
+    def attend(self, mask=None, **kw):
+        if mask is not None:
+            mask = torch.as_tensor(mask).to(self.dev)
+        return cache.attend(self.q.to(self.dev), self.pool, self.table, self.ctx_dev, tree_mask=mask,
+                            tree_lens=self.drafted_dev, **kw)
+
+    def check(self, out, lse, mask=None, rows=None):
+        exact = self.q.dtype == F32
+        out, lse = out.double().cpu().numpy(), lse.double().cpu().numpy()
+        for b in range(len(self.ctx)) if rows is None else rows:
+            m = None if mask is None else np.asarray(mask)[b] if np.ndim(mask) == 3 else np.asarray(mask)
+            o, l, spread = decode.tree_attention(self.q[b], self.k[b], self.v[b], self.ctx[b], self.drafted[b], m)
+            empty = np.isneginf(l)
+            assert np.array_equal(np.isneginf(lse[b]), empty), "rows without a visible key"
+            assert not out[b][empty].any()
+            fin = ~empty
+            if not fin.any():
+                continue
+            if exact:
+                tol_o, tol_l = 2e-5 * max(1.0, float(np.abs(o).max())), 1e-5
+            else:
+                tol_o, tol_l = 2.0 ** -8 * (np.abs(o) + spread) + 4e-4 * spread, 2e-4
+            d_l = np.abs(lse[b][fin] - l[fin]).max()
+            d_o = np.abs(out[b] - o)
+            assert d_l <= tol_l, f"sequence {b}: LSE off by {d_l:.2e}"
+            assert np.all(d_o <= tol_o), f"sequence {b}: out off by {(d_o - tol_o).max():.2e} more than allowed"
+
+
+@pytest.mark.parametrize("dtype,kind", PAIRS, ids=IDS)
+@pytest.mark.parametrize("ctx", [0, 1, 127, 128, 700])
+def test_one_token(cuda_device, dtype, kind, ctx):
+    p = Problem(cuda_device, 1, 16, 4, 1, [ctx], 16, dtype, kind, seed=ctx)
+    p.check(*p.attend())
+    assert cache.status(p.pool) == 0
+
+
+@pytest.mark.parametrize("dtype,kind", PAIRS, ids=IDS)
+@pytest.mark.parametrize("T,page", [(3, 8), (13, 64), (70, 128)])
+def test_trees(cuda_device, dtype, kind, T, page):
+    ctx = [130, 0, 259]
+    p = Problem(cuda_device, 3, 8, 2, T, ctx, page, dtype, kind, seed=T)
+    p.check(*p.attend())
+    masks = np.stack([_tree(T, b) for b in range(3)])
+    p.check(*p.attend(masks), mask=masks)
+    p.check(*p.attend(masks[0]), mask=masks[0])
+    p.check(*p.attend(masks.astype(np.uint8) * 3), mask=masks)
+
+
+@pytest.mark.parametrize("dtype,kind", PAIRS[:3], ids=IDS[:3])
+@pytest.mark.parametrize("Hq,Hkv", [(1, 1), (5, 5), (6, 3), (8, 1), (16, 1), (32, 4)])
+def test_head_layouts(cuda_device, dtype, kind, Hq, Hkv):
+    p = Problem(cuda_device, 2, Hq, Hkv, 5, [37, 301], 32, dtype, kind, seed=Hq)
+    masks = _tree(5, 3)
+    p.check(*p.attend(masks), mask=masks)
+
+
+@pytest.mark.parametrize("dtype,kind", PAIRS[:3], ids=IDS[:3])
+def test_empty_and_padded_rows(cuda_device, dtype, kind):
+    T = 6
+    p = Problem(cuda_device, 5, 16, 4, T, [0, 50, 0, 300, 0], 16, dtype, kind, seed=5, drafted=[6, 2, 0, 0, 3])
+    p.check(*p.attend())
+    mask = _tree(T, 1)
+    mask[2] = mask[5] = False  # rows that name nobody: empty where there is no context
+    p.check(*p.attend(mask), mask=mask)
+    mask[:] = False
+    p.check(*p.attend(mask), mask=mask)
+    # outputs are written whole: what was in them does not stay
+    out = torch.full(p.q.shape, float("nan"), dtype=dtype, device=cuda_device)
+    lse = torch.full(p.q.shape[:3], float("nan"), device=cuda_device)
+    got = p.attend(mask, out=out, lse=lse)
+    assert got[0] is out and got[1] is lse
+    p.check(out, lse, mask=mask)
+    # nothing at all
+    p = Problem(cuda_device, 3, 4, 4, 2, [0, 0, 0], 16, dtype, kind, drafted=[0, 0, 0])
+    p.check(*p.attend())
+
+
+@pytest.mark.parametrize("dtype,kind", [(F32, F32), (BF16, BF16), (F32, BF16)], ids=["f32", "bf16", "f32_bf16"])
+@pytest.mark.parametrize("bad", [float("nan"), float("inf"), -float("inf"), 3.3e38], ids=["nan", "inf", "-inf", "max"])
+@pytest.mark.parametrize("T,ctx", [(5, 20), (33, 200)])
+def test_hidden_values_do_not_reach_a_row(cuda_device, dtype, kind, bad, T, ctx):
+    """One drafted token's value (then its key) is bad: rows that do not see it are as if it
+    were good, the others show it in that column (or in all)."""
+    p = Problem(cuda_device, 2, 4, 2, T, [ctx, ctx + 3], 16, dtype, kind, seed=8)
+    mask = _tree(T, 2)
+    u = 3
+    sees = mask[:, u]
+    assert sees.any() and not sees.all()
+    good, good_lse = p.attend(mask)
+    where = [(int(p.table[b, (c + u) // 16]), (c + u) % 16) for b, c in enumerate(p.ctx)]
+    for pages, column in ((p.pool.v, 77), (p.pool.k, 5)):
+        kept = pages.clone()
+        for page, slot in where:
+            pages[page, :, slot, column] = bad
+        out, lse = p.attend(mask)
+        pages.copy_(kept)
+        hidden = torch.as_tensor(~sees)
+        assert torch.equal(out[:, :, hidden], good[:, :, hidden])
+        assert torch.equal(lse[:, :, hidden], good_lse[:, :, hidden])
+        if abs(bad) > 3e38 and bad == bad and not np.isinf(bad):
+            continue
+        if pages is p.pool.v:
+            seen = out[:, :, ~hidden].float()
+            assert not seen[..., column].isfinite().any()
+            assert torch.equal(out[:, :, ~hidden][..., :column], good[:, :, ~hidden][..., :column])
+            assert torch.equal(lse, good_lse)
+
+
+@pytest.mark.parametrize("dtype,kind", PAIRS[:3], ids=IDS[:3])
+def test_long_context_of_one_sequence_among_short_ones(cuda_device, dtype, kind):
+    """The work list is cut across sequences and heads: boundaries fall anywhere."""
+    ctx = [5, 9000, 1, 0, 640, 129, 4000]
+    p = Problem(cuda_device, 7, 8, 2, 2, ctx, 64, dtype, kind, seed=21)
+    p.check(*p.attend(), rows=range(7))
+
+
+@pytest.mark.parametrize("dtype,kind", PAIRS[:3], ids=IDS[:3])
+def test_many_sequences(cuda_device, dtype, kind):
+    rng = np.random.default_rng(4)
+    ctx = [int(c) for c in rng.integers(0, 200, 150)]
+    p = Problem(cuda_device, 150, 4, 4, 1, ctx, 16, dtype, kind, seed=22)
+    p.check(*p.attend())
+
+
+@pytest.mark.parametrize("dtype,kind", PAIRS[:3], ids=IDS[:3])
+def test_most_tokens(cuda_device, dtype, kind):
+    """T = 1024 of 16 heads to a key/value head, the most rows a call takes: checked by a chain's last rows."""
+    T = 1024
+    p = Problem(cuda_device, 1, 16, 1, T, [200], 128, dtype, kind, seed=23)
+    out, lse = p.attend()
+    k, v = p.k[0], p.v[0]
+    for t in (0, 1, 500, 1023):
+        o, l, spread = decode.tree_attention(p.q[0][:, t:t + 1], k, v, 200 + t, 1)
+        assert np.abs(lse[0, :, t].double().cpu().numpy() - l[:, 0]).max() <= 2e-4
+        d = np.abs(out[0, :, t].double().cpu().numpy() - o[:, 0])
+        assert np.all(d <= 2.0 ** -8 * (np.abs(o[:, 0]) + spread[:, 0]) + 4e-4 * spread[:, 0])
+
+
+@pytest.mark.parametrize("dtype,kind", PAIRS[:3], ids=IDS[:3])
+@pytest.mark.parametrize("gain", [30.0, 1e-3])
+def test_peaked_and_flat_scores(cuda_device, dtype, kind, gain):
+    """Large scores (standard deviation 30: the maximum moves from tile to tile) and nearly equal ones."""
+    p = Problem(cuda_device, 2, 4, 2, 3, [900, 333], 32, dtype, kind, seed=24, gain=gain)
+    out, lse = p.attend()
+    for b in range(2):
+        o, l, spread = decode.tree_attention(p.q[b], p.k[b], p.v[b], p.ctx[b], 3)
+        # The bars of the module's head, for rows of unit variance, scale with the keys: scores are gain times larger.
+        share = (1e-5 if dtype == F32 else 2e-4) * max(1.0, gain)
+        assert np.abs(lse[b].double().cpu().numpy() - l).max() <= share
+        step = 0.0 if dtype == F32 else 2.0 ** -8
+        tol = step * (np.abs(o) + spread) + (2 * share + 2e-5) * spread
+        assert np.all(np.abs(out[b].double().cpu().numpy() - o) <= tol)
+
+
+def test_strided_queries_and_pages(cuda_device):
+    p = Problem(cuda_device, 2, 8, 2, 3, [70, 11], 16, BF16, BF16, seed=25)
+    want, want_lse = p.attend()
+    q = p.q.transpose(1, 2).contiguous().to(cuda_device).transpose(1, 2)
+    got, lse = cache.attend(q, p.pool, p.table, p.ctx_dev)
+    assert torch.equal(got, want) and torch.equal(lse, want_lse) and got.is_contiguous()
+    both = torch.stack((p.pool.k, p.pool.v), 3).transpose(1, 2).contiguous()  # [n, page, Hkv, 2, 256]
+    pool = cache.PagedCache(both[:, :, :, 0].transpose(1, 2), both[:, :, :, 1].transpose(1, 2))
+    got, lse = cache.attend(q, pool, p.table, p.ctx_dev)
+    assert torch.equal(got, want) and torch.equal(lse, want_lse)
+
+
+def test_bad_pages_and_lengths(cuda_device):
+    """A bad page's keys are absent, a length past the table ends with the table; both are recorded."""
+    for dtype, kind in PAIRS[:3]:
+        p = Problem(cuda_device, 2, 4, 2, 1, [60, 60], 16, dtype, kind, seed=26)
+        p.table[0, 1] = p.pool.k.shape[0]
+        out, lse = p.attend()
+        assert cache.status(p.pool) == gqa._lib.GQA_ERR_DEVICE_BOUNDS
+        p.check(out, lse, rows=[1])
+        keep = [j for j in range(61) if not 16 <= j < 32]
+        p.k[0, :, :len(keep)], p.v[0, :, :len(keep)] = p.k[0][:, keep], p.v[0][:, keep]
+        p.ctx[0] = len(keep) - 1
+        p.check(out, lse, rows=[0])
+        p = Problem(cuda_device, 1, 4, 2, 1, [63], 16, dtype, kind, seed=27)
+        p.ctx_dev.fill_(1 << 30)
+        out, lse = p.attend()
+        assert cache.status(p.pool) == gqa._lib.GQA_ERR_DEVICE_BOUNDS
+        p.check(out, lse)  # the table's 64 tokens
+        p = Problem(cuda_device, 1, 4, 2, 1, [0], 16, dtype, kind, seed=28)
+        p.ctx_dev.fill_(-5)
+        out, lse = p.attend()
+        assert cache.status(p.pool) == gqa._lib.GQA_ERR_DEVICE_BOUNDS
+        p.check(out, lse)
+
+
+@pytest.mark.parametrize("dtype,kind", PAIRS[:3], ids=IDS[:3])
+def test_equal_calls_streams_and_graphs(cuda_device, dtype, kind):
+    """Equal calls give equal bits, alone, together on two streams and replayed."""
+    p = Problem(cuda_device, 3, 16, 4, 4, [2000, 10, 777], 32, dtype, kind, seed=29)
+    o = Problem(cuda_device, 2, 16, 4, 4, [500, 3000], 32, dtype, kind, seed=30)
+    mask = torch.as_tensor(_tree(4, 1)).to(cuda_device)
+    want, other = p.attend(mask), o.attend(mask)
+    torch.cuda.synchronize()
+    q, q2 = p.q.to(cuda_device), o.q.to(cuda_device)
+    s1, s2 = torch.cuda.Stream(), torch.cuda.Stream()
+    for s in (s1, s2):
+        s.wait_stream(torch.cuda.current_stream())
+    got = []
+    for _ in range(5):
+        got.append((cache.attend(q, p.pool, p.table, p.ctx_dev, tree_mask=mask, stream=s1),
+                    cache.attend(q2, o.pool, o.table, o.ctx_dev, tree_mask=mask, stream=s2)))
+    torch.cuda.synchronize()
+    for a, b in got:
+        assert torch.equal(a[0], want[0]) and torch.equal(a[1], want[1])
+        assert torch.equal(b[0], other[0]) and torch.equal(b[1], other[1])
+    ws = torch.empty(cache.workspace_bytes(3, 16, 4, p.pool, p.table.shape[1], dtype), dtype=torch.uint8,
+                     device=cuda_device)
+    out, lse = torch.empty_like(want[0]), torch.empty_like(want[1])
+    g, g2 = torch.cuda.CUDAGraph(), torch.cuda.CUDAGraph()
+    for graph in (g, g2):  # two captured steps that share a workspace, replayed in order
+        with torch.cuda.graph(graph):
+            cache.attend(q, p.pool, p.table, p.ctx_dev, tree_mask=mask, out=out, lse=lse, workspace=ws)
+    for ctx in ([2000, 10, 777], [1500, 0, 700], [3, 8, 1]):
+        p.ctx_dev.copy_(torch.tensor(ctx, dtype=torch.int32))
+        for graph in (g, g2):
+            out.fill_(float("nan"))
+            graph.replay()
+            eager = cache.attend(q, p.pool, p.table, p.ctx_dev, tree_mask=mask)
+            assert torch.equal(out, eager[0]) and torch.equal(lse, eager[1])
+
+
+def test_refusals(cuda_device):
+    p = Problem(cuda_device, 2, 16, 4, 3, [20, 30], 16, BF16, BF16)
+    q, dev = p.q.to(cuda_device), cuda_device
+    mask = torch.ones(3, 3, dtype=torch.bool, device=dev)
+    good = dict(q=q, pool=p.pool, page_table=p.table, context_lens=p.ctx_dev)
+    for kw in (dict(q=q.cpu()), dict(q=q.half()), dict(q=q[0]), dict(q=q[..., :128]), dict(page_table=p.table[:1]),
+               dict(page_table=p.table.long()), dict(context_lens=p.ctx_dev.long()), dict(context_lens=p.ctx_dev[:1]),
+               dict(tree_lens=p.ctx_dev.cpu()), dict(tree_mask=mask.float()), dict(tree_mask=mask[:2]),
+               dict(tree_mask=mask.cpu()), dict(tree_mask=mask.expand(2, 3, 3)),
+               dict(out=torch.empty_like(q, dtype=F32)), dict(lse=torch.empty(2, 16, 4, device=dev)),
+               dict(lse=torch.empty(2, 16, 3, device=dev, dtype=torch.float64)),
+               dict(workspace=torch.empty(1 << 20, dtype=torch.uint8))):
+        with pytest.raises(ValueError):
+            cache.attend(**{**good, **kw})
+    for kw in (dict(q=q[:, :15]), dict(q=q[:, :12]), dict(workspace=torch.empty(64, dtype=torch.uint8, device=dev)),
+               dict(q=torch.zeros(2, 16, 0, 256, dtype=BF16, device=dev)),
+               dict(q=torch.zeros(2, 16, 1025, 256, dtype=BF16, device=dev))):
+        with pytest.raises(gqa.GqaAttnError):
+            cache.attend(**{**good, **kw})
+
+
+@pytest.mark.parametrize("dtype,kind", [(F32, F32), (BF16, BF16), (BF16, E4M3)], ids=IDS[:3])
+def test_a_decoder_with_the_operators_together(cuda_device, dtype, kind):
+    """A prompt written with rotated keys, decoded token by token, then a drafted tree whose
+    accepted branch is kept: against the float64 attention of the rotated rows, and for
+    unquantised pages against the dense ``fwd`` over what ``read`` gives back."""
+    dev, Hq, Hkv, L, page = cuda_device, 16, 4, 150, 16
+    t = rotary.Table(128, layout="interleaved", scaling="linear", factor=2.0, device=dev)
+    g = torch.Generator().manual_seed(31)
+    pool = cache.PagedCache.empty(40, Hkv, page, kind, dev)
+    table = torch.randperm(40, generator=g)[:20].view(1, 20).to(torch.int32).to(dev)
+    n = torch.zeros(1, dtype=torch.int32, device=dev)
+
+    def token(T):
+        return [torch.randn((1, h, T, 256), generator=g).to(dtype).to(dev) for h in (Hq, Hkv, Hkv)]
+
+    def bar(out, lse, q, ctx, T, mask=None):
+        kd, vd = cache.read(pool, table, n * 0 + ctx + T, ctx + T, dtype=F32)
+        o, l, spread = decode.tree_attention(q[0], kd[0], vd[0], ctx, T, mask)
+        tol_o = 2e-5 if dtype == F32 else 2.0 ** -8 * (np.abs(o) + spread) + 4e-4 * spread
+        assert np.all(np.abs(out[0].double().cpu().numpy() - o) <= tol_o)
+        assert np.abs(lse[0].double().cpu().numpy() - l).max() <= (1e-5 if dtype == F32 else 2e-4)
+
+    q, k, v = token(L)
+    cache.write(pool, k, v, table, n, rope=t)
+    q, _ = rotary.rotate(q, None, t)
+    if kind != E4M3:  # the prompt's own attention, dense, over the cache read back
+        kd, vd = cache.read(pool, table, n + L, L, dtype=dtype)
+        assert torch.equal(vd, v)
+        full, full_lse = gqa.fwd(q, kd, vd)
+        out, lse = cache.attend(q[:, :, -1:], pool, table, n + L - 1)
+        tol = 4e-5 if dtype == F32 else 2e-2
+        assert (out - full[:, :, -1:]).abs().max() <= tol and (lse - full_lse[:, :, -1:]).abs().max() <= tol
+    n += L
+    for _ in range(5):
+        q, k, v = token(1)
+        cache.write(pool, k, v, table, n, rope=t)
+        q, _ = rotary.rotate(q, None, t, positions=n[:, None])
+        out, lse = cache.attend(q, pool, table, n)
+        bar(out, lse, q, int(n), 1)
+        n += 1
+    parent, depth = [-1, 0, 0, 1, 1, 2], [0, 1, 1, 2, 2, 2]
+    mask = np.eye(6, dtype=bool)
+    for i, p in enumerate(parent):
+        if p >= 0:
+            mask[i] |= mask[p]
+    q, k, v = token(6)
+    pos = n[:, None] + torch.tensor([depth], dtype=torch.int32, device=dev)
+    cache.write(pool, k, v, table, n, rope=t, positions=pos)
+    q, _ = rotary.rotate(q, None, t, positions=pos)
+    out, lse = cache.attend(q, pool, table, n, tree_mask=torch.as_tensor(mask).to(dev))
+    bar(out, lse, q, int(n), 6, mask)
+    # accept 0 -> 1 -> 4: its keys written behind the context; its last row sees what the tree's row 4 saw
+    path = [0, 1, 4]
+    cache.write(pool, k[:, :, path], v[:, :, path], table, n, rope=t)
+    out2, lse2 = cache.attend(q[:, :, path], pool, table, n)
+    bar(out2, lse2, q[:, :, path], int(n), 3)
+    tol = 4e-5 if dtype == F32 else 2e-2
+    assert (out2[:, :, 2] - out[:, :, 4]).abs().max() <= tol and (lse2[:, :, 2] - lse[:, :, 4]).abs().max() <= 4e-4
+    assert cache.status(pool) == 0
