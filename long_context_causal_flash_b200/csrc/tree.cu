@@ -1,6 +1,5 @@
 // Attention of drafted tokens over the paged cache on the FP32 pipe, and the merge of
-// partial results, sm_100a.  All pairs of query and page types run here in fp32; bf16
-// queries over bf16 and e4m3 pages use it where tree_shape says so.
+// partial results, sm_100a: fp32 queries over any pages, and bf16 queries over fp32 ones.
 //
 // A CTA holds R query rows (R / G tokens of the G heads of one key/value head) and
 // streams its worker's tiles; 8 warps take 16 of a tile's 128 keys each, four keys at a
@@ -19,6 +18,7 @@ constexpr int kWarps = 8;
 constexpr int kThreads = 32 * kWarps;
 constexpr int kKeys = 4;  // keys a warp takes at a time (a divisor of every page size)
 constexpr int kKeysPerWarp = kTreeTile / kWarps;
+constexpr int kB200Sms = 148;
 
 // Eight columns of a cache row; e4m3 codes still want their row's scale.
 template <int kCache>
@@ -273,22 +273,26 @@ int launch_one(const TreeParams& p, cudaStream_t stream) {
   return cudaGetLastError() == cudaSuccess ? GQA_OK : GQA_ERR_LAUNCH;
 }
 
-template <int R, typename QT>
-int launch_cache(const TreeParams& p, cudaStream_t stream) {
-  if (p.c.dtype == GQA_F32) return launch_one<R, GQA_F32, QT>(p, stream);
-  if (p.c.dtype == GQA_BF16) return launch_one<R, GQA_BF16, QT>(p, stream);
-  return launch_one<R, GQA_E4M3, QT>(p, stream);
+template <int R>
+int launch_types(const TreeParams& p, bool q_bf16, cudaStream_t stream) {
+  if (q_bf16) return launch_one<R, GQA_F32, __nv_bfloat16>(p, stream);
+  if (p.c.dtype == GQA_F32) return launch_one<R, GQA_F32, float>(p, stream);
+  if (p.c.dtype == GQA_BF16) return launch_one<R, GQA_BF16, float>(p, stream);
+  return launch_one<R, GQA_E4M3, float>(p, stream);
 }
 
 }  // namespace
 
 TreeShape tree_shape(int B, int Hkv, int G, int64_t T, int64_t max_pages, int page_size, bool q_bf16, int cache_dtype) {
-  (void)q_bf16, (void)cache_dtype;
   TreeShape s;
-  s.tensor = false;
-  s.rows = T * G <= 4 ? 4 : 8;
-  s.row_tiles = int((T * G + s.rows - 1) / s.rows);
-  const int slots = 148 * (s.rows == 4 ? 2 : 1);
+  const int64_t rows = T * G;
+  s.tensor = q_bf16 && cache_dtype != GQA_F32;
+  if (s.tensor)
+    s.rows = rows <= 16 ? 16 : rows <= 32 ? 32 : rows <= 64 ? 64 : 128;
+  else
+    s.rows = rows <= 4 ? 4 : 8;
+  s.row_tiles = int((rows + s.rows - 1) / s.rows);
+  const int slots = kB200Sms * (s.rows == 4 ? 2 : 1);
   s.workers = slots / s.row_tiles > 1 ? slots / s.row_tiles : 1;
   // No more workers than tiles that the page tables could hold.
   const int64_t tiles = (max_pages * page_size + kTreeTile - 1) / kTreeTile * B * Hkv;
@@ -296,10 +300,8 @@ TreeShape tree_shape(int B, int Hkv, int G, int64_t T, int64_t max_pages, int pa
   return s;
 }
 
-int launch_tree_ffma(TreeParams p, bool q_bf16, cudaStream_t stream) {
-  const bool small = int64_t(p.T) * p.G <= 4;
-  if (q_bf16) return small ? launch_cache<4, __nv_bfloat16>(p, stream) : launch_cache<8, __nv_bfloat16>(p, stream);
-  return small ? launch_cache<4, float>(p, stream) : launch_cache<8, float>(p, stream);
+int launch_tree_ffma(const TreeParams& p, bool q_bf16, int rows, cudaStream_t stream) {
+  return rows == 4 ? launch_types<4>(p, q_bf16, stream) : launch_types<8>(p, q_bf16, stream);
 }
 
 int launch_tree_merge(const TreeParams& p, int rows_per_tile, cudaStream_t stream) {
