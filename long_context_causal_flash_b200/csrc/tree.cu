@@ -70,14 +70,14 @@ __global__ void __launch_bounds__(kThreads, R == 4 ? 2 : 1) tree_ffma_kernel(con
               q[r]);
     }
     float m = -INFINITY, l = 0.f;  // of my_row; l: the share of this lane's keys
-    for (int64_t tile = g.t0; tile < g.t1; ++tile) {
+    for (int tile = g.t0; tile < g.t1; ++tile) {
       for (int k0 = 0; k0 < kKeysPerWarp; k0 += kKeys) {
-        const int64_t j0 = tile * kTreeTile + warp * kKeysPerWarp + k0;
+        const uint32_t j0 = uint32_t(tile) * kTreeTile + warp * kKeysPerWarp + k0;
         if (j0 >= g.s.keys) break;
         const int page = page_of(p.c, table, p.max_pages, j0);
         if (page < 0) continue;  // recorded; its keys are absent
-        const int slot = int(j0 & ((int64_t(1) << p.c.page_shift) - 1));
-        const int live = int(min(int64_t(kKeys), g.s.keys - j0));
+        const int slot = int(j0 & ((1u << p.c.page_shift) - 1));
+        const int live = int(min(uint32_t(kKeys), g.s.keys - j0));
         const int64_t at = page * p.c.sp + g.h * p.c.sh + slot * p.c.st + 8 * lane;
         float k[kKeys][8], v[kKeys][8];
 #pragma unroll
@@ -117,7 +117,7 @@ __global__ void __launch_bounds__(kThreads, R == 4 ? 2 : 1) tree_ffma_kernel(con
         if (kScores == 16) s[0] += __shfl_xor_sync(0xffffffffu, s[0], 1);
         // Visible: any key of the context; a drafted one by the mask.  Rows past the tile's
         // last (t >= T) are nobody's and see all, so that they ask for no masked path.
-        const int64_t j = j0 + my_key;
+        const uint32_t j = j0 + my_key;
         bool vis = my_key < live && (t_mine < g.s.drafted || t_mine >= p.T);
         if (vis && j >= g.s.ctx && t_mine < p.T) vis = tree_sees(p, g.b, t_mine, int(j - g.s.ctx));
         const float x = vis ? s[0] * k_scale * p.scale_log2 : -INFINITY;
@@ -241,16 +241,28 @@ __global__ void __launch_bounds__(256) tree_merge_kernel(const __grid_constant__
     auto at = [&](int64_t w) {
       return ((w * 2 + (w == w0 ? 1 : 0)) * p.row_tiles + rt) * rows_per_tile + r;
     };
-    for (int64_t w = w0; w <= w1; ++w) mx = fmaxf(mx, p.lse_part[at(w)]);
-    const float ref = mx == -INFINITY ? 0.f : mx;
-    for (int64_t w = w0; w <= w1; ++w) {
-      const float a = expf(p.lse_part[at(w)] - ref);
-      if (a == 0.f) continue;
-      sum += a;
-      float y[8];
-      load8(p.o_part + at(w) * kHeadDim + 8 * lane, y);
+    // Lane i takes the log-sum-exp of partial result i of each 32: their weights first, then
+    // the outputs, eight loads in flight.
+    for (int64_t w = w0 + lane; w <= w1; w += 32) mx = fmaxf(mx, p.lse_part[at(w)]);
 #pragma unroll
-      for (int c = 0; c < 8; ++c) acc[c] = fmaf(a, y[c], acc[c]);
+    for (int s = 16; s >= 1; s >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, s));
+    const float ref = mx == -INFINITY ? 0.f : mx;
+    for (int64_t wb = w0; wb <= w1; wb += 32) {
+      const float mine = wb + lane <= w1 ? expf(p.lse_part[at(wb + lane)] - ref) : 0.f;
+      const int n = int(min(int64_t(32), w1 - wb + 1));
+      for (int i = 0; i < n; i += 4) {
+        float y[4][8];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) load8(p.o_part + at(min(wb + i + k, w1)) * kHeadDim + 8 * lane, y[k]);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const float a = __shfl_sync(0xffffffffu, mine, (i + k) & 31);
+          if (i + k >= n || a == 0.f) continue;  // a partial result without a visible key is not used
+          sum += a;
+#pragma unroll
+          for (int c = 0; c < 8; ++c) acc[c] = fmaf(a, y[k][c], acc[c]);
+        }
+      }
     }
   }
   const float inv = sum == 0.f ? 0.f : 1.f / sum;

@@ -40,27 +40,26 @@ struct TreeParams {
 
 // Context, drafted tokens and tiles of sequence b; what lies past the page table is left out.
 struct TreeSeq {
-  int64_t ctx, keys;
-  int drafted;
-  int64_t tiles;
+  uint32_t ctx, keys;  // below 2^31 + 2^10
+  int drafted, tiles;
 };
 
 __device__ __forceinline__ TreeSeq tree_seq(const TreeParams& p, int b) {
   TreeSeq s;
   const int64_t cap = p.max_pages << p.c.page_shift;
-  s.ctx = p.ctx[b];
+  const int ctx = p.ctx[b];
   s.drafted = p.tree_lens ? min(max(p.tree_lens[b], 0), p.T) : p.T;
-  if (s.ctx < 0 || s.ctx + s.drafted > cap) set_status(p.c.status, GQA_ERR_DEVICE_BOUNDS);
-  s.ctx = max(s.ctx, int64_t(0));
-  s.keys = min(s.ctx + s.drafted, cap);
-  s.tiles = s.drafted > 0 ? (s.keys + kTreeTile - 1) / kTreeTile : 0;
+  s.ctx = uint32_t(max(ctx, 0));
+  if (ctx < 0 || int64_t(s.ctx) + s.drafted > cap) set_status(p.c.status, GQA_ERR_DEVICE_BOUNDS);
+  s.keys = uint32_t(min(int64_t(s.ctx) + s.drafted, cap));
+  s.tiles = s.drafted > 0 ? int((s.keys + kTreeTile - 1) / kTreeTile) : 0;
   return s;
 }
 
 // Where a worker starts and how many items it has.
 struct TreeCursor {
-  int b, h;
-  int64_t tile, left;
+  int b, h, tile;
+  int64_t left;
 };
 
 // One warp: sum of the sequences' tiles, and of those before sequence b_end.
@@ -89,7 +88,15 @@ __device__ __forceinline__ int64_t tree_workers(const TreeParams& p, int64_t W) 
 // One warp: the cursor of worker w (left = 0 if it has no work).
 __device__ __forceinline__ TreeCursor tree_start(const TreeParams& p, int w) {
   const int lane = threadIdx.x & 31;
-  const int64_t W = tree_total(p, 0, nullptr) * p.c.Hkv;
+  const int first = lane < p.B ? tree_seq(p, lane).tiles : 0;  // all there is of up to 32 sequences
+  int64_t all = first;
+  if (p.B > 32) {
+    all = tree_total(p, 0, nullptr);
+  } else {
+#pragma unroll
+    for (int s = 16; s >= 1; s >>= 1) all += __shfl_xor_sync(0xffffffffu, all, s);
+  }
+  const int64_t W = all * p.c.Hkv;
   const int64_t n = tree_workers(p, W);
   TreeCursor c{0, 0, 0, 0};
   if (w >= n) return c;
@@ -97,7 +104,7 @@ __device__ __forceinline__ TreeCursor tree_start(const TreeParams& p, int w) {
   c.left = (w + 1) * W / n - at;
   for (int b0 = 0; b0 < p.B; b0 += 32) {
     const int b = b0 + lane;
-    const int64_t mine = b < p.B ? tree_seq(p, b).tiles * p.c.Hkv : 0;
+    const int64_t mine = int64_t(b0 == 0 ? first : b < p.B ? tree_seq(p, b).tiles : 0) * p.c.Hkv;
     int64_t upto = mine;  // inclusive scan
 #pragma unroll
     for (int s = 1; s < 32; s <<= 1) {
@@ -111,7 +118,7 @@ __device__ __forceinline__ TreeCursor tree_start(const TreeParams& p, int w) {
       const int64_t tiles = __shfl_sync(0xffffffffu, mine, src) / p.c.Hkv;
       c.b = b0 + src;
       c.h = int(in / tiles);
-      c.tile = in - c.h * tiles;
+      c.tile = int(in - c.h * tiles);
       return c;
     }
     at -= __shfl_sync(0xffffffffu, upto, 31);
@@ -123,8 +130,7 @@ __device__ __forceinline__ TreeCursor tree_start(const TreeParams& p, int w) {
 // A segment: tiles [t0, t1) of (b, h).
 struct TreeSegment {
   TreeSeq s;
-  int b, h;
-  int64_t t0, t1;
+  int b, h, t0, t1;
   __device__ __forceinline__ bool whole() const { return t0 == 0 && t1 == s.tiles; }
   __device__ __forceinline__ int slot() const { return t0 > 0 ? 0 : 1; }
 };
@@ -137,7 +143,7 @@ __device__ __forceinline__ bool tree_next(const TreeParams& p, TreeCursor& c, Tr
   g->b = c.b;
   g->h = c.h;
   g->t0 = c.tile;
-  g->t1 = min(g->s.tiles, c.tile + c.left);
+  g->t1 = int(min(int64_t(g->s.tiles), c.tile + c.left));
   c.left -= g->t1 - g->t0;
   c.tile = 0;
   if (++c.h == p.c.Hkv) {

@@ -8,23 +8,23 @@
 // two halves of O^T (lane = column of the output), 4 N columns in all.
 //
 // e4m3 pages are multiplied as they are (kind::f8f6f4, exact products in fp32): the query
-// is scaled by a power of two so that its largest element lies in [224, 448) and taken
+// is scaled by a power of two so that its largest element lies in (224, 448] and taken
 // apart into two e4m3 pieces, q = hi + lo, off by at most 2^-10 of that scale; so is each
-// probability.  Both pieces are multiplied into the same accumulator, which costs a second
-// instruction at twice the rate.  The scales of a key go into its scores, those of a value
-// into its probability, before that is rounded.
+// probability.  Up to 64 rows the pieces lie side by side in N and their products are added
+// afterwards; above, two instructions add them into one accumulator.  The scales of a key
+// go into its scores, those of a value into its probability, before that is rounded.
 //
 // Softmax: one thread per key and up to 32 rows; the running maximum m of a row is raised
 // only when a score passes it by kSlack (in powers of two), so most tiles need no
 // reduction over the keys and no rescaling of O.  P = 2^(x - m) goes to shared memory as
 // the B operand; the row sum stays with the threads, in fp32, until the end.  For e4m3, x
 // includes log2 of the value's scale, so that m follows the largest product p v rather
-// than the largest p, and P is stored as 64 P <= 256: a probability then keeps 8 bits down
-// to 2^-10 of the largest, and is off by 2^-15 of it below.
+// than the largest p, and P is stored as 16 P <= 256: a probability then keeps 8 bits down
+// to 2^-8 of the first maximum, and is off by at most 2^-14 of it below.
 //
 // Warps: 4 softmax warps per 32 (or 16) rows, one producer warp per 32 KiB slot of the
 // ring (cp.async, 16 bytes at a time, through the page table; two rows to an
-// instruction), and one warp whose first lane issues the MMAs.
+// instruction), and two warps whose first lanes issue the products.
 #include "internal.h"
 #include "tcgen05.cuh"
 #include "tree.cuh"
@@ -41,12 +41,15 @@ struct Cfg {
   static constexpr int kCols = kN < 32 ? kN : 32;  // rows of a softmax thread
   static constexpr int kParts = kN / kCols;
   static constexpr int kSoftWarps = 4 * kParts;
-  static constexpr int kPieces = kFp8 ? 2 : 1;
-  static constexpr int kItems = kFp8 ? 2 : 4;  // slots of a tile
-  static constexpr int kQBytes = kN * 512;     // bf16, or two e4m3 pieces
-  static constexpr int kPBytes = kFp8 || kN > 64 ? 2 * kChunk : kChunk;
-  static constexpr int kSlots = kN > 64 ? 4 : kFp8 || kN > 32 ? 5 : 6;  // what shared memory has room for
-  static constexpr int kWarps = kSoftWarps + kSlots + 1;
+  static constexpr bool kWide = kFp8 && kN <= 64;           // both pieces side by side in one product's N
+  static constexpr int kNN = kWide ? 2 * kN : kN;           // N of a product
+  static constexpr int kPieces = kFp8 && !kWide ? 2 : 1;    // products per step
+  static constexpr int kItems = kFp8 ? 2 : 4;               // slots of a tile
+  static constexpr int kQBytes = kN * 512;                  // bf16, or two e4m3 pieces
+  static constexpr int kPBytes = kN > 64 ? 2 * kChunk : kChunk;
+  static constexpr int kSlots = kN > 64 ? 4 : kN > 32 ? 5 : 6;  // what shared memory has room for
+  static constexpr int kIssuer = kSoftWarps + kSlots;           // the S issuer's warp; the O issuer's is the next
+  static constexpr int kWarps = kIssuer + 2;
   static constexpr int kThreads = 32 * kWarps;
   static constexpr int kOffQ = 0;
   static constexpr int kOffP = kOffQ + kQBytes;
@@ -56,10 +59,11 @@ struct Cfg {
   static constexpr int kOffF = kOffM + kN * 4;    // [kN] factor of a row's scores (e4m3 pages)
   static constexpr int kOffBad = kOffF + kN * 4;  // 32 words: drafted tokens with a value that is not finite
   static constexpr int kSmem = kOffBad + 128;
-  static constexpr float kSlack = kFp8 ? 2.f : 8.f;
-  static constexpr uint32_t kTmem = 4 * kN;
-  static_assert(kSmem <= 232448 - 64, "shared memory per block");
+  static constexpr float kSlack = kFp8 ? 4.f : 8.f;
+  static constexpr uint32_t kTmem = 4 * kNN;
+  static_assert(kSmem <= 232448 - 1024, "shared memory per block");
 };
+constexpr float kPScale = 16.f;  // e4m3 probabilities are stored times this: 2^4 above the maximum is 256
 
 // Barriers: S^T, its release, P and O per parity of the tile; the ring's slots.
 enum { kBarQ = 0, kBarS = 1, kBarSFree = 3, kBarP = 5, kBarPV = 7, kBarDrain = 9, kBarFull = 10, kBarEmpty = 16 };
@@ -130,35 +134,80 @@ __host__ __device__ constexpr uint32_t idesc(int N, int a_mn, int b_mn) {
          (uint32_t(N >> 3) << 17) | (8u << 24);
 }
 
-template <int C>
-__device__ __forceinline__ void tmem_ld(uint32_t addr, float (&v)[C]) {
-  if constexpr (C == 32)
-    umma::tmem_ld32(addr, v);
-  else
-    umma::tmem_ld16(addr, v);
-}
-
-// Sum or maximum over the 32 lanes of each of C values: lane l ends with value l (C = 32)
-// or l / 2 (C = 16).  A lane sends the half that it does not keep.
-template <int C, bool kMax>
-__device__ __forceinline__ float lanes_reduce(float (&v)[C]) {
+// Sum or maximum over the 32 lanes of each of 16 values: lane l ends with value l / 2.  A
+// lane sends the half that it does not keep.
+template <bool kMax>
+__device__ __forceinline__ float lanes_reduce(float (&v)[16]) {
   const int lane = threadIdx.x & 31;
 #pragma unroll
-  for (int half = C / 2, off = 16; half >= 1; half >>= 1, off >>= 1) {
+  for (int half = 8, off = 16; half >= 1; half >>= 1, off >>= 1) {
     const bool up = (lane & off) != 0;
 #pragma unroll
-    for (int i = 0; i < C / 2; ++i)
+    for (int i = 0; i < 8; ++i)
       if (i < half) {
         const float keep = up ? v[i + half] : v[i], send = up ? v[i] : v[i + half];
         const float got = __shfl_xor_sync(0xffffffffu, send, off);
         v[i] = kMax ? fmaxf(keep, got) : keep + got;
       }
   }
-  if (C == 16) {
-    const float got = __shfl_xor_sync(0xffffffffu, v[0], 1);
-    v[0] = kMax ? fmaxf(v[0], got) : v[0] + got;
+  const float got = __shfl_xor_sync(0xffffffffu, v[0], 1);
+  return kMax ? fmaxf(v[0], got) : v[0] + got;
+}
+
+// What the cleared elements of column d (drafted values that are not finite) add to a row of
+// token t: an infinity or NaN for each that the row sees.
+template <bool kFp8>
+__device__ __noinline__ float hidden_values(const TreeParams& p, const TreeSegment& g, const int32_t* table,
+                                            const uint32_t* bad, int t, int d) {
+  float sum = 0.f;
+  for (int u = 0; u < g.s.drafted; ++u) {
+    if (!((bad[u >> 5] >> (u & 31)) & 1u) || !tree_sees(p, g.b, t, u)) continue;
+    const uint32_t j = g.s.ctx + u, slot = j & ((1u << p.c.page_shift) - 1);
+    const int64_t at = table[j >> p.c.page_shift] * p.c.sp + g.h * p.c.sh + slot * p.c.st + d;
+    if constexpr (kFp8) {
+      if ((uint8_t(p.c.v[at]) & 0x7f) == 0x7f) sum = __uint_as_float(0x7fc00000u);
+    } else {
+      const float y = __bfloat162float(reinterpret_cast<const __nv_bfloat16*>(p.c.v)[at]);
+      if (!(fabsf(y) < INFINITY)) sum += y;
+    }
   }
-  return v[0];
+  return sum;
+}
+
+// One warp: row r of an e4m3 Q operand, both pieces of the row's eight columns per lane.
+// Returns the row's scale, NaN for a row with an infinity or a NaN: it has no finite score.
+template <int kN, bool kWide>
+__device__ __forceinline__ float put_query(uint4 u, uint32_t sQ, int r) {
+  const int lane = threadIdx.x & 31;
+  float x[8], lo[8];
+  unpack8(u, x);
+  float amax = 0.f;
+  bool finite = true;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    amax = fmaxf(amax, fabsf(x[i]));
+    finite = finite && fabsf(x[i]) < INFINITY;
+  }
+#pragma unroll
+  for (int o = 16; o >= 1; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+  finite = __all_sync(0xffffffffu, finite);
+  const float scale = e4m3_row_scale(finite ? amax : 0.f);
+  const float inv = __uint_as_float((254u << 23) - __float_as_uint(scale));
+#pragma unroll
+  for (int i = 0; i < 8; ++i) x[i] *= inv;
+  const uint32_t h0 = e4m3_encode4(x), h1 = e4m3_encode4(x + 4);
+  e4m3_decode4(h0, lo);
+  e4m3_decode4(h1, lo + 4);
+#pragma unroll
+  for (int i = 0; i < 8; ++i) lo[i] = x[i] - lo[i];
+  constexpr uint32_t kBlock = (kWide ? 2 * kN : kN) * 128u;
+  const uint32_t a = sQ + uint32_t(lane >> 4) * kBlock + uint32_t(r) * 128u +
+                     uint32_t((((lane & 15) >> 1) ^ (r & 7)) << 4) + uint32_t(lane & 1) * 8u;
+  constexpr uint32_t kLo = kWide ? kN * 128u : kN * 256u;  // kN is a multiple of 8: the same swizzle
+  asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(a), "r"(h0), "r"(h1) : "memory");
+  asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(a + kLo), "r"(e4m3_encode4(lo)), "r"(e4m3_encode4(lo + 4))
+               : "memory");
+  return finite ? scale : __uint_as_float(0x7fc00000u);
 }
 
 template <int kN, bool kFp8>
@@ -191,7 +240,7 @@ __global__ void __launch_bounds__(Cfg<kN, kFp8>::kThreads, 1) tree_tc_kernel(con
         mbar_init(bar(kBarP + i), F::kSoftWarps);
         mbar_init(bar(kBarPV + i), 1);
       }
-      mbar_init(bar(kBarDrain), 1);
+      mbar_init(bar(kBarDrain), 2);
       for (int i = 0; i < F::kSlots; ++i) {
         mbar_init(bar(kBarFull + i), 1);
         mbar_init(bar(kBarEmpty + i), 1);
@@ -200,7 +249,7 @@ __global__ void __launch_bounds__(Cfg<kN, kFp8>::kThreads, 1) tree_tc_kernel(con
       if (misaligned) set_status(status, GQA_ERR_LAUNCH);
     }
   }
-  if (warp == F::kWarps - 1) umma::tmem_alloc(smem_u32(&tmem_slot), F::kTmem);
+  if (warp == F::kIssuer) umma::tmem_alloc(smem_u32(&tmem_slot), F::kTmem);
   umma::fence_before_sync();
   __syncthreads();
   umma::fence_after_sync();
@@ -210,7 +259,7 @@ __global__ void __launch_bounds__(Cfg<kN, kFp8>::kThreads, 1) tree_tc_kernel(con
 
   if (misaligned) {
     // no role
-  } else if (warp >= F::kSoftWarps && warp < F::kWarps - 1) {
+  } else if (warp >= F::kSoftWarps && warp < F::kIssuer) {
     // ---------------------------------------------------------------- producers
     // This warp fills slot `s`: items s, s + kSlots, ... of the tiles' list.  A bf16 tile is
     // four items (key columns 0 - 127, 128 - 255, the same of the values), an e4m3 tile two.
@@ -219,10 +268,15 @@ __global__ void __launch_bounds__(Cfg<kN, kFp8>::kThreads, 1) tree_tc_kernel(con
     const int s = warp - F::kSoftWarps;
     const uint32_t slot = sRing + uint32_t(s) * kSlotBytes;
     const int unit = lane & 15, odd = lane >> 4;
-    const uint32_t dst0 = slot + uint32_t(unit >> 3) * kChunk;
     constexpr int kEs = kFp8 ? 1 : 2;
-    const int64_t slot_mask = (int64_t(1) << p.c.page_shift) - 1;
-    int64_t idx = s;
+    const uint32_t slot_mask = (1u << p.c.page_shift) - 1;
+    const int64_t row_bytes = p.c.st * kEs;
+    uint32_t dst[4];  // this lane's units of rows 0 / 1, 2 / 3, 4 / 5 and 6 / 7 of a group
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      dst[i] = slot + uint32_t(unit >> 3) * kChunk + uint32_t(2 * i + odd) * 128u +
+               uint32_t(((unit & 7) ^ (2 * i + odd)) << 4);
+    int idx = s;
     bool live = tree_next(p, cur, &g);
     // The page of each group of eight keys of this item, in lanes 0 .. 15.
     auto pages = [&]() {
@@ -231,29 +285,31 @@ __global__ void __launch_bounds__(Cfg<kN, kFp8>::kThreads, 1) tree_tc_kernel(con
         live = tree_next(p, cur, &g);
       }
       if (!live) return -1;
-      const int64_t j = (g.t0 + idx / F::kItems) * kTreeTile + lane * 8;
+      const uint32_t j = uint32_t(g.t0 + idx / F::kItems) * kTreeTile + lane * 8;
       return lane < 16 && j < g.s.keys ? page_of(p.c, p.table + int64_t(g.b) * p.max_pages, p.max_pages, j) : -1;
     };
     int pg = pages();
     for (uint32_t n = 0; live; ++n) {
       if (!warp_wait(bar(kBarEmpty + s), (n & 1u) ^ 1u, budget, status)) break;
-      const int item = int(idx % F::kItems);
-      const int64_t j0 = (g.t0 + idx / F::kItems) * kTreeTile;
+      const int item = idx % F::kItems;
+      const uint32_t j0 = uint32_t(g.t0 + idx / F::kItems) * kTreeTile;
       const char* pool = (item >= F::kItems / 2 ? p.c.v : p.c.k) + int64_t(g.h) * p.c.sh * kEs;
-      const int column = kFp8 ? 0 : (item & 1) * 256;
-      const int64_t row_bytes = p.c.st * kEs;
-#pragma unroll 4
+      const char* lane_src = pool + (kFp8 ? 0 : (item & 1) * 256) + unit * 16 + odd * row_bytes;
+      const int left = int(min(uint32_t(kTreeTile), g.s.keys - j0));
+#pragma unroll 2
       for (int grp = 0; grp < 16; ++grp) {
         const int page = __shfl_sync(0xffffffffu, pg, grp);
-        const int64_t in_page = (j0 + grp * 8) & slot_mask;
-        const char* src = pool + (int64_t(page) * p.c.sp + in_page * p.c.st) * kEs + column + unit * 16 + odd * row_bytes;
-        const int rows = page < 0 ? 0 : int(min(int64_t(8), g.s.keys - (j0 + grp * 8)));
+        const char* src = lane_src + (int64_t(page) * p.c.sp + ((j0 + grp * 8) & slot_mask) * p.c.st) * kEs;
+        if (page >= 0 && left >= grp * 8 + 8) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int r = 2 * i + odd;
-          const bool there = r < rows;
-          cp_async16(dst0 + uint32_t(grp * 8 + r) * 128u + uint32_t(((unit & 7) ^ r) << 4),
-                     there ? src + 2 * i * row_bytes : pool, there ? 16u : 0u);
+          for (int i = 0; i < 4; ++i) cp_async16(dst[i] + uint32_t(grp) * 1024u, src + 2 * i * row_bytes, 16u);
+        } else {
+          const int rows = page < 0 ? 0 : left - grp * 8;
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const bool there = 2 * i + odd < rows;
+            cp_async16(dst[i] + uint32_t(grp) * 1024u, there ? src + 2 * i * row_bytes : pool, there ? 16u : 0u);
+          }
         }
       }
       idx += F::kSlots;
@@ -264,89 +320,70 @@ __global__ void __launch_bounds__(Cfg<kN, kFp8>::kThreads, 1) tree_tc_kernel(con
       if (lane == 0) mbar_arrive(bar(kBarFull + s));
     }
     asm volatile("cp.async.wait_all;" ::: "memory");
-  } else if (warp == F::kWarps - 1) {
-    // ---------------------------------------------------------------- MMA issuer
-    // S(t + 1) is issued ahead of O += P(t) V(t), so that the softmax of a tile runs beside
-    // the products of its neighbours.
+  } else if (warp >= F::kIssuer) {
+    // ---------------------------------------------------------------- MMA issuers
+    // One thread issues every S^T = K Q^T, another every O^T += V^T P^T, so that neither
+    // waits for the other's tiles to arrive.
     if (lane == 0) {
-      constexpr uint32_t id_s = idesc<kFp8>(kN, 0, 0), id_o = idesc<kFp8>(kN, 1, 1);
+      const bool is_s = warp == F::kIssuer;
+      constexpr uint32_t id_s = idesc<kFp8>(F::kNN, 0, 0), id_o = idesc<kFp8>(F::kNN, 1, 1);
       constexpr int kRowSteps = kFp8 ? 4 : 8;  // K steps of O: 32 or 16 keys each
-      uint32_t item = 0;   // next item of the ring
-      uint32_t ts = 0, tp = 0;  // tiles whose S / whose O has been issued
+      const uint64_t dq = umma::smem_desc(sQ, 16, 1024), dp = umma::smem_desc(sP, kChunk, 1024);
+      uint32_t tt = 0, segs = 0;  // tiles issued
       bool ok = true;
-      uint32_t segs = 0;
-      auto full = [&](uint32_t it) {
-        return mbar_wait_inline(bar(kBarFull + int(it % F::kSlots)), (it / F::kSlots) & 1u, budget, status);
-      };
-      auto release = [&](uint32_t it) { umma::commit(bar(kBarEmpty + int(it % F::kSlots))); };
-      auto slot_of = [&](uint32_t it) { return sRing + (it % F::kSlots) * uint32_t(kSlotBytes); };
-      auto issue_s = [&]() {
-        const uint32_t b = ts & 1u;
-        if (ts >= 2 && !mbar_wait_inline(bar(kBarSFree + int(b)), ((ts - 2) >> 1) & 1u, budget, status)) return false;
-        const uint32_t d = tmem + b * kN;
-        const uint64_t dq = umma::smem_desc(sQ, 16, 1024);
-        for (int half = 0; half < F::kItems / 2; ++half) {
-          if (!full(item + half)) return false;
-          umma::fence_after_sync();
-          const uint64_t dk = umma::smem_desc(slot_of(item + half), 16, 1024);
-#pragma unroll
-          for (int k = 0; k < 8; ++k) {
-            // column block (kFp8: 128 columns, else 64) and 32-byte step inside it
-            const uint32_t a = uint32_t(k >> 2) * kChunk + uint32_t(k & 3) * 32u;
-            const uint32_t q = uint32_t((kFp8 ? 0 : 2 * half) + (k >> 2)) * (kN * 128u) + uint32_t(k & 3) * 32u;
-#pragma unroll
-            for (int piece = 0; piece < F::kPieces; ++piece)
-              mma<kFp8>(d, umma::desc_add(dk, a), umma::desc_add(dq, q + uint32_t(piece) * (kN * 256u)), id_s,
-                        (half | k | piece) != 0);
-          }
-          release(item + half);
-        }
-        umma::commit(bar(kBarS + int(b)));
-        item += F::kItems / 2;
-        ++ts;
-        return true;
-      };
-      auto issue_o = [&](uint32_t it, bool first) {
-        const uint32_t b = tp & 1u;
-        if (!mbar_wait_inline(bar(kBarP + int(b)), (tp >> 1) & 1u, budget, status)) return false;
-        const uint64_t dp = umma::smem_desc(sP, kChunk, 1024);
-        for (int half = 0; half < 2; ++half) {
-          const uint32_t vit = kFp8 ? it : it + half;
-          if ((!kFp8 || half == 0) && !full(vit)) return false;
-          umma::fence_after_sync();
-          const uint64_t dv = umma::smem_desc(slot_of(vit) + (kFp8 ? uint32_t(half) * kChunk : 0u), kChunk, 1024);
-          const uint32_t d = tmem + (2 + half) * kN;
-#pragma unroll
-          for (int k = 0; k < kRowSteps; ++k) {
-            const uint32_t rows = uint32_t(k) * (kFp8 ? 4096u : 2048u);
-#pragma unroll
-            for (int piece = 0; piece < F::kPieces; ++piece)
-              mma<kFp8>(d, umma::desc_add(dv, rows), umma::desc_add(dp, rows + uint32_t(piece) * kChunk), id_o,
-                        !first || (k | piece) != 0);
-          }
-          if (!kFp8 || half == 1) release(vit);
-        }
-        umma::commit(bar(kBarPV + int(b)));
-        ++tp;
-        return true;
-      };
       while (ok && tree_next(p, cur, &g)) {
-        if (!(ok = mbar_wait_inline(bar(kBarQ), segs & 1u, budget, status))) break;
+        if (is_s && !(ok = mbar_wait_inline(bar(kBarQ), segs & 1u, budget, status))) break;
         ++segs;
-        const int64_t n = g.t1 - g.t0;
-        // Items run K(0) V(0) K(1) V(1) ...: V(t) lies kItems / 2 behind K(t).
-        ok = issue_s();
-        for (int64_t t = 0; ok && t < n; ++t) {
-          const uint32_t v = item;
-          item += F::kItems / 2;
-          if (t + 1 < n) ok = issue_s();
-          ok = ok && issue_o(v, t == 0);
+        for (int tile = g.t0; ok && tile < g.t1; ++tile, ++tt) {
+          const uint32_t b = tt & 1u, ph = (tt >> 1) & 1u;
+          // The softmax has read S(t - 2), or written P(t).
+          if (is_s)
+            ok = tt < 2 || mbar_wait_inline(bar(kBarSFree + int(b)), ph ^ 1u, budget, status);
+          else
+            ok = mbar_wait_inline(bar(kBarP + int(b)), ph, budget, status);
+          const uint32_t first = tt * F::kItems + (is_s ? 0 : F::kItems / 2);
+#pragma unroll
+          for (int part = 0; part < 2; ++part) {  // halves of the key's columns, or of the value's
+            const uint32_t item = kFp8 ? first : first + part, slot = item % F::kSlots;
+            if ((!kFp8 || part == 0) && ok)
+              ok = mbar_wait_inline(bar(kBarFull + int(slot)), (item / F::kSlots) & 1u, budget, status);
+            if (!ok) break;
+            umma::fence_after_sync();
+            const uint32_t base = sRing + slot * uint32_t(kSlotBytes);
+            if (is_s) {
+              const uint64_t dk = umma::smem_desc(base, 16, 1024);
+#pragma unroll
+              for (int k = kFp8 ? 4 * part : 0; k < (kFp8 ? 4 * part + 4 : 8); ++k) {
+                // 32-byte step k & 3 of column block k / 4
+                const uint32_t a = uint32_t(k >> 2) * kChunk + uint32_t(k & 3) * 32u;
+                const uint32_t q = uint32_t((kFp8 ? 0 : 2 * part) + (k >> 2)) * (F::kNN * 128u) + uint32_t(k & 3) * 32u;
+#pragma unroll
+                for (int piece = 0; piece < F::kPieces; ++piece)
+                  mma<kFp8>(tmem + b * F::kNN, umma::desc_add(dk, a), umma::desc_add(dq, q + uint32_t(piece) * (kN * 256u)),
+                            id_s, (part | k | piece) != 0);
+              }
+            } else {
+              const uint64_t dv = umma::smem_desc(base + (kFp8 ? uint32_t(part) * kChunk : 0u), kChunk, 1024);
+#pragma unroll
+              for (int k = 0; k < kRowSteps; ++k) {
+                const uint32_t rows = uint32_t(k) * (kFp8 ? 4096u : 2048u);
+#pragma unroll
+                for (int piece = 0; piece < F::kPieces; ++piece)
+                  mma<kFp8>(tmem + uint32_t(2 + part) * F::kNN, umma::desc_add(dv, rows),
+                            umma::desc_add(dp, rows + uint32_t(piece) * kChunk), id_o, tile > g.t0 || (k | piece) != 0);
+              }
+            }
+            if (!kFp8 || part == 1) umma::commit(bar(kBarEmpty + int(slot)));
+          }
+          if (ok) umma::commit(bar((is_s ? kBarS : kBarPV) + int(b)));
         }
       }
-      if (ts > 0) {  // every product complete before TMEM is released
+      // Every product complete before TMEM is released.
+      if (tt > 0)
         umma::commit(bar(kBarDrain));
-        mbar_wait_inline(bar(kBarDrain), 0, budget, status);
-      }
+      else
+        mbar_arrive(bar(kBarDrain));
+      mbar_wait_inline(bar(kBarDrain), 0, budget, status);
     }
     __syncwarp();
   } else {
@@ -360,19 +397,21 @@ __global__ void __launch_bounds__(Cfg<kN, kFp8>::kThreads, 1) tree_tc_kernel(con
     const int g_shift = __ffs(p.G) - 1;
     const int rows_all = p.T * p.G;
     const int row0 = rt * kN;  // this CTA's first row among the T G of a head
-    const int64_t slot_mask = (int64_t(1) << p.c.page_shift) - 1;
-    // This thread's 16-byte unit `i` of P (its key, eight or sixteen rows from n0 on).
-    auto p_unit = [&](int k, int i) {
-      const int un = n0 / (kFp8 ? 16 : 8) + i;
-      return sP + uint32_t(un >> 3) * kChunk + uint32_t(k) * 128u + uint32_t(((un & 7) ^ (k & 7)) << 4);
+    const uint32_t slot_mask = (1u << p.c.page_shift) - 1;
+    // The 16-byte unit `i` of key k's P: eight or sixteen rows from n0 on, of a piece.
+    auto p_unit = [&](int k, int i, int piece) {
+      const int un = (n0 + (F::kWide ? piece * kN : 0)) / (kFp8 ? 16 : 8) + i;
+      const uint32_t block = uint32_t(un >> 3) + (kFp8 && !F::kWide ? uint32_t(piece) : 0u);
+      return sP + block * kChunk + uint32_t(k) * 128u + uint32_t(((un & 7) ^ (k & 7)) << 4);
     };
-    // The quarters' exchange of one value per row lies in the part's own columns of P, which
-    // no product reads then: row n's from quarter q is with the thread of lane n % 32 of it.
-    static_assert(C == 16 || C == 32, "a row's value fits a lane");
-    auto put = [&](float v) { asm volatile("st.shared.f32 [%0], %1;" ::"r"(p_unit(key, 0)), "f"(v) : "memory"); };
-    auto get = [&](int q, int n) {
+    // The quarters' exchange of one value for each of sixteen rows lies in the thread's own
+    // columns of P, which no product reads then: row c0 + n's from quarter q is with lane n.
+    auto put = [&](int c0, float v) {
+      asm volatile("st.shared.f32 [%0], %1;" ::"r"(p_unit(key, c0 / (kFp8 ? 16 : 8), 0)), "f"(v) : "memory");
+    };
+    auto get = [&](int c0, int q, int n) {
       float v;
-      asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v) : "r"(p_unit(q * 32 + n, 0)) : "memory");
+      asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v) : "r"(p_unit(q * 32 + n, c0 / (kFp8 ? 16 : 8), 0)) : "memory");
       return v;
     };
     uint32_t tt = 0;  // tiles so far
@@ -381,44 +420,28 @@ __global__ void __launch_bounds__(Cfg<kN, kFp8>::kThreads, 1) tree_tc_kernel(con
     while (ok && tree_next(p, cur, &g)) {
       const int32_t* table = p.table + int64_t(g.b) * p.max_pages;
       // Q of this head: all softmax warps, a row each time; every reader of the last one is done.
-      for (int r = warp; r < kN; r += F::kSoftWarps) {
-        const int n = row0 + r, t = n >> g_shift;
-        uint4 u = make_uint4(0, 0, 0, 0);
-        if (t < g.s.drafted)
-          u = *reinterpret_cast<const uint4*>(reinterpret_cast<const __nv_bfloat16*>(p.q.p) + g.b * p.q.sb +
-                                              int64_t(g.h * p.G + (n & (p.G - 1))) * p.q.sh + t * p.q.sl + 8 * lane);
-        if constexpr (!kFp8) {
-          sts16(sQ + uint32_t(lane >> 3) * (kN * 128u) + uint32_t(r) * 128u + uint32_t(((lane & 7) ^ (r & 7)) << 4), u);
-        } else {
-          float x[8], lo[8];
-          unpack8(u, x);
-          float amax = 0.f;
-          bool finite = true;
+      constexpr int kQRows = kN / F::kSoftWarps < 4 ? kN / F::kSoftWarps : 4;  // loads in flight
+#pragma unroll 1
+      for (int r0 = warp; r0 < kN; r0 += kQRows * F::kSoftWarps) {
+        uint4 u[kQRows];
 #pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            amax = fmaxf(amax, fabsf(x[i]));
-            finite = finite && fabsf(x[i]) < INFINITY;
+        for (int i = 0; i < kQRows; ++i) {
+          const int n = row0 + r0 + i * F::kSoftWarps, t = n >> g_shift;
+          u[i] = make_uint4(0, 0, 0, 0);
+          if (t < g.s.drafted)
+            u[i] = *reinterpret_cast<const uint4*>(reinterpret_cast<const __nv_bfloat16*>(p.q.p) + g.b * p.q.sb +
+                                                   int64_t(g.h * p.G + (n & (p.G - 1))) * p.q.sh + t * p.q.sl + 8 * lane);
+        }
+#pragma unroll
+        for (int i = 0; i < kQRows; ++i) {
+          const int r = r0 + i * F::kSoftWarps;
+          if constexpr (!kFp8) {
+            sts16(sQ + uint32_t(lane >> 3) * (kN * 128u) + uint32_t(r) * 128u + uint32_t(((lane & 7) ^ (r & 7)) << 4),
+                  u[i]);
+          } else {
+            const float f = put_query<kN, F::kWide>(u[i], sQ, r);
+            if (lane == 0) sh_f[r] = f * p.scale_log2;
           }
-#pragma unroll
-          for (int o = 16; o >= 1; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
-          finite = __all_sync(0xffffffffu, finite);
-          const float scale = e4m3_row_scale(finite ? amax : 0.f);
-          const float inv = __uint_as_float((254u << 23) - __float_as_uint(scale));
-#pragma unroll
-          for (int i = 0; i < 8; ++i) x[i] *= inv;
-          const uint32_t h0 = e4m3_encode4(x), h1 = e4m3_encode4(x + 4);
-          e4m3_decode4(h0, lo);
-          e4m3_decode4(h1, lo + 4);
-#pragma unroll
-          for (int i = 0; i < 8; ++i) lo[i] = x[i] - lo[i];
-          const uint32_t a = sQ + uint32_t(lane >> 4) * (kN * 128u) + uint32_t(r) * 128u +
-                             uint32_t((((lane & 15) >> 1) ^ (r & 7)) << 4) + uint32_t(lane & 1) * 8u;
-          asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(a), "r"(h0), "r"(h1) : "memory");
-          asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(a + kN * 256u), "r"(e4m3_encode4(lo)),
-                       "r"(e4m3_encode4(lo + 4))
-                       : "memory");
-          // A row with an infinity or NaN has no finite score.
-          if (lane == 0) sh_f[r] = finite ? scale * p.scale_log2 : __uint_as_float(0x7fc00000u);
         }
       }
       if (quarter == 0 && lane < C) sh_m[n0 + lane] = kNoMax;
@@ -432,196 +455,247 @@ __global__ void __launch_bounds__(Cfg<kN, kFp8>::kThreads, 1) tree_tc_kernel(con
 #pragma unroll
       for (int i = 0; i < C; ++i) l[i] = 0.f;
 
-      for (int64_t tile = g.t0; tile < g.t1; ++tile, ++tt) {
+      // The key's page two tiles ahead and its scales one tile ahead of their use: neither
+      // load, the second through the first, is waited for.
+      auto page_at = [&](int tile) {
+        const uint32_t j = uint32_t(tile) * kTreeTile + key;
+        return tile < g.t1 && j < g.s.keys ? page_of(p.c, table, p.max_pages, j) : -1;
+      };
+      int page = page_at(g.t0), page_next = page_at(g.t0 + 1);
+      auto scales_at = [&](int tile, int page, float* ks, float* vs) {
+        if (kFp8 && page >= 0) {
+          const int64_t at =
+              (int64_t(page) * p.c.Hkv + g.h) * (slot_mask + 1) + ((uint32_t(tile) * kTreeTile + key) & slot_mask);
+          *ks = p.c.ks[at];
+          *vs = p.c.vs[at];
+        }
+      };
+      float ks_next = 0.f, vs_next = 1.f;
+      scales_at(g.t0, page, &ks_next, &vs_next);
+
+      for (int tile = g.t0; tile < g.t1; ++tile, ++tt) {
         const uint32_t sb = tt & 1u, ph = (tt >> 1) & 1u;
-        const int64_t j = tile * kTreeTile + key;
-        // Is the key there, and what are its scales?
-        const int page = j < g.s.keys ? page_of(p.c, table, p.max_pages, j) : -1;
-        float ks = p.scale_log2, lvs = 0.f, inv_vs = 1.f;
+        const uint32_t j = uint32_t(tile) * kTreeTile + key;
+        const uint32_t v_item = tt * F::kItems + F::kItems / 2;  // this tile's values in the ring
+        auto values_there = [&]() {
+          bool there = true;
+#pragma unroll
+          for (int i = 0; i < F::kItems / 2; ++i)
+            there = warp_wait(bar(kBarFull + int((v_item + i) % F::kSlots)), ((v_item + i) / F::kSlots) & 1u, budget,
+                              status) &&
+                    there;
+          return there;
+        };
+        auto value_unit = [&](int c) {  // 16-byte unit c of the key's values, in any order
+          return sRing + ((v_item + uint32_t(c >> 4)) % F::kSlots) * uint32_t(kSlotBytes) + uint32_t((c >> 3) & 1) * kChunk +
+                 uint32_t(key) * 128u + uint32_t(((c ^ key) & 7) << 4);
+        };
+        const float ks = kFp8 ? (page < 0 ? 0.f : ks_next) : p.scale_log2;
+        float vs = kFp8 && page >= 0 ? vs_next : 1.f, lvs = 0.f, inv_vs = 1.f;
+        const int page_now = page;
+        page = page_next;
+        scales_at(tile + 1, page, &ks_next, &vs_next);
+        page_next = page_at(tile + 2);
+        // Which of this thread's rows see the key: all, unless it is not there or is drafted.
+        const bool drafted = page_now >= 0 && j >= g.s.ctx;
+        uint32_t vis = page_now >= 0 ? 0xffffffffu : 0u;
+        if (drafted) {
+          vis = 0;
+          const int t0 = (row0 + n0) >> g_shift;
+#pragma unroll 4
+          for (int i = 0; i < C >> g_shift; ++i)
+            // (rows past the last drafted token are cleared at the end)
+            if (t0 + i >= g.s.drafted || tree_sees(p, g.b, t0 + i, int(j - g.s.ctx)))
+              vis |= ((1u << p.G) - 1u) << (i * p.G);
+        }
+        const bool masked = __any_sync(0xffffffffu, vis != 0xffffffffu && (C == 32 || (vis & 0xffffu) != 0xffffu));
+        bool fine = ok;
         if constexpr (kFp8) {
-          float vs = 1.f;
-          ks = 0.f;
-          if (page >= 0) {
-            const int64_t at = (int64_t(page) * p.c.Hkv + g.h) * (slot_mask + 1) + (j & slot_mask);
-            ks = p.c.ks[at];
-            vs = p.c.vs[at];
-            if (vs == 0.f) vs = 7.8886090522101181e-31f;  // 2^-100: the weight stays, the value is as good as none
+          // A row of zeros (written with scale 1) puts nothing into O: its scale must not set the
+          // maximum, on which P's few bits hang.  2^-100 keeps the row's weight in the sums.
+          if (__any_sync(0xffffffffu, page_now >= 0 && vs == 1.f)) {
+            fine = values_there() && fine;
+            uint32_t any = 0;
+            if (fine && vs == 1.f)
+#pragma unroll 4
+              for (int c = 0; c < 16; ++c) {
+                const uint4 v = lds16(value_unit(c));
+                any |= (v.x | v.y | v.z | v.w) & 0x7f7f7f7fu;
+              }
+            if (vs == 1.f && any == 0) vs = 0.f;
+            __syncwarp();
           }
+          if (vs == 0.f) vs = 7.8886090522101181e-31f;
           lvs = log2f(vs);
           inv_vs = 1.f / vs;
         }
-        const bool ok_s = ok && warp_wait(bar(kBarS + int(sb)), ph, budget, status);
-        float x[C];
-        if (ok_s) {
-          umma::fence_after_sync();
-          tmem_ld<C>(lane_addr + sb * kN, x);
-          umma::tmem_wait_ld();
-          umma::fence_before_sync();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(bar(kBarSFree + int(sb)));
-        } else {
-#pragma unroll
-          for (int i = 0; i < C; ++i) x[i] = 0.f;
-        }
-#pragma unroll
-        for (int i = 0; i < C; i += 4) {
-          if constexpr (kFp8) {
-            const float4 f = *reinterpret_cast<const float4*>(sh_f + n0 + i);
-            x[i] = fmaf(x[i], ks * f.x, lvs);
-            x[i + 1] = fmaf(x[i + 1], ks * f.y, lvs);
-            x[i + 2] = fmaf(x[i + 2], ks * f.z, lvs);
-            x[i + 3] = fmaf(x[i + 3], ks * f.w, lvs);
-          } else {
-#pragma unroll
-            for (int k = 0; k < 4; ++k) x[i + k] *= ks;
-          }
-        }
-        // Keys that are not there, and drafted tokens that a row does not see.
-        const bool drafted = page >= 0 && j >= g.s.ctx;
-        if (__any_sync(0xffffffffu, page < 0 || drafted)) {
-          const int u = int(j - g.s.ctx);
-#pragma unroll
-          for (int i = 0; i < C; ++i) {
-            const int t = (row0 + n0 + i) >> g_shift;
-            if (page < 0 || (drafted && t < g.s.drafted && !tree_sees(p, g.b, t, u))) x[i] = -INFINITY;
-          }
-        }
-        bool raise = false;
-#pragma unroll
-        for (int i = 0; i < C; i += 4) {
-          const float4 m = *reinterpret_cast<const float4*>(sh_m + n0 + i);
-          raise = raise || x[i] > m.x + F::kSlack || x[i + 1] > m.y + F::kSlack || x[i + 2] > m.z + F::kSlack ||
-                  x[i + 3] > m.w + F::kSlack;
-        }
         // Values that some row must not see: elements that are not finite would reach it as 0 x
         // infinity.  They are cleared in the tile, and added at the end for the rows that see them.
-        const bool scrub = p.T > 1 && (tile + 1) * kTreeTile > g.s.ctx;
-        if (any_thread(part_bar, 128, raise || scrub || !ok_s)) {
-          // O holds tiles up to the last one: complete before it is rescaled, and before the
-          // exchange takes P's place.
-          bool fine = ok_s;
-          if (tt > 0)
-            fine = warp_wait(bar(kBarPV + int((tt - 1) & 1u)), ((tt - 1) >> 1) & 1u, budget, status) && fine;
-          bool zero_row = false;
-          if (kFp8 || scrub) {  // a look at the tile's values
-            const uint32_t v_item = tt * F::kItems + F::kItems / 2;
-#pragma unroll
-            for (int i = 0; i < F::kItems / 2; ++i)
-              fine = warp_wait(bar(kBarFull + int((v_item + i) % F::kSlots)), ((v_item + i) / F::kSlots) & 1u, budget,
-                               status) &&
-                     fine;
-            uint32_t any = 0, bad = 0;
-            if (fine) {
+        if (p.T > 1 && part == 0 && __any_sync(0xffffffffu, drafted)) {
+          fine = values_there() && fine;
+          if (fine && drafted) {
+            uint32_t bad = 0;
 #pragma unroll 1
-              for (int c = 0; c < 8 * F::kItems; ++c) {  // 16-byte units of the row, in any order
-                const uint32_t a = sRing + ((v_item + uint32_t(c >> 4)) % F::kSlots) * uint32_t(kSlotBytes) +
-                                   uint32_t((c >> 3) & 1) * kChunk + uint32_t(key) * 128u + uint32_t(((c ^ key) & 7) << 4);
-                const uint4 v = lds16(a);
-                uint32_t w[4] = {v.x, v.y, v.z, v.w}, hit = 0;
+            for (int c = 0; c < 8 * F::kItems; ++c) {
+              const uint4 v = lds16(value_unit(c));
+              uint32_t w[4] = {v.x, v.y, v.z, v.w}, hit = 0;
 #pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                  any |= w[k] & (kFp8 ? 0x7f7f7f7fu : 0u);
-                  const uint32_t m = kFp8 ? __vcmpeq4(w[k] & 0x7f7f7f7fu, 0x7f7f7f7fu)  // e4m3 has NaN alone
-                                          : __vcmpeq2(w[k] & 0x7f807f80u, 0x7f807f80u);
-                  hit |= m;
-                  w[k] &= ~m;
-                }
-                if (scrub && drafted && hit) {
-                  bad = 1;
-                  if (part == 0) sts16(a, make_uint4(w[0], w[1], w[2], w[3]));  // for all parts
-                }
+              for (int k = 0; k < 4; ++k) {
+                const uint32_t m = kFp8 ? __vcmpeq4(w[k] & 0x7f7f7f7fu, 0x7f7f7f7fu)  // e4m3 has NaN alone
+                                        : __vcmpeq2(w[k] & 0x7f807f80u, 0x7f807f80u);
+                hit |= m;
+                w[k] &= ~m;
+              }
+              if (hit) sts16(value_unit(c), make_uint4(w[0], w[1], w[2], w[3]));
+              bad |= hit;
+            }
+            const int u = int(j - g.s.ctx);
+            if (bad) atomicOr(&sh_bad[u >> 5], 1u << (u & 31));
+          }
+          fence_proxy_async_smem();
+          __syncwarp();
+        }
+        fine = warp_wait(bar(kBarS + int(sb)), ph, budget, status) && fine;
+        umma::fence_after_sync();
+        // The product of the tile before: P's last reader, and what O holds.
+        auto last_product = [&]() {
+          return tt == 0 || warp_wait(bar(kBarPV + int((tt - 1) & 1u)), ((tt - 1) >> 1) & 1u, budget, status);
+        };
+        bool stop = false;
+#pragma unroll
+        for (int c0 = 0; c0 < C; c0 += 16) {
+          // Scores of the rows n0 + c0 .. + 15, in powers of two.
+          auto scores = [&](float (&x)[16]) {
+            umma::tmem_ld16(lane_addr + sb * F::kNN + uint32_t(c0), x);
+            if constexpr (F::kWide) {
+              float y[16];
+              umma::tmem_ld16(lane_addr + sb * F::kNN + kN + uint32_t(c0), y);
+              umma::tmem_wait_ld();
+#pragma unroll
+              for (int i = 0; i < 16; ++i) x[i] += y[i];
+            } else {
+              umma::tmem_wait_ld();
+            }
+#pragma unroll
+            for (int i = 0; i < 16; i += 4) {
+              if constexpr (kFp8) {
+                const float4 f = *reinterpret_cast<const float4*>(sh_f + n0 + c0 + i);
+                x[i] = fmaf(x[i], ks * f.x, lvs);
+                x[i + 1] = fmaf(x[i + 1], ks * f.y, lvs);
+                x[i + 2] = fmaf(x[i + 2], ks * f.z, lvs);
+                x[i + 3] = fmaf(x[i + 3], ks * f.w, lvs);
+              } else {
+#pragma unroll
+                for (int k = 0; k < 4; ++k) x[i + k] *= ks;
               }
             }
-            // A row of zeros puts nothing into O: its scale must not set the maximum.
-            zero_row = kFp8 && any == 0;
-            if (part == 0 && bad) {
-              const int u = int(j - g.s.ctx);
-              atomicOr(&sh_bad[u >> 5], 1u << (u & 31));
+            if (masked) {
+#pragma unroll
+              for (int i = 0; i < 16; ++i)
+                if (!((vis >> (c0 + i)) & 1u)) x[i] = -INFINITY;
             }
-            fence_proxy_async_smem();
-          }
+          };
+          // 2^(x - m) with the maxima so far; the largest exponent.
+          float x[16];
+          auto weights = [&]() {
+            float top[4];
 #pragma unroll
-          for (int c0 = 0; c0 < C; c0 += 16) {
-            float y[16];
+            for (int i = 0; i < 16; i += 4) {
+              const float4 m = *reinterpret_cast<const float4*>(sh_m + n0 + c0 + i);
+              x[i] -= m.x, x[i + 1] -= m.y, x[i + 2] -= m.z, x[i + 3] -= m.w;
 #pragma unroll
-            for (int i = 0; i < 16; ++i) y[i] = zero_row ? -INFINITY : x[c0 + i];
-            const float mx = lanes_reduce<16, true>(y);  // lane l: row c0 + l / 2
+              for (int k = 0; k < 4; ++k) top[k] = i == 0 ? x[k] : fmaxf(top[k], x[i + k]);
+            }
+            const float z = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
+#pragma unroll
+            for (int i = 0; i < 16; ++i) x[i] = ex2(x[i]);
+            return z;
+          };
+          scores(x);
+          const bool raise = weights() > F::kSlack;
+          if (any_thread(part_bar, 128, raise || !fine)) {
+            fine = last_product() && fine;
+            if (any_thread(part_bar, 128, !fine)) {
+              stop = true;
+              break;
+            }
+            umma::fence_after_sync();
+            scores(x);
+            const float mx = lanes_reduce<true>(x);  // lane l: row c0 + l / 2
             const float v = __shfl_sync(0xffffffffu, mx, (2 * lane) & 31);
-            if ((lane & 16) == c0) put(v);  // lane n of the quarter: row n (only lanes below C have one)
-          }
-          if (any_thread(part_bar, 128, !fine)) {
-            ok = false;
-            break;
-          }
-          umma::fence_after_sync();
-#pragma unroll
-          for (int c0 = 0; c0 < C; c0 += 16) {
-            float alpha[16];
-            bool any = false;
-#pragma unroll
-            for (int i = 0; i < 16; ++i) {
-              const int n = c0 + i;
-              const float top = fmaxf(fmaxf(get(0, n), get(1, n)), fmaxf(get(2, n), get(3, n)));
-              const float m = sh_m[n0 + n];
-              const bool up = top > m + F::kSlack;
-              alpha[i] = up ? ex2(m - top) : 1.f;
-              any = any || up;
-              l[n] *= alpha[i];
+            if (lane < 16) put(c0, v);  // lane n of the quarter: row c0 + n
+            sync_threads(part_bar, 128);
+            float top = 0.f, m_old = 0.f;
+            if (lane < 16) {
+              top = fmaxf(fmaxf(get(c0, 0, lane), get(c0, 1, lane)), fmaxf(get(c0, 2, lane), get(c0, 3, lane)));
+              m_old = sh_m[n0 + c0 + lane];
             }
-            if (any && tile > g.t0) {  // the same in all threads of the part
+            const bool up = lane < 16 && top > m_old + F::kSlack;
+            const float alpha = up ? ex2(m_old - top) : 1.f;
+            sync_threads(part_bar, 128);  // all have read the old maxima and the exchange
+            if (quarter == 0 && up) sh_m[n0 + c0 + lane] = top;
+            if (__any_sync(0xffffffffu, up)) {  // the same in the part's four warps
 #pragma unroll
-              for (int half = 0; half < 2; ++half) {
-                float o[16];
-                const uint32_t a = lane_addr + uint32_t((2 + half) * kN + c0);
-                umma::tmem_ld16(a, o);
-                umma::tmem_wait_ld();
-                uint32_t w[16];
+              for (int i = 0; i < 16; ++i) l[c0 + i] *= __shfl_sync(0xffffffffu, alpha, i);
+              if (tile > g.t0) {
+#pragma unroll 1
+                for (int block = 0; block < (F::kWide ? 4 : 2); ++block) {  // halves of O, and pieces
+                  float o[16];
+                  const uint32_t a = lane_addr + uint32_t((2 + (block & 1)) * F::kNN + (block >> 1) * kN + c0);
+                  umma::tmem_ld16(a, o);
+                  umma::tmem_wait_ld();
+                  uint32_t w[16];
 #pragma unroll
-                for (int i = 0; i < 16; ++i) w[i] = __float_as_uint(o[i] * alpha[i]);
-                umma::tmem_st16u(a, w);
+                  for (int i = 0; i < 16; ++i) w[i] = __float_as_uint(o[i] * __shfl_sync(0xffffffffu, alpha, i));
+                  umma::tmem_st16u(a, w);
+                }
+                umma::tmem_wait_st();
               }
-              umma::tmem_wait_st();
+            }
+            sync_threads(part_bar, 128);
+            scores(x);
+            weights();
+          }
+          if (c0 + 16 == C) {  // the last read of S
+            umma::fence_before_sync();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar(kBarSFree + int(sb)));
+          }
+          // The row sums, and P.  A wait that ran out here is agreed upon with the next tile.
+          if (c0 == 0) ok = last_product() && ok;
+          uint32_t hi[kFp8 ? 4 : 8], lo[4];
+          (void)lo;
+#pragma unroll
+          for (int i = 0; i < 16; i += 4) {
+            if constexpr (kFp8) {
+              float e[4], h[4];
+#pragma unroll
+              for (int k = 0; k < 4; ++k) {
+                l[c0 + i + k] = fmaf(x[i + k], inv_vs, l[c0 + i + k]);
+                e[k] = x[i + k] * kPScale;
+                h[k] = __uint_as_float(__float_as_uint(e[k]) & 0xfff00000u);  // three mantissa bits
+                e[k] -= h[k];
+              }
+              hi[i / 4] = e4m3_encode4(h);
+              lo[i / 4] = e4m3_encode4(e);
+            } else {
+#pragma unroll
+              for (int k = 0; k < 4; ++k) l[c0 + i + k] += x[i + k];
+              hi[i / 2] = pack_bf16x2(x[i], x[i + 1]);
+              hi[i / 2 + 1] = pack_bf16x2(x[i + 2], x[i + 3]);
             }
           }
-          float top = 0.f;
-          if (lane < C) top = fmaxf(fmaxf(get(0, lane), get(1, lane)), fmaxf(get(2, lane), get(3, lane)));
-          sync_threads(part_bar, 128);  // all have read the old maxima and the exchange
-          if (quarter == 0 && lane < C && top > sh_m[n0 + lane] + F::kSlack) sh_m[n0 + lane] = top;
-          sync_threads(part_bar, 128);
-        }
-        // P and the row sums.
-        uint32_t hi[kFp8 ? C / 4 : C / 2];
-        uint32_t lo[kFp8 ? C / 4 : 1];
-        (void)lo;
-#pragma unroll
-        for (int i = 0; i < C; i += 4) {
-          const float4 m = *reinterpret_cast<const float4*>(sh_m + n0 + i);
-          float e[4] = {ex2(x[i] - m.x), ex2(x[i + 1] - m.y), ex2(x[i + 2] - m.z), ex2(x[i + 3] - m.w)};
           if constexpr (kFp8) {
-            float h[4];
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-              l[i + k] = fmaf(e[k], inv_vs, l[i + k]);
-              e[k] *= 64.f;
-              h[k] = __uint_as_float(__float_as_uint(e[k]) & 0xfff00000u);  // three mantissa bits
-              e[k] -= h[k];
-            }
-            hi[i / 4] = e4m3_encode4(h);
-            lo[i / 4] = e4m3_encode4(e);
+            sts16(p_unit(key, c0 / 16, 0), make_uint4(hi[0], hi[1], hi[2], hi[3]));
+            sts16(p_unit(key, c0 / 16, 1), make_uint4(lo[0], lo[1], lo[2], lo[3]));
           } else {
-#pragma unroll
-            for (int k = 0; k < 4; ++k) l[i + k] += e[k];
-            hi[i / 2] = pack_bf16x2(e[0], e[1]);
-            hi[i / 2 + 1] = pack_bf16x2(e[2], e[3]);
+            sts16(p_unit(key, c0 / 8, 0), make_uint4(hi[0], hi[1], hi[2], hi[3]));
+            sts16(p_unit(key, c0 / 8 + 1, 0), make_uint4(hi[4], hi[5], hi[6], hi[7]));
           }
         }
-        // P's last reader is the product of the tile before.
-        if (tt > 0) ok = warp_wait(bar(kBarPV + int((tt - 1) & 1u)), ((tt - 1) >> 1) & 1u, budget, status) && ok;
-#pragma unroll
-        for (int i = 0; i < (kFp8 ? C / 16 : C / 8); ++i) {
-          const uint32_t a = p_unit(key, i);
-          sts16(a, make_uint4(hi[4 * i], hi[4 * i + 1], hi[4 * i + 2], hi[4 * i + 3]));
-          if constexpr (kFp8) sts16(a + kChunk, make_uint4(lo[4 * i], lo[4 * i + 1], lo[4 * i + 2], lo[4 * i + 3]));
+        if (stop) {
+          ok = false;
+          break;
         }
         fence_proxy_async_smem();
         umma::fence_before_sync();
@@ -639,60 +713,67 @@ __global__ void __launch_bounds__(Cfg<kN, kFp8>::kThreads, 1) tree_tc_kernel(con
           float y[16];
 #pragma unroll
           for (int i = 0; i < 16; ++i) y[i] = l[c0 + i];
-          const float sum = lanes_reduce<16, false>(y);
+          const float sum = lanes_reduce<false>(y);
           const float v = __shfl_sync(0xffffffffu, sum, (2 * lane) & 31);
-          if ((lane & 16) == c0) put(v);
+          if (lane < 16) put(c0, v);
         }
         sync_threads(part_bar, 128);
         const bool whole = g.whole();
         const int64_t part_at = ((int64_t(worker) * 2 + g.slot()) * p.row_tiles + rt) * kN;
         const int64_t head_row = (int64_t(g.b) * p.c.Hkv + g.h) * p.G;
-        uint32_t bad = 0;
-        for (int i = 0; i < 32; ++i) bad |= sh_bad[i];
-#pragma unroll 1
-        for (int n = 0; n < C; ++n) {
-          const int row = row0 + n0 + n, t = row >> g_shift;
-          if (row >= rows_all) break;
-          const float sum = (get(0, n) + get(1, n)) + (get(2, n) + get(3, n));
-          const bool none = t >= g.s.drafted || sum == 0.f;
-          const float inv = none ? 0.f : (kFp8 ? 0.015625f : 1.f) / sum;
-          const int64_t out_row = (head_row + (row & (p.G - 1))) * p.T + t;
-          if (key == 0) {
-            const float lse = none ? -INFINITY : (sh_m[n0 + n] + log2f(sum)) * kLn2;
+        const bool bad = __any_sync(0xffffffffu, sh_bad[lane] != 0);
+        // Lane n of every warp: row n's factor.
+        const int my_row = row0 + n0 + lane, my_t = my_row >> g_shift;
+        float inv = 0.f;
+        if (lane < C && my_row < rows_all) {
+          const int c0 = lane & 16, n = lane & 15;
+          const float sum = (get(c0, 0, n) + get(c0, 1, n)) + (get(c0, 2, n) + get(c0, 3, n));
+          const bool none = my_t >= g.s.drafted || sum == 0.f;
+          inv = none ? 0.f : (kFp8 ? 1.f / kPScale : 1.f) / sum;
+          if (quarter == 0) {
+            const float lse = none ? -INFINITY : (sh_m[n0 + lane] + log2f(sum)) * kLn2;
             if (whole)
-              p.lse[out_row] = lse;
+              p.lse[(head_row + (my_row & (p.G - 1))) * p.T + my_t] = lse;
             else
-              p.lse_part[part_at + n0 + n] = lse;
+              p.lse_part[part_at + n0 + lane] = lse;
           }
-#pragma unroll
-          for (int half = 0; half < 2; ++half) {
-            uint32_t w;
-            asm volatile("tcgen05.ld.sync.aligned.32x32b.x1.b32 {%0}, [%1];"
-                         : "=r"(w)
-                         : "r"(lane_addr + uint32_t((2 + half) * kN + n)));
-            umma::tmem_wait_ld();
-            float v = none ? 0.f : __uint_as_float(w) * inv;
-            const int d = half * 128 + key;
-            if (bad && !none) {  // values that were cleared, for the rows that see them
+        }
 #pragma unroll 1
-              for (int u = 0; u < g.s.drafted; ++u) {
-                if (!((sh_bad[u >> 5] >> (u & 31)) & 1u) || !tree_sees(p, g.b, t, u)) continue;
-                const int64_t jb = g.s.ctx + u;
-                const int64_t at = table[jb >> p.c.page_shift] * p.c.sp + g.h * p.c.sh + (jb & slot_mask) * p.c.st + d;
-                if constexpr (kFp8) {
-                  if ((uint8_t(p.c.v[at]) & 0x7f) == 0x7f) v = __uint_as_float(0x7fc00000u);
+        for (int c0 = 0; c0 < C; c0 += 16) {
+          if (row0 + n0 + c0 >= rows_all) break;
+#pragma unroll 1
+          for (int half = 0; half < 2; ++half) {
+            float o[16];
+            const uint32_t a = lane_addr + uint32_t((2 + half) * F::kNN + c0);
+            umma::tmem_ld16(a, o);
+            if constexpr (F::kWide) {
+              float y[16];
+              umma::tmem_ld16(a + kN, y);
+              umma::tmem_wait_ld();
+#pragma unroll
+              for (int i = 0; i < 16; ++i) o[i] += y[i];
+            } else {
+              umma::tmem_wait_ld();
+            }
+            const int d = half * 128 + key;
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+              const int n = c0 + i, row = row0 + n0 + n, t = row >> g_shift;
+              const float f = __shfl_sync(0xffffffffu, inv, n);
+              float v = f == 0.f ? 0.f : o[i] * f;
+              if (bad && f != 0.f) v += hidden_values<kFp8>(p, g, table, sh_bad, t, d);
+              if (row < rows_all) {
+                if (!whole) {
+                  p.o_part[(part_at + n0 + n) * kHeadDim + d] = v;
                 } else {
-                  const float y = __bfloat162float(reinterpret_cast<const __nv_bfloat16*>(p.c.v)[at]);
-                  if (!(fabsf(y) < INFINITY)) v += y;
+                  const int64_t at = ((head_row + (row & (p.G - 1))) * p.T + t) * kHeadDim + d;
+                  if (p.out_bf16)
+                    static_cast<__nv_bfloat16*>(p.out)[at] = __float2bfloat16_rn(v);
+                  else
+                    static_cast<float*>(p.out)[at] = v;
                 }
               }
             }
-            if (!whole)
-              p.o_part[(part_at + n0 + n) * kHeadDim + d] = v;
-            else if (p.out_bf16)
-              static_cast<__nv_bfloat16*>(p.out)[out_row * kHeadDim + d] = __float2bfloat16_rn(v);
-            else
-              static_cast<float*>(p.out)[out_row * kHeadDim + d] = v;
           }
         }
         umma::fence_before_sync();
@@ -703,7 +784,7 @@ __global__ void __launch_bounds__(Cfg<kN, kFp8>::kThreads, 1) tree_tc_kernel(con
   }
   umma::fence_before_sync();
   __syncthreads();
-  if (warp == F::kWarps - 1) {
+  if (warp == F::kIssuer) {
     umma::fence_after_sync();
     umma::tmem_dealloc(tmem, F::kTmem);
   }
