@@ -19,12 +19,13 @@ range is skipped on the device and recorded in the pool's status word (``status`
 from __future__ import annotations
 
 import ctypes
+import functools
 
 import torch
 
 from . import _device, _lib
 from . import status as _status_of
-from ._views import check_ints, check_positions, float_code, launch, on_stream, rows
+from ._views import check_ints, check_positions, float_code, launch, new_like, on_stream, rows
 
 _CODES = {torch.float32: _lib.GQA_F32, torch.bfloat16: _lib.GQA_BF16, torch.float8_e4m3fn: _lib.GQA_E4M3}
 
@@ -60,13 +61,11 @@ class PagedCache:
         if status_word is not None:
             check_ints(status_word, (1,), k.device, "status_word")
         self.k, self.v, self.k_scale, self.v_scale, self.status_word = k, v, k_scale, v_scale, status_word
-        self.device, self.dtype, self.Hkv, self.page_size = k.device, k.dtype, Hkv, page
-
-        def ptr(t):
-            return None if t is None else t.data_ptr()
-
-        self._struct = _lib.Cache(k.data_ptr(), v.data_ptr(), ptr(k_scale), ptr(v_scale), ptr(status_word), sp, sh, st,
-                                  n, Hkv, page, code)
+        self.device, self.dtype, self.code, self.Hkv, self.page_size = k.device, k.dtype, code, Hkv, page
+        self._struct = _lib.Cache(k.data_ptr(), v.data_ptr(), None if k_scale is None else k_scale.data_ptr(),
+                                  None if v_scale is None else v_scale.data_ptr(),
+                                  None if status_word is None else status_word.data_ptr(), sp, sh, st, n, Hkv, page,
+                                  code)
         self._ref = ctypes.byref(self._struct)
 
     @classmethod
@@ -149,10 +148,14 @@ def read(pool, page_table, lens, max_len, *, dtype=torch.bfloat16, out=None, str
     return k, v
 
 
+@functools.lru_cache(maxsize=1024)
+def _tree_bytes(B, Hq, Hkv, T, max_pages, page_size, code, cache_code) -> int:
+    return int(_lib.load().gqa_attn_tree_workspace_bytes(B, Hq, Hkv, T, max_pages, page_size, 256, code, cache_code))
+
+
 def workspace_bytes(B, Hq, T, pool, max_pages, dtype=torch.bfloat16) -> int:
     """Device workspace bytes of one ``attend`` call (0 if the shape is rejected)."""
-    return int(_lib.load().gqa_attn_tree_workspace_bytes(B, Hq, pool.Hkv, T, max_pages, pool.page_size, 256,
-                                                         float_code(dtype), _CODES[pool.dtype]))
+    return _tree_bytes(B, Hq, pool.Hkv, T, max_pages, pool.page_size, float_code(dtype), pool.code)
 
 
 def attend(q, pool, page_table, context_lens, *, tree_mask=None, tree_lens=None, out=None, lse=None, workspace=None,
@@ -180,16 +183,14 @@ def attend(q, pool, page_table, context_lens, *, tree_mask=None, tree_lens=None,
                 or not tree_mask.is_contiguous()):
             raise ValueError(f"tree_mask must be a contiguous bool or uint8 tensor [{T}, {T}] or [{B}, {T}, {T}]")
         mask, mask_sb = tree_mask.data_ptr(), T * T if tree_mask.dim() == 3 else 0
-    lib = _lib.load()
     with on_stream(stream):
         if out is None:
-            out = torch.empty((B, Hq, T, d), dtype=q.dtype, device=dev)
+            out = new_like(q)
         if lse is None:
             lse = torch.empty((B, Hq, T), dtype=torch.float32, device=dev)
         if workspace is None:
-            need = lib.gqa_attn_tree_workspace_bytes(B, Hq, pool.Hkv, T, max_pages, pool.page_size, d, code,
-                                                     pool._struct.dtype)
-            workspace = torch.empty(max(need, 256), dtype=torch.uint8, device=dev)
+            workspace = torch.empty(max(_tree_bytes(B, Hq, pool.Hkv, T, max_pages, pool.page_size, code, pool.code), 256),
+                                    dtype=torch.uint8, device=dev)
     if out.shape != q.shape or out.dtype != q.dtype or out.device != dev or not out.is_contiguous():
         raise ValueError("out must be a contiguous tensor of q's shape and dtype")
     if lse.shape != (B, Hq, T) or lse.dtype != torch.float32 or lse.device != dev or not lse.is_contiguous():

@@ -162,8 +162,9 @@ __device__ __forceinline__ bool tree_sees(const TreeParams& p, int b, int t, int
 
 // FP32 pipe: q of either type, any pages but bf16 q over bf16 or e4m3 ones; rows 4 or 8.
 int launch_tree_ffma(const TreeParams& p, bool q_bf16, int rows, cudaStream_t stream);
-// Tensor cores: bf16 q over bf16 or e4m3 pages; rows 16, 32, 64 or 128.
+// Tensor cores: bf16 q over bf16 or e4m3 pages; rows 16, 32, 64 (the keys as M) or 128.
 int launch_tree_tc(const TreeParams& p, int rows, cudaStream_t stream);
+int launch_tree_rows(const TreeParams& p, cudaStream_t stream);
 int launch_tree_merge(const TreeParams& p, int rows_per_tile, cudaStream_t stream);
 
 // Rows per CTA and worker count of a call, by types and shape (host).

@@ -1,0 +1,550 @@
+// Attention of drafted tokens over the paged cache on the tensor cores with the query rows
+// as M, sm_100a: tiles of 128 rows (T G rows of a key/value head, above 64), bf16 queries,
+// bf16 or e4m3 pages.  With this many rows the keys as M (tree_tc.cu) would cost more: its
+// products take both operands from shared memory, one of them transposed (a 128 x 128 x 16
+// step measured 140 cycles against 97 for S and 136 for twice the work of O here).
+//
+// S = Q K^T (M = rows, N = 128 keys) and O += P V (P in TMEM, N = 256 columns).  TMEM: O in
+// columns 0 .. 255, two S buffers of 128; P(t) takes the place of the first 64 columns of
+// S(t): bf16 pairs, or both e4m3 pieces of 32 columns each.  Softmax: one thread per row and
+// 32 keys, so that maxima and sums are the thread's own, joined over four warps through
+// shared memory only when a maximum rises.  e4m3 pages, their scales, the pieces of queries
+// and probabilities, lazy maxima and values that a mask hides: as in tree_tc.cu.
+//
+// Warps: 16 for the softmax (lane quarter x 32 keys), one producer per 32 KiB slot, two
+// issuers.  A bf16 tile is four slots: the keys' columns 0 - 127 and 128 - 255 ([2][128
+// keys][128 bytes]), then the values of keys 0 - 63 and 64 - 127 ([4][64 keys][128 bytes]),
+// so that one product spans all 256 columns; an e4m3 tile is two ([2][128 keys][128 bytes]).
+#include "tree_tc.cuh"
+
+namespace gqa {
+namespace {
+
+constexpr int kRows = 128;
+constexpr int kSoftWarps = 16;
+
+template <bool kFp8>
+struct RowsCfg {
+  static constexpr int kItems = kFp8 ? 2 : 4;
+  static constexpr int kSlots = kFp8 ? 4 : 5;  // what shared memory has room for
+  static constexpr int kIssuer = kSoftWarps + kSlots;
+  static constexpr int kThreads = 32 * (kIssuer + 2);
+  static constexpr int kOffQ = 0;  // bf16 [4][128 rows][128 bytes], or e4m3 [2 pieces][2][128 rows][128 bytes]
+  static constexpr int kOffRing = kRows * 512;
+  static constexpr int kOffBar = kOffRing + kSlots * kSlotBytes;
+  static constexpr int kOffStart = kOffBar + 8 * 20;  // the worker's cursor, the TMEM address
+  static constexpr int kOffBad = kOffStart + 48;      // 32 words: drafted tokens with a value that is not finite
+  static constexpr int kOffRed = kOffBad + 128 + 48;  // [4 parts][128 rows] exchange
+  static constexpr int kOffF = kOffRed + 4 * kRows * 4;       // [128] factors of the rows' scores (e4m3)
+  static constexpr int kOffScale = kOffF + (kFp8 ? 512 : 0);  // [16 warps][3][32]: ks, log2 vs, 1 / vs (e4m3)
+  static constexpr int kSmem = kOffScale + (kFp8 ? kSoftWarps * 384 : 0);
+  static constexpr float kSlack = kFp8 ? 4.f : 8.f;
+  static_assert(kSmem <= 232448 && kOffRed % 16 == 0 && sizeof(TreeCursor) <= 40, "shared memory per block");
+};
+
+enum { kRBarQ = 0, kRBarS = 1, kRBarP = 3, kRBarPV = 5, kRBarDrain = 7, kRBarFull = 8, kRBarEmpty = 14 };
+
+// Eight consecutive 32-bit columns of raw words into this thread's TMEM lane.
+__device__ __forceinline__ void tmem_st8u(uint32_t taddr, const uint32_t (&r)[8]) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(taddr), "r"(r[0]), "r"(r[1]),
+               "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+               : "memory");
+}
+
+template <bool kFp8>
+__global__ void __launch_bounds__(RowsCfg<kFp8>::kThreads, 1) tree_rows_kernel(const __grid_constant__ TreeParams p) {
+  using F = RowsCfg<kFp8>;
+  extern __shared__ __align__(1024) char smem_raw[];
+  const uint32_t sbase = smem_u32(smem_raw);
+  const bool misaligned = (sbase & 1023u) != 0;  // the swizzle needs it; never expected to fail
+  const uint32_t sQ = sbase + F::kOffQ, sRing = sbase + F::kOffRing;
+  auto bar = [&](int i) { return sbase + F::kOffBar + 8u * uint32_t(i); };
+  TreeCursor& start = *reinterpret_cast<TreeCursor*>(smem_raw + F::kOffStart);
+  volatile uint32_t& tmem_slot = *reinterpret_cast<uint32_t*>(smem_raw + F::kOffStart + 40);
+  uint32_t* sh_bad = reinterpret_cast<uint32_t*>(smem_raw + F::kOffBad);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int worker = blockIdx.x / p.row_tiles, rt = blockIdx.x % p.row_tiles;
+  const int64_t budget = p.wait_budget_ns;
+  int32_t* status = p.c.status;
+
+  if (warp == 0) {
+    const TreeCursor c = tree_start(p, worker);
+    if (lane == 0) {
+      start = c;
+      mbar_init(bar(kRBarQ), kSoftWarps);
+      for (int i = 0; i < 2; ++i) {
+        mbar_init(bar(kRBarS + i), 1);
+        mbar_init(bar(kRBarP + i), kSoftWarps);
+        mbar_init(bar(kRBarPV + i), 1);
+      }
+      mbar_init(bar(kRBarDrain), 2);
+      for (int i = 0; i < F::kSlots; ++i) {
+        mbar_init(bar(kRBarFull + i), 1);
+        mbar_init(bar(kRBarEmpty + i), 1);
+      }
+      fence_barrier_init();
+      if (misaligned) set_status(status, GQA_ERR_LAUNCH);
+    }
+  }
+  if (warp == F::kIssuer) umma::tmem_alloc(sbase + F::kOffStart + 40, 512);
+  umma::fence_before_sync();
+  __syncthreads();
+  umma::fence_after_sync();
+  const uint32_t tmem = tmem_slot;
+  TreeCursor cur = start;
+  TreeSegment g;
+
+  if (misaligned) {
+    // no role
+  } else if (warp >= kSoftWarps && warp < F::kIssuer) {
+    // ---------------------------------------------------------------- producers
+    const int s = warp - kSoftWarps;
+    const uint32_t slot = sRing + uint32_t(s) * kSlotBytes;
+    constexpr int kEs = kFp8 ? 1 : 2;
+    const uint32_t slot_mask = (1u << p.c.page_shift) - 1;
+    const int64_t row_bytes = p.c.st * kEs;
+    int idx = s;
+    bool live = tree_next(p, cur, &g);
+    // The page of each group of eight keys of this item's tile, in lanes 0 .. 15.
+    auto pages = [&]() {
+      while (live && idx >= (g.t1 - g.t0) * F::kItems) {
+        idx -= (g.t1 - g.t0) * F::kItems;
+        live = tree_next(p, cur, &g);
+      }
+      if (!live) return -1;
+      const uint32_t j = uint32_t(g.t0 + idx / F::kItems) * kTreeTile + lane * 8;
+      return lane < 16 && j < g.s.keys ? page_of(p.c, p.table + int64_t(g.b) * p.max_pages, p.max_pages, j) : -1;
+    };
+    int pg = pages();
+    for (uint32_t n = 0; live; ++n) {
+      if (!warp_wait(bar(kRBarEmpty + s), (n & 1u) ^ 1u, budget, status)) break;
+      const int item = idx % F::kItems;
+      const uint32_t j0 = uint32_t(g.t0 + idx / F::kItems) * kTreeTile;
+      const int left = int(min(uint32_t(kTreeTile), g.s.keys - j0));
+      const bool is_v = item >= F::kItems / 2;
+      const char* pool = (is_v ? p.c.v : p.c.k) + int64_t(g.h) * p.c.sh * kEs;
+      if (kFp8 || !is_v) {
+        // 256 bytes of each of 128 keys, two keys to an instruction
+        const int unit = lane & 15, odd = lane >> 4;
+        const char* lane_src = pool + (kFp8 ? 0 : item * 256) + unit * 16 + odd * row_bytes;
+        const uint32_t dst0 = slot + uint32_t(unit >> 3) * kChunk;
+#pragma unroll 2
+        for (int grp = 0; grp < 16; ++grp) {
+          const int page = __shfl_sync(0xffffffffu, pg, grp);
+          const char* src = lane_src + (int64_t(page) * p.c.sp + ((j0 + grp * 8) & slot_mask) * p.c.st) * kEs;
+          const int rows = page < 0 ? 0 : left - grp * 8;
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const int r = 2 * i + odd;
+            const bool there = r < rows;
+            cp_async16(dst0 + uint32_t(grp * 8 + r) * 128u + uint32_t(((unit & 7) ^ r) << 4),
+                       there ? src + 2 * i * row_bytes : pool, there ? 16u : 0u);
+          }
+        }
+      } else {
+        // 512 bytes of each of 64 keys, one key to an instruction
+        const int k0 = (item & 1) * 8;  // first group
+        const uint32_t dst0 = slot + uint32_t(lane >> 3) * (kSlotBytes / 4);
+        const char* lane_src = pool + lane * 16;
+#pragma unroll 1
+        for (int grp = 0; grp < 8; ++grp) {
+          const int page = __shfl_sync(0xffffffffu, pg, k0 + grp);
+          const char* src = lane_src + (int64_t(page) * p.c.sp + ((j0 + (k0 + grp) * 8) & slot_mask) * p.c.st) * kEs;
+          const int rows = page < 0 ? 0 : left - (k0 + grp) * 8;
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            const bool there = i < rows;
+            cp_async16(dst0 + uint32_t(grp * 8 + i) * 128u + uint32_t(((lane & 7) ^ i) << 4),
+                       there ? src + i * row_bytes : pool, there ? 16u : 0u);
+          }
+        }
+      }
+      idx += F::kSlots;
+      pg = pages();  // the next item's, while this one's copies are under way
+      asm volatile("cp.async.wait_all;" ::: "memory");
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar(kRBarFull + s));
+    }
+    asm volatile("cp.async.wait_all;" ::: "memory");
+  } else if (warp >= F::kIssuer) {
+    // ---------------------------------------------------------------- MMA issuers
+    if (lane == 0) {
+      const bool is_s = warp == F::kIssuer;
+      constexpr uint32_t id_s = idesc<kFp8>(128, 0, 0), id_o = idesc<kFp8>(256, 0, 1);
+      const uint64_t dq = umma::smem_desc(sQ, 16, 1024);
+      uint32_t tt = 0, segs = 0;  // tiles issued
+      bool ok = true;
+      while (ok && tree_next(p, cur, &g)) {
+        if (is_s && !(ok = mbar_wait_inline(bar(kRBarQ), segs & 1u, budget, status))) break;
+        ++segs;
+        for (int tile = g.t0; ok && tile < g.t1; ++tile, ++tt) {
+          const uint32_t b = tt & 1u, ph = (tt >> 1) & 1u;
+          // O += P(t - 2) V has read what S(t) overwrites; P(t) is there.
+          if (is_s)
+            ok = tt < 2 || mbar_wait_inline(bar(kRBarPV + int(b)), ph ^ 1u, budget, status);
+          else
+            ok = mbar_wait_inline(bar(kRBarP + int(b)), ph, budget, status);
+          const uint32_t first = tt * F::kItems + (is_s ? 0 : F::kItems / 2);
+          const uint32_t sbuf = tmem + 256u + b * 128u;
+#pragma unroll
+          for (int part = 0; part < F::kItems / 2; ++part) {
+            const uint32_t item = first + part, slot = item % F::kSlots;
+            ok = ok && mbar_wait_inline(bar(kRBarFull + int(slot)), (item / F::kSlots) & 1u, budget, status);
+            if (!ok) break;
+            umma::fence_after_sync();
+            const uint32_t base = sRing + slot * uint32_t(kSlotBytes);
+            if (is_s) {
+              const uint64_t dk = umma::smem_desc(base, 16, 1024);
+#pragma unroll
+              for (int k = 0; k < 8; ++k) {
+                const uint32_t a = uint32_t(k >> 2) * kChunk + uint32_t(k & 3) * 32u;
+#pragma unroll
+                for (int piece = 0; piece < (kFp8 ? 2 : 1); ++piece)
+                  mma<kFp8>(sbuf, umma::desc_add(dq, a + uint32_t(kFp8 ? piece : part) * (2 * kChunk)),
+                            umma::desc_add(dk, a), id_s, (part | k | piece) != 0);
+              }
+            } else {
+              const uint64_t dv = umma::smem_desc(base, kFp8 ? kChunk : kSlotBytes / 4, 1024);
+#pragma unroll
+              for (int k = 0; k < 4; ++k) {
+#pragma unroll
+                for (int piece = 0; piece < (kFp8 ? 2 : 1); ++piece)
+                  mma_ts<kFp8>(tmem, sbuf + uint32_t(kFp8 ? 32 * piece : 32 * part) + 8u * uint32_t(k),
+                               umma::desc_add(dv, uint32_t(k) * (kFp8 ? 4096u : 2048u)), id_o,
+                               tile > g.t0 || (part | k | piece) != 0);
+              }
+            }
+            umma::commit(bar(kRBarEmpty + int(slot)));
+          }
+          if (ok) umma::commit(bar((is_s ? kRBarS : kRBarPV) + int(b)));
+        }
+      }
+      // Every product complete before TMEM is released.
+      if (tt > 0)
+        umma::commit(bar(kRBarDrain));
+      else
+        mbar_arrive(bar(kRBarDrain));
+      mbar_wait_inline(bar(kRBarDrain), 0, budget, status);
+    }
+    __syncwarp();
+  } else {
+    // ---------------------------------------------------------------- softmax
+    constexpr uint32_t kAll = 32 * kSoftWarps;  // threads of barrier 15
+    const int quarter = warp & 3, part = warp >> 2;
+    const uint32_t quarter_bar = 1u + uint32_t(quarter);  // the four parts of a lane quarter
+    const int r = quarter * 32 + lane;                    // row of the tile = TMEM lane
+    const uint32_t lane_addr = tmem + (uint32_t(quarter * 32) << 16);
+    const int g_shift = __ffs(p.G) - 1;
+    const int row = rt * kRows + r, t = row >> g_shift;
+    const bool mine = row < p.T * p.G;
+    const uint32_t slot_mask = (1u << p.c.page_shift) - 1;
+    float* sh_f = reinterpret_cast<float*>(smem_raw + F::kOffF);
+    float* sh_scale = reinterpret_cast<float*>(smem_raw + F::kOffScale) + warp * 96;
+    // One value per part and row.
+    float* sh_red = reinterpret_cast<float*>(smem_raw + F::kOffRed);
+    auto red = [&](int q) -> float& { return sh_red[q * kRows + r]; };
+    uint32_t tt = 0;
+    bool ok = true;
+
+    while (ok && tree_next(p, cur, &g)) {
+      const int32_t* table = p.table + int64_t(g.b) * p.max_pages;
+      // Q of this head, eight rows per warp, four loads in flight.
+#pragma unroll 1
+      for (int r0 = warp; r0 < kRows; r0 += 4 * kSoftWarps) {
+        uint4 u[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int n = rt * kRows + r0 + i * kSoftWarps, tq = n >> g_shift;
+          u[i] = make_uint4(0, 0, 0, 0);
+          if (tq < g.s.drafted)
+            u[i] = *reinterpret_cast<const uint4*>(reinterpret_cast<const __nv_bfloat16*>(p.q.p) + g.b * p.q.sb +
+                                                   int64_t(g.h * p.G + (n & (p.G - 1))) * p.q.sh + tq * p.q.sl + 8 * lane);
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int rq = r0 + i * kSoftWarps;
+          if constexpr (!kFp8) {
+            sts16(sQ + uint32_t(lane >> 3) * kChunk + uint32_t(rq) * 128u + uint32_t(((lane & 7) ^ (rq & 7)) << 4), u[i]);
+          } else {
+            const float f = put_query<kRows, false>(u[i], sQ, rq);
+            if (lane == 0) sh_f[rq] = f * p.scale_log2;
+          }
+        }
+      }
+      if (warp == 0) sh_bad[lane] = 0;
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar(kRBarQ));
+      sync_threads(15, kAll);  // sh_f and sh_bad are other warps' too
+      const float factor = kFp8 ? sh_f[r] : p.scale_log2;
+      const bool live = t < g.s.drafted;
+
+      // Lane i looks after key 32 part + i of each tile: its page two tiles ahead of its use,
+      // its scales one tile ahead.
+      const int key = part * 32 + lane;
+      auto page_at = [&](int tile) {
+        const uint32_t j = uint32_t(tile) * kTreeTile + key;
+        return tile < g.t1 && j < g.s.keys ? page_of(p.c, table, p.max_pages, j) : -1;
+      };
+      int page = page_at(g.t0), page_next = page_at(g.t0 + 1);
+      float ks_next = 0.f, vs_next = 1.f;
+      auto scales_at = [&](int tile) {
+        if (kFp8 && page >= 0) {
+          const int64_t at =
+              (int64_t(page) * p.c.Hkv + g.h) * (slot_mask + 1) + ((uint32_t(tile) * kTreeTile + key) & slot_mask);
+          ks_next = p.c.ks[at];
+          vs_next = p.c.vs[at];
+        }
+      };
+      scales_at(g.t0);
+
+      float m = kNoMax, l = 0.f;  // this row's maximum (the same in all parts), this part's share of its sum
+      for (int tile = g.t0; tile < g.t1; ++tile, ++tt) {
+        const uint32_t sb = tt & 1u, ph = (tt >> 1) & 1u;
+        const uint32_t j0 = uint32_t(tile) * kTreeTile + part * 32;
+        const uint32_t v_item = tt * F::kItems + F::kItems / 2;  // this tile's values in the ring
+        const int page_now = page;
+        const float ks = ks_next;
+        float vs = kFp8 && page_now >= 0 ? vs_next : 1.f;
+        page = page_next;
+        scales_at(tile + 1);
+        page_next = page_at(tile + 2);
+        bool fine = ok;
+        // The values of keys k of the tile: 16-byte unit c, in any order.
+        auto value_there = [&](int k) {
+          const uint32_t it = v_item + (kFp8 ? 0 : uint32_t(k >> 6));
+          return warp_wait(bar(kRBarFull + int(it % F::kSlots)), (it / F::kSlots) & 1u, budget, status);
+        };
+        auto value_unit = [&](int k, int c) {
+          const uint32_t it = v_item + (kFp8 ? 0 : uint32_t(k >> 6));
+          const uint32_t base = sRing + (it % F::kSlots) * uint32_t(kSlotBytes);
+          return base + uint32_t(c >> 3) * (kFp8 ? kChunk : kSlotBytes / 4) + uint32_t(kFp8 ? k : k & 63) * 128u +
+                 uint32_t(((c ^ k) & 7) << 4);
+        };
+        // Which of the 32 keys are there, and which this row sees.
+        uint32_t vis = __ballot_sync(0xffffffffu, page_now >= 0);
+        const bool drafted_tile = j0 + 32 > g.s.ctx && vis != 0;
+        if (drafted_tile && live) {
+#pragma unroll 8
+          for (int i = 0; i < 32; ++i)
+            if (j0 + i >= g.s.ctx && ((vis >> i) & 1u) && !tree_sees(p, g.b, t, int(j0 + i - g.s.ctx))) vis &= ~(1u << i);
+        }
+        const bool masked = __any_sync(0xffffffffu, vis != 0xffffffffu);
+        if constexpr (kFp8) {
+          // A row of zeros (written with scale 1): see tree_tc.cu.
+          if (__any_sync(0xffffffffu, page_now >= 0 && vs == 1.f)) {
+            fine = value_there(key) && fine;
+            uint32_t any = 0;
+            if (fine && vs == 1.f)
+#pragma unroll 4
+              for (int c = 0; c < 16; ++c) {
+                const uint4 v = lds16(value_unit(key, c));
+                any |= (v.x | v.y | v.z | v.w) & 0x7f7f7f7fu;
+              }
+            if (vs == 1.f && any == 0) vs = 0.f;
+            __syncwarp();
+          }
+          if (vs == 0.f) vs = 7.8886090522101181e-31f;  // 2^-100
+          sh_scale[lane] = page_now >= 0 ? ks : 0.f;
+          sh_scale[32 + lane] = page_now >= 0 ? log2f(vs) : 0.f;
+          sh_scale[64 + lane] = 1.f / vs;
+          __syncwarp();
+        }
+        // Values that some row must not see and that are not finite are cleared in the tile and
+        // added at the end (tree_tc.cu).  Quarter 0's warps look after the 128 keys.
+        if (p.T > 1 && quarter == 0 && drafted_tile) {
+          fine = value_there(part * 32) && fine;
+          if (fine && page_now >= 0 && j0 + lane >= g.s.ctx) {
+            uint32_t bad = 0;
+#pragma unroll 1
+            for (int c = 0; c < (kFp8 ? 16 : 32); ++c) {
+              const uint4 v = lds16(value_unit(key, c));
+              uint32_t w[4] = {v.x, v.y, v.z, v.w}, hit = 0;
+#pragma unroll
+              for (int k = 0; k < 4; ++k) {
+                const uint32_t x = kFp8 ? __vcmpeq4(w[k] & 0x7f7f7f7fu, 0x7f7f7f7fu)
+                                        : __vcmpeq2(w[k] & 0x7f807f80u, 0x7f807f80u);
+                hit |= x;
+                w[k] &= ~x;
+              }
+              if (hit) sts16(value_unit(key, c), make_uint4(w[0], w[1], w[2], w[3]));
+              bad |= hit;
+            }
+            const int u = int(j0 + lane - g.s.ctx);
+            if (bad) atomicOr(&sh_bad[u >> 5], 1u << (u & 31));
+          }
+          fence_proxy_async_smem();
+          __syncwarp();
+        }
+        fine = warp_wait(bar(kRBarS + int(sb)), ph, budget, status) && fine;
+        umma::fence_after_sync();
+        float x[32];
+        umma::tmem_ld32(lane_addr + 256u + sb * 128u + uint32_t(part * 32), x);
+        umma::tmem_wait_ld();
+#pragma unroll
+        for (int i = 0; i < 32; i += 4) {
+          if constexpr (kFp8) {
+            const float4 k4 = *reinterpret_cast<const float4*>(sh_scale + i);
+            const float4 l4 = *reinterpret_cast<const float4*>(sh_scale + 32 + i);
+            x[i] = fmaf(x[i] * factor, k4.x, l4.x);
+            x[i + 1] = fmaf(x[i + 1] * factor, k4.y, l4.y);
+            x[i + 2] = fmaf(x[i + 2] * factor, k4.z, l4.z);
+            x[i + 3] = fmaf(x[i + 3] * factor, k4.w, l4.w);
+          } else {
+#pragma unroll
+            for (int k = 0; k < 4; ++k) x[i + k] *= factor;
+          }
+        }
+        if (masked) {
+#pragma unroll
+          for (int i = 0; i < 32; ++i)
+            if (!((vis >> i) & 1u)) x[i] = -INFINITY;
+        }
+        float top[4] = {x[0], x[1], x[2], x[3]};
+#pragma unroll
+        for (int i = 4; i < 32; ++i) top[i & 3] = fmaxf(top[i & 3], x[i]);
+        const float mx = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
+        // The barrier also tells that all four parts have read S, whose place P takes.
+        if (any_thread(quarter_bar, 128, mx > m + F::kSlack || !fine)) {
+          red(part) = mx;
+          if (any_thread(quarter_bar, 128, !fine)) {
+            ok = false;
+            break;
+          }
+          const float all = fmaxf(fmaxf(red(0), red(1)), fmaxf(red(2), red(3)));
+          const bool up = all > m + F::kSlack;
+          const float alpha = up ? ex2(m - all) : 1.f;
+          if (up) m = all;
+          l *= alpha;
+          if (tile > g.t0 && __any_sync(0xffffffffu, up)) {
+            // O holds tiles up to the last one: complete before it is rescaled.
+            ok = warp_wait(bar(kRBarPV + int((tt - 1) & 1u)), ((tt - 1) >> 1) & 1u, budget, status) && ok;
+            umma::fence_after_sync();
+            if (ok) {
+#pragma unroll 1
+              for (int c0 = part * 64; c0 < part * 64 + 64; c0 += 16) {
+                float o[16];
+                umma::tmem_ld16(lane_addr + uint32_t(c0), o);
+                umma::tmem_wait_ld();
+                uint32_t w[16];
+#pragma unroll
+                for (int i = 0; i < 16; ++i) w[i] = __float_as_uint(o[i] * alpha);
+                umma::tmem_st16u(lane_addr + uint32_t(c0), w);
+              }
+            }
+          }
+          sync_threads(quarter_bar, 128);  // the exchange is read
+        }
+        // P and the row's sum.
+        if constexpr (kFp8) {
+          uint32_t hi[8], lo[8];
+#pragma unroll
+          for (int i = 0; i < 32; i += 4) {
+            const float4 inv = *reinterpret_cast<const float4*>(sh_scale + 64 + i);
+            float e[4], h[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) e[k] = ex2(x[i + k] - m);
+            l = fmaf(e[0], inv.x, fmaf(e[1], inv.y, fmaf(e[2], inv.z, fmaf(e[3], inv.w, l))));
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              e[k] *= kPScale;
+              h[k] = __uint_as_float(__float_as_uint(e[k]) & 0xfff00000u);  // three mantissa bits
+              e[k] -= h[k];
+            }
+            hi[i / 4] = e4m3_encode4(h);
+            lo[i / 4] = e4m3_encode4(e);
+          }
+          tmem_st8u(lane_addr + 256u + sb * 128u + uint32_t(part * 8), hi);
+          tmem_st8u(lane_addr + 256u + sb * 128u + 32u + uint32_t(part * 8), lo);
+          __syncwarp();  // sh_scale is read
+        } else {
+          uint32_t pk[16];
+          float sum[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+          for (int i = 0; i < 32; i += 2) {
+            const float a = ex2(x[i] - m), b = ex2(x[i + 1] - m);
+            sum[(i >> 1) & 3] += a + b;
+            pk[i / 2] = pack_bf16x2(a, b);
+          }
+          l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+          umma::tmem_st16u(lane_addr + 256u + sb * 128u + uint32_t(part * 16), pk);
+        }
+        umma::tmem_wait_st();
+        umma::fence_before_sync();
+        __syncwarp();
+        if (lane == 0 && ok) mbar_arrive(bar(kRBarP + int(sb)));
+      }
+      // ------------------------------------------------------------ the segment's result
+      const uint32_t last = tt - 1;
+      if (ok) ok = warp_wait(bar(kRBarPV + int(last & 1u)), (last >> 1) & 1u, budget, status);
+      umma::fence_after_sync();
+      ok = !any_thread(15, kAll, !ok);
+      if (ok) {
+        red(part) = l;
+        sync_threads(quarter_bar, 128);
+        const float sum = (red(0) + red(1)) + (red(2) + red(3));
+        const bool none = !live || sum == 0.f;
+        const float inv = none ? 0.f : (kFp8 ? 1.f / kPScale : 1.f) / sum;
+        const float lse = none ? -INFINITY : (m + log2f(sum)) * kLn2;
+        const bool whole = g.whole();
+        const int64_t part_row = ((int64_t(worker) * 2 + g.slot()) * p.row_tiles + rt) * kRows + r;
+        const int64_t out_row =
+            ((int64_t(g.b) * p.c.Hkv + g.h) * p.G + (row & (p.G - 1))) * int64_t(p.T) + t;
+        if (mine && part == 0) {
+          if (whole)
+            p.lse[out_row] = lse;
+          else
+            p.lse_part[part_row] = lse;
+        }
+        const bool bad = __any_sync(0xffffffffu, sh_bad[lane] != 0);
+#pragma unroll 1
+        for (int c0 = part * 64; c0 < part * 64 + 64; c0 += 16) {
+          float o[16];
+          umma::tmem_ld16(lane_addr + uint32_t(c0), o);
+          umma::tmem_wait_ld();
+#pragma unroll
+          for (int i = 0; i < 16; ++i) {
+            o[i] = none ? 0.f : o[i] * inv;
+            if (bad && !none) o[i] += hidden_values<kFp8>(p, g, table, sh_bad, t, c0 + i);
+          }
+          if (mine && whole) {
+            __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(p.out) + out_row * kHeadDim + c0;
+            store8(dst, o);
+            store8(dst + 8, o + 8);
+          } else if (mine) {
+            float* dst = p.o_part + part_row * kHeadDim + c0;
+            store8(dst, o);
+            store8(dst + 8, o + 8);
+          }
+        }
+        umma::fence_before_sync();
+      }
+      // The next segment's Q and factors take this one's place: all warps are done.
+      ok = !any_thread(15, kAll, !ok);
+    }
+  }
+  umma::fence_before_sync();
+  __syncthreads();
+  if (warp == F::kIssuer) {
+    umma::fence_after_sync();
+    umma::tmem_dealloc(tmem, 512);
+  }
+}
+
+template <bool kFp8>
+int launch(const TreeParams& p, cudaStream_t stream) {
+  using F = RowsCfg<kFp8>;
+  if (cudaFuncSetAttribute(tree_rows_kernel<kFp8>, cudaFuncAttributeMaxDynamicSharedMemorySize, F::kSmem) != cudaSuccess)
+    return GQA_ERR_LAUNCH;
+  tree_rows_kernel<kFp8><<<unsigned(p.workers) * unsigned(p.row_tiles), F::kThreads, F::kSmem, stream>>>(p);
+  return cudaGetLastError() == cudaSuccess ? GQA_OK : GQA_ERR_LAUNCH;
+}
+
+}  // namespace
+
+int launch_tree_rows(const TreeParams& p, cudaStream_t stream) {
+  return p.c.dtype == GQA_E4M3 ? launch<true>(p, stream) : launch<false>(p, stream);
+}
+
+}  // namespace gqa

@@ -2,17 +2,17 @@
 // (tcgen05 / TMEM), sm_100a: bf16 queries, bf16 or e4m3 pages.
 //
 // Few query rows meet many keys, so the keys take the long side of every product: a tile
-// of 128 keys is the M of S^T = K Q^T (N = the query rows, 16 .. 128), and the 256 columns
+// of 128 keys is the M of S^T = K Q^T (N = the query rows, 16 .. 64), and the 256 columns
 // of the values, in two halves, are the M of O^T += V^T P^T.  With the rows as M, 4 rows
-// would cost what 128 do.  TMEM, per CTA: two S^T buffers of N columns (lane = key) and the
+// would cost what 128 do (tree_rows.cu, for more rows).  TMEM, per CTA: two S^T buffers of N columns (lane = key) and the
 // two halves of O^T (lane = column of the output), 4 N columns in all.
 //
 // e4m3 pages are multiplied as they are (kind::f8f6f4, exact products in fp32): the query
 // is scaled by a power of two so that its largest element lies in (224, 448] and taken
 // apart into two e4m3 pieces, q = hi + lo, off by at most 2^-10 of that scale; so is each
-// probability.  Up to 64 rows the pieces lie side by side in N and their products are added
-// afterwards; above, two instructions add them into one accumulator.  The scales of a key
-// go into its scores, those of a value into its probability, before that is rounded.
+// probability.  The pieces lie side by side in N and their products are added afterwards.
+// The scales of a key go into its scores, those of a value into its probability, before
+// that is rounded.
 //
 // Softmax: one thread per key and up to 32 rows; the running maximum m of a row is raised
 // only when a score passes it by kSlack (in powers of two), so most tiles need no
@@ -25,29 +25,21 @@
 // Warps: 4 softmax warps per 32 (or 16) rows, one producer warp per 32 KiB slot of the
 // ring (cp.async, 16 bytes at a time, through the page table; two rows to an
 // instruction), and two warps whose first lanes issue the products.
-#include "internal.h"
-#include "tcgen05.cuh"
-#include "tree.cuh"
+#include "tree_tc.cuh"
 
 namespace gqa {
 namespace {
-
-constexpr int kSlotBytes = 32768;  // 128 keys x 256 bytes: half of a bf16 tile, a whole e4m3 one
-constexpr int kChunk = 16384;      // 128 keys x 128 bytes, one swizzled column block
-constexpr float kNoMax = -1e30f;   // a row's maximum before its first visible key
 
 template <int kN, bool kFp8>
 struct Cfg {
   static constexpr int kCols = kN < 32 ? kN : 32;  // rows of a softmax thread
   static constexpr int kParts = kN / kCols;
   static constexpr int kSoftWarps = 4 * kParts;
-  static constexpr bool kWide = kFp8 && kN <= 64;           // both pieces side by side in one product's N
-  static constexpr int kNN = kWide ? 2 * kN : kN;           // N of a product
-  static constexpr int kPieces = kFp8 && !kWide ? 2 : 1;    // products per step
+  static constexpr int kNN = kFp8 ? 2 * kN : kN;            // N of a product: e4m3 pieces lie side by side
   static constexpr int kItems = kFp8 ? 2 : 4;               // slots of a tile
   static constexpr int kQBytes = kN * 512;                  // bf16, or two e4m3 pieces
-  static constexpr int kPBytes = kN > 64 ? 2 * kChunk : kChunk;
-  static constexpr int kSlots = kN > 64 ? 4 : kN > 32 ? 5 : 6;  // what shared memory has room for
+  static constexpr int kPBytes = kChunk;
+  static constexpr int kSlots = kN > 32 ? 5 : 6;  // what shared memory has room for
   static constexpr int kIssuer = kSoftWarps + kSlots;           // the S issuer's warp; the O issuer's is the next
   static constexpr int kWarps = kIssuer + 2;
   static constexpr int kThreads = 32 * kWarps;
@@ -63,76 +55,8 @@ struct Cfg {
   static constexpr uint32_t kTmem = 4 * kNN;
   static_assert(kSmem <= 232448 - 1024, "shared memory per block");
 };
-constexpr float kPScale = 16.f;  // e4m3 probabilities are stored times this: 2^4 above the maximum is 256
-
 // Barriers: S^T, its release, P and O per parity of the tile; the ring's slots.
 enum { kBarQ = 0, kBarS = 1, kBarSFree = 3, kBarP = 5, kBarPV = 7, kBarDrain = 9, kBarFull = 10, kBarEmpty = 16 };
-
-__device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, int64_t budget, int32_t* status) {
-  return __all_sync(0xffffffffu, mbar_wait_inline(bar, parity, budget, status));
-}
-
-// Barriers over `n` threads, and the OR of `pred` over them: all take the same branch.
-__device__ __forceinline__ void sync_threads(uint32_t id, uint32_t n) {
-  asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(n) : "memory");
-}
-__device__ __forceinline__ bool any_thread(uint32_t id, uint32_t n, bool pred) {
-  uint32_t out;
-  asm volatile(
-      "{\n\t.reg .pred p, q;\n\t"
-      "setp.ne.u32 p, %1, 0;\n\t"
-      "bar.red.or.pred q, %2, %3, p;\n\t"
-      "selp.u32 %0, 1, 0, q;\n\t}"
-      : "=r"(out)
-      : "r"(uint32_t(pred)), "r"(id), "r"(n)
-      : "memory");
-  return out != 0;
-}
-
-__device__ __forceinline__ float ex2(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
-
-__device__ __forceinline__ uint32_t pack_bf16x2(float lo, float hi) {
-  __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
-  return *reinterpret_cast<uint32_t*>(&h);
-}
-
-__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, uint32_t bytes) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
-}
-
-__device__ __forceinline__ void sts16(uint32_t a, uint4 v) {
-  asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(a), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
-}
-__device__ __forceinline__ uint4 lds16(uint32_t a) {
-  uint4 v;
-  asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a) : "memory");
-  return v;
-}
-
-// D[tmem] (+)= A[smem] B[smem]^T in the type of the pages.
-template <bool kFp8>
-__device__ __forceinline__ void mma(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool add) {
-  if constexpr (kFp8)
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "setp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}\n" ::"r"(d),
-        "l"(a), "l"(b), "r"(idesc), "r"(uint32_t(add)));
-  else
-    umma::mma_ss(d, a, b, idesc, add);
-}
-
-// Instruction descriptor: fp32 accumulator, M = 128; e4m3 is format 0 of kind::f8f6f4, bf16
-// format 1 of kind::f16.
-template <bool kFp8>
-__host__ __device__ constexpr uint32_t idesc(int N, int a_mn, int b_mn) {
-  return (1u << 4) | (kFp8 ? 0u : (1u << 7) | (1u << 10)) | (uint32_t(a_mn) << 15) | (uint32_t(b_mn) << 16) |
-         (uint32_t(N >> 3) << 17) | (8u << 24);
-}
 
 // Sum or maximum over the 32 lanes of each of 16 values: lane l ends with value l / 2.  A
 // lane sends the half that it does not keep.
@@ -152,62 +76,6 @@ __device__ __forceinline__ float lanes_reduce(float (&v)[16]) {
   }
   const float got = __shfl_xor_sync(0xffffffffu, v[0], 1);
   return kMax ? fmaxf(v[0], got) : v[0] + got;
-}
-
-// What the cleared elements of column d (drafted values that are not finite) add to a row of
-// token t: an infinity or NaN for each that the row sees.
-template <bool kFp8>
-__device__ __noinline__ float hidden_values(const TreeParams& p, const TreeSegment& g, const int32_t* table,
-                                            const uint32_t* bad, int t, int d) {
-  float sum = 0.f;
-  for (int u = 0; u < g.s.drafted; ++u) {
-    if (!((bad[u >> 5] >> (u & 31)) & 1u) || !tree_sees(p, g.b, t, u)) continue;
-    const uint32_t j = g.s.ctx + u, slot = j & ((1u << p.c.page_shift) - 1);
-    const int64_t at = table[j >> p.c.page_shift] * p.c.sp + g.h * p.c.sh + slot * p.c.st + d;
-    if constexpr (kFp8) {
-      if ((uint8_t(p.c.v[at]) & 0x7f) == 0x7f) sum = __uint_as_float(0x7fc00000u);
-    } else {
-      const float y = __bfloat162float(reinterpret_cast<const __nv_bfloat16*>(p.c.v)[at]);
-      if (!(fabsf(y) < INFINITY)) sum += y;
-    }
-  }
-  return sum;
-}
-
-// One warp: row r of an e4m3 Q operand, both pieces of the row's eight columns per lane.
-// Returns the row's scale, NaN for a row with an infinity or a NaN: it has no finite score.
-template <int kN, bool kWide>
-__device__ __forceinline__ float put_query(uint4 u, uint32_t sQ, int r) {
-  const int lane = threadIdx.x & 31;
-  float x[8], lo[8];
-  unpack8(u, x);
-  float amax = 0.f;
-  bool finite = true;
-#pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    amax = fmaxf(amax, fabsf(x[i]));
-    finite = finite && fabsf(x[i]) < INFINITY;
-  }
-#pragma unroll
-  for (int o = 16; o >= 1; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
-  finite = __all_sync(0xffffffffu, finite);
-  const float scale = e4m3_row_scale(finite ? amax : 0.f);
-  const float inv = __uint_as_float((254u << 23) - __float_as_uint(scale));
-#pragma unroll
-  for (int i = 0; i < 8; ++i) x[i] *= inv;
-  const uint32_t h0 = e4m3_encode4(x), h1 = e4m3_encode4(x + 4);
-  e4m3_decode4(h0, lo);
-  e4m3_decode4(h1, lo + 4);
-#pragma unroll
-  for (int i = 0; i < 8; ++i) lo[i] = x[i] - lo[i];
-  constexpr uint32_t kBlock = (kWide ? 2 * kN : kN) * 128u;
-  const uint32_t a = sQ + uint32_t(lane >> 4) * kBlock + uint32_t(r) * 128u +
-                     uint32_t((((lane & 15) >> 1) ^ (r & 7)) << 4) + uint32_t(lane & 1) * 8u;
-  constexpr uint32_t kLo = kWide ? kN * 128u : kN * 256u;  // kN is a multiple of 8: the same swizzle
-  asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(a), "r"(h0), "r"(h1) : "memory");
-  asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(a + kLo), "r"(e4m3_encode4(lo)), "r"(e4m3_encode4(lo + 4))
-               : "memory");
-  return finite ? scale : __uint_as_float(0x7fc00000u);
 }
 
 template <int kN, bool kFp8>
@@ -357,20 +225,15 @@ __global__ void __launch_bounds__(Cfg<kN, kFp8>::kThreads, 1) tree_tc_kernel(con
                 // 32-byte step k & 3 of column block k / 4
                 const uint32_t a = uint32_t(k >> 2) * kChunk + uint32_t(k & 3) * 32u;
                 const uint32_t q = uint32_t((kFp8 ? 0 : 2 * part) + (k >> 2)) * (F::kNN * 128u) + uint32_t(k & 3) * 32u;
-#pragma unroll
-                for (int piece = 0; piece < F::kPieces; ++piece)
-                  mma<kFp8>(tmem + b * F::kNN, umma::desc_add(dk, a), umma::desc_add(dq, q + uint32_t(piece) * (kN * 256u)),
-                            id_s, (part | k | piece) != 0);
+                mma<kFp8>(tmem + b * F::kNN, umma::desc_add(dk, a), umma::desc_add(dq, q), id_s, (part | k) != 0);
               }
             } else {
               const uint64_t dv = umma::smem_desc(base + (kFp8 ? uint32_t(part) * kChunk : 0u), kChunk, 1024);
 #pragma unroll
               for (int k = 0; k < kRowSteps; ++k) {
                 const uint32_t rows = uint32_t(k) * (kFp8 ? 4096u : 2048u);
-#pragma unroll
-                for (int piece = 0; piece < F::kPieces; ++piece)
-                  mma<kFp8>(tmem + uint32_t(2 + part) * F::kNN, umma::desc_add(dv, rows),
-                            umma::desc_add(dp, rows + uint32_t(piece) * kChunk), id_o, tile > g.t0 || (k | piece) != 0);
+                mma<kFp8>(tmem + uint32_t(2 + part) * F::kNN, umma::desc_add(dv, rows), umma::desc_add(dp, rows), id_o,
+                          tile > g.t0 || k != 0);
               }
             }
             if (!kFp8 || part == 1) umma::commit(bar(kBarEmpty + int(slot)));
@@ -400,9 +263,8 @@ __global__ void __launch_bounds__(Cfg<kN, kFp8>::kThreads, 1) tree_tc_kernel(con
     const uint32_t slot_mask = (1u << p.c.page_shift) - 1;
     // The 16-byte unit `i` of key k's P: eight or sixteen rows from n0 on, of a piece.
     auto p_unit = [&](int k, int i, int piece) {
-      const int un = (n0 + (F::kWide ? piece * kN : 0)) / (kFp8 ? 16 : 8) + i;
-      const uint32_t block = uint32_t(un >> 3) + (kFp8 && !F::kWide ? uint32_t(piece) : 0u);
-      return sP + block * kChunk + uint32_t(k) * 128u + uint32_t(((un & 7) ^ (k & 7)) << 4);
+      const int un = (n0 + piece * kN) / (kFp8 ? 16 : 8) + i;
+      return sP + uint32_t(k) * 128u + uint32_t((un ^ (k & 7)) << 4);
     };
     // The quarters' exchange of one value for each of sixteen rows lies in the thread's own
     // columns of P, which no product reads then: row c0 + n's from quarter q is with lane n.
@@ -439,7 +301,7 @@ __global__ void __launch_bounds__(Cfg<kN, kFp8>::kThreads, 1) tree_tc_kernel(con
             sts16(sQ + uint32_t(lane >> 3) * (kN * 128u) + uint32_t(r) * 128u + uint32_t(((lane & 7) ^ (r & 7)) << 4),
                   u[i]);
           } else {
-            const float f = put_query<kN, F::kWide>(u[i], sQ, r);
+            const float f = put_query<kN, true>(u[i], sQ, r);
             if (lane == 0) sh_f[r] = f * p.scale_log2;
           }
         }
@@ -567,7 +429,7 @@ __global__ void __launch_bounds__(Cfg<kN, kFp8>::kThreads, 1) tree_tc_kernel(con
           // Scores of the rows n0 + c0 .. + 15, in powers of two.
           auto scores = [&](float (&x)[16]) {
             umma::tmem_ld16(lane_addr + sb * F::kNN + uint32_t(c0), x);
-            if constexpr (F::kWide) {
+            if constexpr (kFp8) {
               float y[16];
               umma::tmem_ld16(lane_addr + sb * F::kNN + kN + uint32_t(c0), y);
               umma::tmem_wait_ld();
@@ -639,7 +501,7 @@ __global__ void __launch_bounds__(Cfg<kN, kFp8>::kThreads, 1) tree_tc_kernel(con
               for (int i = 0; i < 16; ++i) l[c0 + i] *= __shfl_sync(0xffffffffu, alpha, i);
               if (tile > g.t0) {
 #pragma unroll 1
-                for (int block = 0; block < (F::kWide ? 4 : 2); ++block) {  // halves of O, and pieces
+                for (int block = 0; block < (kFp8 ? 4 : 2); ++block) {  // halves of O, and pieces
                   float o[16];
                   const uint32_t a = lane_addr + uint32_t((2 + (block & 1)) * F::kNN + (block >> 1) * kN + c0);
                   umma::tmem_ld16(a, o);
@@ -746,7 +608,7 @@ __global__ void __launch_bounds__(Cfg<kN, kFp8>::kThreads, 1) tree_tc_kernel(con
             float o[16];
             const uint32_t a = lane_addr + uint32_t((2 + half) * F::kNN + c0);
             umma::tmem_ld16(a, o);
-            if constexpr (F::kWide) {
+            if constexpr (kFp8) {
               float y[16];
               umma::tmem_ld16(a + kN, y);
               umma::tmem_wait_ld();
@@ -805,14 +667,14 @@ int launch_type(const TreeParams& p, int rows, cudaStream_t stream) {
   switch (rows) {
     case 16: return launch_n<16, kFp8>(p, stream);
     case 32: return launch_n<32, kFp8>(p, stream);
-    case 64: return launch_n<64, kFp8>(p, stream);
-    default: return launch_n<128, kFp8>(p, stream);
+    default: return launch_n<64, kFp8>(p, stream);
   }
 }
 
 }  // namespace
 
 int launch_tree_tc(const TreeParams& p, int rows, cudaStream_t stream) {
+  if (rows > 64) return launch_tree_rows(p, stream);
   return p.c.dtype == GQA_E4M3 ? launch_type<true>(p, rows, stream) : launch_type<false>(p, rows, stream);
 }
 
