@@ -11,8 +11,8 @@
 // shared memory only when a maximum rises.  e4m3 pages, their scales, the pieces of queries
 // and probabilities, lazy maxima and values that a mask hides: as in tree_tc.cu.
 //
-// Warps: 16 for the softmax (lane quarter x 32 keys), one producer per 32 KiB slot, two
-// issuers.  A bf16 tile is four slots: the keys' columns 0 - 127 and 128 - 255 ([2][128
+// Warps: 16 for the softmax (lane quarter x 32 keys), a producer, one that fetches the keys'
+// scales, two issuers.  A bf16 tile is four slots: the keys' columns 0 - 127 and 128 - 255 ([2][128
 // keys][128 bytes]), then the values of keys 0 - 63 and 64 - 127 ([4][64 keys][128 bytes]),
 // so that one product spans all 256 columns; an e4m3 tile is two ([2][128 keys][128 bytes]).
 #include "tree_tc.cuh"
@@ -25,24 +25,39 @@ constexpr int kSoftWarps = 16;
 
 template <bool kFp8>
 struct RowsCfg {
-  static constexpr int kItems = kFp8 ? 2 : 4;
-  static constexpr int kSlots = kFp8 ? 4 : 5;  // what shared memory has room for
-  static constexpr int kIssuer = kSoftWarps + kSlots;
+  static constexpr int kPer = kFp8 ? 1 : 2;                        // slots of a tile's keys, and of its values
+  static constexpr int kKSlots = 2, kVSlots = kFp8 ? 2 : 3;        // what shared memory has room for
+  static constexpr int kIssuer = kSoftWarps + 2;                   // after the producer and the keys' warp: 20 warps
+                                                                   // leave 96 registers a thread, 21 only 80
   static constexpr int kThreads = 32 * (kIssuer + 2);
   static constexpr int kOffQ = 0;  // bf16 [4][128 rows][128 bytes], or e4m3 [2 pieces][2][128 rows][128 bytes]
-  static constexpr int kOffRing = kRows * 512;
-  static constexpr int kOffBar = kOffRing + kSlots * kSlotBytes;
-  static constexpr int kOffStart = kOffBar + 8 * 20;  // the worker's cursor, the TMEM address
+  static constexpr int kOffK = kRows * 512;
+  static constexpr int kOffV = kOffK + kKSlots * kSlotBytes;
+  static constexpr int kOffBar = kOffV + kVSlots * kSlotBytes;
+  static constexpr int kOffStart = kOffBar + 8 * 22;  // the worker's cursor, the TMEM address
   static constexpr int kOffBad = kOffStart + 48;      // 32 words: drafted tokens with a value that is not finite
-  static constexpr int kOffRed = kOffBad + 128 + 48;  // [4 parts][128 rows] exchange
+  static constexpr int kOffThere = kOffBad + 128;     // [2][4] words: which keys of the tile are there
+  static constexpr int kOffRed = kOffThere + 32;      // [4 parts][128 rows] exchange
   static constexpr int kOffF = kOffRed + 4 * kRows * 4;       // [128] factors of the rows' scores (e4m3)
-  static constexpr int kOffScale = kOffF + (kFp8 ? 512 : 0);  // [16 warps][3][32]: ks, log2 vs, 1 / vs (e4m3)
-  static constexpr int kSmem = kOffScale + (kFp8 ? kSoftWarps * 384 : 0);
+  static constexpr int kOffScale = kOffF + (kFp8 ? 512 : 0);  // [2][3][128]: ks, log2 vs, 1 / vs (e4m3)
+  static constexpr int kSmem = kOffScale + (kFp8 ? 2 * 3 * 128 * 4 : 0);
   static constexpr float kSlack = kFp8 ? 4.f : 8.f;
   static_assert(kSmem <= 232448 && kOffRed % 16 == 0 && sizeof(TreeCursor) <= 40, "shared memory per block");
 };
 
-enum { kRBarQ = 0, kRBarS = 1, kRBarP = 3, kRBarPV = 5, kRBarDrain = 7, kRBarFull = 8, kRBarEmpty = 14 };
+// Barriers: Q; S, P, O and the keys' scales per parity of the tile; the rings' slots.
+enum {
+  kRBarQ = 0,
+  kRBarS = 1,
+  kRBarP = 3,
+  kRBarPV = 5,
+  kRBarKeys = 7,
+  kRBarDrain = 9,
+  kRBarKFull = 10,
+  kRBarKEmpty = 13,
+  kRBarVFull = 16,
+  kRBarVEmpty = 19
+};
 
 // Eight consecutive 32-bit columns of raw words into this thread's TMEM lane.
 __device__ __forceinline__ void tmem_st8u(uint32_t taddr, const uint32_t (&r)[8]) {
@@ -52,16 +67,19 @@ __device__ __forceinline__ void tmem_st8u(uint32_t taddr, const uint32_t (&r)[8]
 }
 
 template <bool kFp8>
-__global__ void __launch_bounds__(RowsCfg<kFp8>::kThreads, 1) tree_rows_kernel(const __grid_constant__ TreeParams p) {
+__global__ void __launch_bounds__(RowsCfg<kFp8>::kThreads, 1) tree_rows_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v,
+                 const __grid_constant__ TreeParams p) {
   using F = RowsCfg<kFp8>;
   extern __shared__ __align__(1024) char smem_raw[];
   const uint32_t sbase = smem_u32(smem_raw);
   const bool misaligned = (sbase & 1023u) != 0;  // the swizzle needs it; never expected to fail
-  const uint32_t sQ = sbase + F::kOffQ, sRing = sbase + F::kOffRing;
+  const uint32_t sQ = sbase + F::kOffQ, sK = sbase + F::kOffK, sV = sbase + F::kOffV;
   auto bar = [&](int i) { return sbase + F::kOffBar + 8u * uint32_t(i); };
   TreeCursor& start = *reinterpret_cast<TreeCursor*>(smem_raw + F::kOffStart);
   volatile uint32_t& tmem_slot = *reinterpret_cast<uint32_t*>(smem_raw + F::kOffStart + 40);
   uint32_t* sh_bad = reinterpret_cast<uint32_t*>(smem_raw + F::kOffBad);
+  uint32_t* sh_there = reinterpret_cast<uint32_t*>(smem_raw + F::kOffThere);
+  float* sh_scale = reinterpret_cast<float*>(smem_raw + F::kOffScale);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int worker = blockIdx.x / p.row_tiles, rt = blockIdx.x % p.row_tiles;
   const int64_t budget = p.wait_budget_ns;
@@ -76,11 +94,16 @@ __global__ void __launch_bounds__(RowsCfg<kFp8>::kThreads, 1) tree_rows_kernel(c
         mbar_init(bar(kRBarS + i), 1);
         mbar_init(bar(kRBarP + i), kSoftWarps);
         mbar_init(bar(kRBarPV + i), 1);
+        mbar_init(bar(kRBarKeys + i), 1);
       }
       mbar_init(bar(kRBarDrain), 2);
-      for (int i = 0; i < F::kSlots; ++i) {
-        mbar_init(bar(kRBarFull + i), 1);
-        mbar_init(bar(kRBarEmpty + i), 1);
+      for (int i = 0; i < F::kKSlots; ++i) {
+        mbar_init(bar(kRBarKFull + i), 1);
+        mbar_init(bar(kRBarKEmpty + i), 1);
+      }
+      for (int i = 0; i < F::kVSlots; ++i) {
+        mbar_init(bar(kRBarVFull + i), 1);
+        mbar_init(bar(kRBarVEmpty + i), 1);
       }
       fence_barrier_init();
       if (misaligned) set_status(status, GQA_ERR_LAUNCH);
@@ -96,77 +119,98 @@ __global__ void __launch_bounds__(RowsCfg<kFp8>::kThreads, 1) tree_rows_kernel(c
 
   if (misaligned) {
     // no role
-  } else if (warp >= kSoftWarps && warp < F::kIssuer) {
-    // ---------------------------------------------------------------- producers
-    const int s = warp - kSoftWarps;
-    const uint32_t slot = sRing + uint32_t(s) * kSlotBytes;
-    constexpr int kEs = kFp8 ? 1 : 2;
+  } else if (warp == kSoftWarps) {
+    Feed<kFp8, false, F::kKSlots> k;
+    Feed<kFp8, !kFp8, F::kVSlots> v;
+    k.begin(p, cur, &map_k, sK, bar(kRBarKFull), bar(kRBarKEmpty));
+    v.begin(p, cur, &map_v, sV, bar(kRBarVFull), bar(kRBarVEmpty));
+    produce(p, k, v);
+  } else if (warp == kSoftWarps + 1) {
+    // ---------------------------------------------------------------- keys
+    // Lane i looks after keys i, 32 + i, 64 + i and 96 + i of each tile: which are there, and
+    // (e4m3) their scales, in two buffers.  Pages are loaded two tiles ahead, scales one.
     const uint32_t slot_mask = (1u << p.c.page_shift) - 1;
-    const int64_t row_bytes = p.c.st * kEs;
-    int idx = s;
-    bool live = tree_next(p, cur, &g);
-    // The page of each group of eight keys of this item's tile, in lanes 0 .. 15.
-    auto pages = [&]() {
-      while (live && idx >= (g.t1 - g.t0) * F::kItems) {
-        idx -= (g.t1 - g.t0) * F::kItems;
-        live = tree_next(p, cur, &g);
-      }
-      if (!live) return -1;
-      const uint32_t j = uint32_t(g.t0 + idx / F::kItems) * kTreeTile + lane * 8;
-      return lane < 16 && j < g.s.keys ? page_of(p.c, p.table + int64_t(g.b) * p.max_pages, p.max_pages, j) : -1;
-    };
-    int pg = pages();
-    for (uint32_t n = 0; live; ++n) {
-      if (!warp_wait(bar(kRBarEmpty + s), (n & 1u) ^ 1u, budget, status)) break;
-      const int item = idx % F::kItems;
-      const uint32_t j0 = uint32_t(g.t0 + idx / F::kItems) * kTreeTile;
-      const int left = int(min(uint32_t(kTreeTile), g.s.keys - j0));
-      const bool is_v = item >= F::kItems / 2;
-      const char* pool = (is_v ? p.c.v : p.c.k) + int64_t(g.h) * p.c.sh * kEs;
-      if (kFp8 || !is_v) {
-        // 256 bytes of each of 128 keys, two keys to an instruction
-        const int unit = lane & 15, odd = lane >> 4;
-        const char* lane_src = pool + (kFp8 ? 0 : item * 256) + unit * 16 + odd * row_bytes;
-        const uint32_t dst0 = slot + uint32_t(unit >> 3) * kChunk;
-#pragma unroll 2
-        for (int grp = 0; grp < 16; ++grp) {
-          const int page = __shfl_sync(0xffffffffu, pg, grp);
-          const char* src = lane_src + (int64_t(page) * p.c.sp + ((j0 + grp * 8) & slot_mask) * p.c.st) * kEs;
-          const int rows = page < 0 ? 0 : left - grp * 8;
+    uint32_t tt = 0;
+    bool ok = true;
+    while (ok && tree_next(p, cur, &g)) {
+      const int32_t* table = p.table + int64_t(g.b) * p.max_pages;
+      int page[4], page_next[4];
+      float ks[4], vs[4];
+      auto pages_at = [&](int tile, int (&pg)[4]) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const uint32_t j = uint32_t(tile) * kTreeTile + i * 32 + lane;
+          pg[i] = tile < g.t1 && j < g.s.keys ? page_of(p.c, table, p.max_pages, j) : -1;
+        }
+      };
+      auto scales_at = [&](int tile, const int (&pg)[4]) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          ks[i] = 0.f, vs[i] = 1.f;
+          if (kFp8 && pg[i] >= 0) {
+            const int64_t at = (int64_t(pg[i]) * p.c.Hkv + g.h) * (slot_mask + 1) +
+                               ((uint32_t(tile) * kTreeTile + i * 32 + lane) & slot_mask);
+            ks[i] = p.c.ks[at];
+            vs[i] = p.c.vs[at];
+          }
+        }
+      };
+      pages_at(g.t0, page);
+      pages_at(g.t0 + 1, page_next);
+      scales_at(g.t0, page);
+      for (int tile = g.t0; tile < g.t1; ++tile, ++tt) {
+        const uint32_t b = tt & 1u;
+        float k_now[4], v_now[4];
+        uint32_t there[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          k_now[i] = ks[i], v_now[i] = vs[i];
+          there[i] = __ballot_sync(0xffffffffu, page[i] >= 0);
+        }
+        const bool one = kFp8 && ((page[0] >= 0 && vs[0] == 1.f) || (page[1] >= 0 && vs[1] == 1.f) ||
+                                  (page[2] >= 0 && vs[2] == 1.f) || (page[3] >= 0 && vs[3] == 1.f));
+#pragma unroll
+        for (int i = 0; i < 4; ++i) page[i] = page_next[i];
+        scales_at(tile + 1, page);
+        pages_at(tile + 2, page_next);
+        // The softmax has read what the buffer held for tile t - 2.
+        if (tt >= 2) ok = warp_wait(bar(kRBarP + int(b)), ((tt - 2) >> 1) & 1u, budget, status);
+        if constexpr (kFp8) {
+          // A row of zeros (written with scale 1): see tree_tc.cu.
+          if (__any_sync(0xffffffffu, one)) {
+            // The product before is over first, so that the slot's barrier stands at no earlier use;
+            // and the one two before that, which the same barrier counts.
+            if (tt >= 3) ok = warp_wait(bar(kRBarPV + int((tt - 3) & 1u)), ((tt - 3) >> 1) & 1u, budget, status) && ok;
+            if (tt > 0) ok = warp_wait(bar(kRBarPV + int((tt - 1) & 1u)), ((tt - 1) >> 1) & 1u, budget, status) && ok;
+            ok = ok && warp_wait(bar(kRBarVFull + int(tt % F::kVSlots)), (tt / F::kVSlots) & 1u, budget, status);
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              if (ok && v_now[i] == 1.f && ((there[i] >> lane) & 1u)) {
+                uint32_t any = 0;
+                for (int c = 0; c < 16; ++c) {
+                  const uint4 v = lds16(sV + (tt % F::kVSlots) * uint32_t(kSlotBytes) + uint32_t(c >> 3) * kChunk +
+                                        uint32_t(i * 32 + lane) * 128u + uint32_t((c & 7) << 4));
+                  any |= (v.x | v.y | v.z | v.w) & 0x7f7f7f7fu;
+                }
+                if (any == 0) v_now[i] = 0.f;
+              }
+            __syncwarp();
+          }
+          float* sc = sh_scale + b * 384;
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
-            const int r = 2 * i + odd;
-            const bool there = r < rows;
-            cp_async16(dst0 + uint32_t(grp * 8 + r) * 128u + uint32_t(((unit & 7) ^ r) << 4),
-                       there ? src + 2 * i * row_bytes : pool, there ? 16u : 0u);
+            const float v = v_now[i] == 0.f ? 7.8886090522101181e-31f : v_now[i];  // 2^-100
+            sc[i * 32 + lane] = k_now[i];
+            sc[128 + i * 32 + lane] = log2f(v);
+            sc[256 + i * 32 + lane] = 1.f / v;
           }
         }
-      } else {
-        // 512 bytes of each of 64 keys, one key to an instruction
-        const int k0 = (item & 1) * 8;  // first group
-        const uint32_t dst0 = slot + uint32_t(lane >> 3) * (kSlotBytes / 4);
-        const char* lane_src = pool + lane * 16;
-#pragma unroll 1
-        for (int grp = 0; grp < 8; ++grp) {
-          const int page = __shfl_sync(0xffffffffu, pg, k0 + grp);
-          const char* src = lane_src + (int64_t(page) * p.c.sp + ((j0 + (k0 + grp) * 8) & slot_mask) * p.c.st) * kEs;
-          const int rows = page < 0 ? 0 : left - (k0 + grp) * 8;
-#pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            const bool there = i < rows;
-            cp_async16(dst0 + uint32_t(grp * 8 + i) * 128u + uint32_t(((lane & 7) ^ i) << 4),
-                       there ? src + i * row_bytes : pool, there ? 16u : 0u);
-          }
-        }
+        if (lane < 4) sh_there[b * 4 + lane] = lane == 0 ? there[0] : lane == 1 ? there[1] : lane == 2 ? there[2] : there[3];
+        __syncwarp();
+        if (!ok) break;
+        if (lane == 0) mbar_arrive(bar(kRBarKeys + int(b)));
       }
-      idx += F::kSlots;
-      pg = pages();  // the next item's, while this one's copies are under way
-      asm volatile("cp.async.wait_all;" ::: "memory");
-      fence_proxy_async_smem();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(bar(kRBarFull + s));
     }
-    asm volatile("cp.async.wait_all;" ::: "memory");
   } else if (warp >= F::kIssuer) {
     // ---------------------------------------------------------------- MMA issuers
     if (lane == 0) {
@@ -185,15 +229,16 @@ __global__ void __launch_bounds__(RowsCfg<kFp8>::kThreads, 1) tree_rows_kernel(c
             ok = tt < 2 || mbar_wait_inline(bar(kRBarPV + int(b)), ph ^ 1u, budget, status);
           else
             ok = mbar_wait_inline(bar(kRBarP + int(b)), ph, budget, status);
-          const uint32_t first = tt * F::kItems + (is_s ? 0 : F::kItems / 2);
+          const uint32_t slots = is_s ? F::kKSlots : F::kVSlots;
+          const uint32_t full = bar(is_s ? kRBarKFull : kRBarVFull), empty = bar(is_s ? kRBarKEmpty : kRBarVEmpty);
           const uint32_t sbuf = tmem + 256u + b * 128u;
 #pragma unroll
-          for (int part = 0; part < F::kItems / 2; ++part) {
-            const uint32_t item = first + part, slot = item % F::kSlots;
-            ok = ok && mbar_wait_inline(bar(kRBarFull + int(slot)), (item / F::kSlots) & 1u, budget, status);
+          for (int part = 0; part < F::kPer; ++part) {
+            const uint32_t item = F::kPer * tt + part, slot = item % slots;
+            ok = ok && mbar_wait_inline(full + 8u * slot, (item / slots) & 1u, budget, status);
             if (!ok) break;
             umma::fence_after_sync();
-            const uint32_t base = sRing + slot * uint32_t(kSlotBytes);
+            const uint32_t base = (is_s ? sK : sV) + slot * uint32_t(kSlotBytes);
             if (is_s) {
               const uint64_t dk = umma::smem_desc(base, 16, 1024);
 #pragma unroll
@@ -215,7 +260,7 @@ __global__ void __launch_bounds__(RowsCfg<kFp8>::kThreads, 1) tree_rows_kernel(c
                                tile > g.t0 || (part | k | piece) != 0);
               }
             }
-            umma::commit(bar(kRBarEmpty + int(slot)));
+            umma::commit(empty + 8u * slot);
           }
           if (ok) umma::commit(bar((is_s ? kRBarS : kRBarPV) + int(b)));
         }
@@ -238,9 +283,8 @@ __global__ void __launch_bounds__(RowsCfg<kFp8>::kThreads, 1) tree_rows_kernel(c
     const int g_shift = __ffs(p.G) - 1;
     const int row = rt * kRows + r, t = row >> g_shift;
     const bool mine = row < p.T * p.G;
-    const uint32_t slot_mask = (1u << p.c.page_shift) - 1;
+    const bool idle = rt * kRows + quarter * 32 >= p.T * p.G;  // no row in the whole quarter
     float* sh_f = reinterpret_cast<float*>(smem_raw + F::kOffF);
-    float* sh_scale = reinterpret_cast<float*>(smem_raw + F::kOffScale) + warp * 96;
     // One value per part and row.
     float* sh_red = reinterpret_cast<float*>(smem_raw + F::kOffRed);
     auto red = [&](int q) -> float& { return sh_red[q * kRows + r]; };
@@ -280,50 +324,35 @@ __global__ void __launch_bounds__(RowsCfg<kFp8>::kThreads, 1) tree_rows_kernel(c
       const float factor = kFp8 ? sh_f[r] : p.scale_log2;
       const bool live = t < g.s.drafted;
 
-      // Lane i looks after key 32 part + i of each tile: its page two tiles ahead of its use,
-      // its scales one tile ahead.
-      const int key = part * 32 + lane;
-      auto page_at = [&](int tile) {
-        const uint32_t j = uint32_t(tile) * kTreeTile + key;
-        return tile < g.t1 && j < g.s.keys ? page_of(p.c, table, p.max_pages, j) : -1;
-      };
-      int page = page_at(g.t0), page_next = page_at(g.t0 + 1);
-      float ks_next = 0.f, vs_next = 1.f;
-      auto scales_at = [&](int tile) {
-        if (kFp8 && page >= 0) {
-          const int64_t at =
-              (int64_t(page) * p.c.Hkv + g.h) * (slot_mask + 1) + ((uint32_t(tile) * kTreeTile + key) & slot_mask);
-          ks_next = p.c.ks[at];
-          vs_next = p.c.vs[at];
-        }
-      };
-      scales_at(g.t0);
-
+      const int key = part * 32 + lane;  // the key whose values this thread mends (quarter 0)
       float m = kNoMax, l = 0.f;  // this row's maximum (the same in all parts), this part's share of its sum
       for (int tile = g.t0; tile < g.t1; ++tile, ++tt) {
         const uint32_t sb = tt & 1u, ph = (tt >> 1) & 1u;
         const uint32_t j0 = uint32_t(tile) * kTreeTile + part * 32;
-        const uint32_t v_item = tt * F::kItems + F::kItems / 2;  // this tile's values in the ring
-        const int page_now = page;
-        const float ks = ks_next;
-        float vs = kFp8 && page_now >= 0 ? vs_next : 1.f;
-        page = page_next;
-        scales_at(tile + 1);
-        page_next = page_at(tile + 2);
         bool fine = ok;
-        // The values of keys k of the tile: 16-byte unit c, in any order.
+        // Key k's values are in their slot.  The product of the tile before is over first, so that
+        // the barrier stands at no earlier use of the slot.
         auto value_there = [&](int k) {
-          const uint32_t it = v_item + (kFp8 ? 0 : uint32_t(k >> 6));
-          return warp_wait(bar(kRBarFull + int(it % F::kSlots)), (it / F::kSlots) & 1u, budget, status);
+          if (tt > 0 && !warp_wait(bar(kRBarPV + int((tt - 1) & 1u)), ((tt - 1) >> 1) & 1u, budget, status)) return false;
+          const uint32_t it = F::kPer * tt + (kFp8 ? 0 : uint32_t(k >> 6));
+          return warp_wait(bar(kRBarVFull + int(it % F::kVSlots)), (it / F::kVSlots) & 1u, budget, status);
         };
-        auto value_unit = [&](int k, int c) {
-          const uint32_t it = v_item + (kFp8 ? 0 : uint32_t(k >> 6));
-          const uint32_t base = sRing + (it % F::kSlots) * uint32_t(kSlotBytes);
-          return base + uint32_t(c >> 3) * (kFp8 ? kChunk : kSlotBytes / 4) + uint32_t(kFp8 ? k : k & 63) * 128u +
-                 uint32_t(((c ^ k) & 7) << 4);
+        auto value_unit = [&](int k, int c) {  // 16-byte unit c of key k's values, in any order
+          const uint32_t it = F::kPer * tt + (kFp8 ? 0 : uint32_t(k >> 6));
+          return sV + (it % F::kVSlots) * uint32_t(kSlotBytes) + uint32_t(c >> 3) * (kFp8 ? kChunk : kSlotBytes / 4) +
+                 uint32_t(kFp8 ? k : k & 63) * 128u + uint32_t(((c ^ k) & 7) << 4);
         };
+        if (idle) {  // its rows of S and O are nobody's; the tiles are counted
+          ok = warp_wait(bar(kRBarS + int(sb)), ph, budget, status);
+          if (!ok) break;
+          if (lane == 0) mbar_arrive(bar(kRBarP + int(sb)));
+          continue;
+        }
+        fine = warp_wait(bar(kRBarKeys + int(sb)), ph, budget, status) && fine;
         // Which of the 32 keys are there, and which this row sees.
-        uint32_t vis = __ballot_sync(0xffffffffu, page_now >= 0);
+        const uint32_t there = sh_there[sb * 4 + part];
+        const float* scale = sh_scale + sb * 384 + part * 32;
+        uint32_t vis = there;
         const bool drafted_tile = j0 + 32 > g.s.ctx && vis != 0;
         if (drafted_tile && live) {
 #pragma unroll 8
@@ -331,46 +360,14 @@ __global__ void __launch_bounds__(RowsCfg<kFp8>::kThreads, 1) tree_rows_kernel(c
             if (j0 + i >= g.s.ctx && ((vis >> i) & 1u) && !tree_sees(p, g.b, t, int(j0 + i - g.s.ctx))) vis &= ~(1u << i);
         }
         const bool masked = __any_sync(0xffffffffu, vis != 0xffffffffu);
-        if constexpr (kFp8) {
-          // A row of zeros (written with scale 1): see tree_tc.cu.
-          if (__any_sync(0xffffffffu, page_now >= 0 && vs == 1.f)) {
-            fine = value_there(key) && fine;
-            uint32_t any = 0;
-            if (fine && vs == 1.f)
-#pragma unroll 4
-              for (int c = 0; c < 16; ++c) {
-                const uint4 v = lds16(value_unit(key, c));
-                any |= (v.x | v.y | v.z | v.w) & 0x7f7f7f7fu;
-              }
-            if (vs == 1.f && any == 0) vs = 0.f;
-            __syncwarp();
-          }
-          if (vs == 0.f) vs = 7.8886090522101181e-31f;  // 2^-100
-          sh_scale[lane] = page_now >= 0 ? ks : 0.f;
-          sh_scale[32 + lane] = page_now >= 0 ? log2f(vs) : 0.f;
-          sh_scale[64 + lane] = 1.f / vs;
-          __syncwarp();
-        }
-        // Values that some row must not see and that are not finite are cleared in the tile and
-        // added at the end (tree_tc.cu).  Quarter 0's warps look after the 128 keys.
-        if (p.T > 1 && quarter == 0 && drafted_tile) {
+        // Values that take no part, as in tree_tc.cu.  Quarter 0's warps look after the 128 keys.
+        const bool gone = !((there >> lane) & 1u), drafted = !gone && p.T > 1 && j0 + lane >= g.s.ctx;
+        if (quarter == 0 && __any_sync(0xffffffffu, gone || drafted)) {
           fine = value_there(part * 32) && fine;
-          if (fine && page_now >= 0 && j0 + lane >= g.s.ctx) {
+          if (fine && (gone || drafted)) {
             uint32_t bad = 0;
 #pragma unroll 1
-            for (int c = 0; c < (kFp8 ? 16 : 32); ++c) {
-              const uint4 v = lds16(value_unit(key, c));
-              uint32_t w[4] = {v.x, v.y, v.z, v.w}, hit = 0;
-#pragma unroll
-              for (int k = 0; k < 4; ++k) {
-                const uint32_t x = kFp8 ? __vcmpeq4(w[k] & 0x7f7f7f7fu, 0x7f7f7f7fu)
-                                        : __vcmpeq2(w[k] & 0x7f807f80u, 0x7f807f80u);
-                hit |= x;
-                w[k] &= ~x;
-              }
-              if (hit) sts16(value_unit(key, c), make_uint4(w[0], w[1], w[2], w[3]));
-              bad |= hit;
-            }
+            for (int c = 0; c < (kFp8 ? 16 : 32); ++c) bad |= mend_unit<kFp8>(value_unit(key, c), gone);
             const int u = int(j0 + lane - g.s.ctx);
             if (bad) atomicOr(&sh_bad[u >> 5], 1u << (u & 31));
           }
@@ -385,8 +382,8 @@ __global__ void __launch_bounds__(RowsCfg<kFp8>::kThreads, 1) tree_rows_kernel(c
 #pragma unroll
         for (int i = 0; i < 32; i += 4) {
           if constexpr (kFp8) {
-            const float4 k4 = *reinterpret_cast<const float4*>(sh_scale + i);
-            const float4 l4 = *reinterpret_cast<const float4*>(sh_scale + 32 + i);
+            const float4 k4 = *reinterpret_cast<const float4*>(scale + i);
+            const float4 l4 = *reinterpret_cast<const float4*>(scale + 128 + i);
             x[i] = fmaf(x[i] * factor, k4.x, l4.x);
             x[i + 1] = fmaf(x[i + 1] * factor, k4.y, l4.y);
             x[i + 2] = fmaf(x[i + 2] * factor, k4.z, l4.z);
@@ -441,7 +438,7 @@ __global__ void __launch_bounds__(RowsCfg<kFp8>::kThreads, 1) tree_rows_kernel(c
           uint32_t hi[8], lo[8];
 #pragma unroll
           for (int i = 0; i < 32; i += 4) {
-            const float4 inv = *reinterpret_cast<const float4*>(sh_scale + 64 + i);
+            const float4 inv = *reinterpret_cast<const float4*>(scale + 256 + i);
             float e[4], h[4];
 #pragma unroll
             for (int k = 0; k < 4; ++k) e[k] = ex2(x[i + k] - m);
@@ -457,7 +454,6 @@ __global__ void __launch_bounds__(RowsCfg<kFp8>::kThreads, 1) tree_rows_kernel(c
           }
           tmem_st8u(lane_addr + 256u + sb * 128u + uint32_t(part * 8), hi);
           tmem_st8u(lane_addr + 256u + sb * 128u + 32u + uint32_t(part * 8), lo);
-          __syncwarp();  // sh_scale is read
         } else {
           uint32_t pk[16];
           float sum[4] = {0.f, 0.f, 0.f, 0.f};
@@ -535,9 +531,14 @@ __global__ void __launch_bounds__(RowsCfg<kFp8>::kThreads, 1) tree_rows_kernel(c
 template <bool kFp8>
 int launch(const TreeParams& p, cudaStream_t stream) {
   using F = RowsCfg<kFp8>;
+  CUtensorMap mk, mv;
+  const int most = kFp8 ? 7 : 6;  // bf16 values come in halves of 64 keys
+  if (!encode_pages(&mk, p.c, p.c.k, 1 << (p.c.page_shift < 7 ? p.c.page_shift : 7)) ||
+      !encode_pages(&mv, p.c, p.c.v, 1 << (p.c.page_shift < most ? p.c.page_shift : most)))
+    return GQA_ERR_LAUNCH;
   if (cudaFuncSetAttribute(tree_rows_kernel<kFp8>, cudaFuncAttributeMaxDynamicSharedMemorySize, F::kSmem) != cudaSuccess)
     return GQA_ERR_LAUNCH;
-  tree_rows_kernel<kFp8><<<unsigned(p.workers) * unsigned(p.row_tiles), F::kThreads, F::kSmem, stream>>>(p);
+  tree_rows_kernel<kFp8><<<unsigned(p.workers) * unsigned(p.row_tiles), F::kThreads, F::kSmem, stream>>>(mk, mv, p);
   return cudaGetLastError() == cudaSuccess ? GQA_OK : GQA_ERR_LAUNCH;
 }
 

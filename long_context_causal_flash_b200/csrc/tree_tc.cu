@@ -22,9 +22,8 @@
 // than the largest p, and P is stored as 16 P <= 256: a probability then keeps 8 bits down
 // to 2^-8 of the first maximum, and is off by at most 2^-14 of it below.
 //
-// Warps: 4 softmax warps per 32 (or 16) rows, one producer warp per 32 KiB slot of the
-// ring (cp.async, 16 bytes at a time, through the page table; two rows to an
-// instruction), and two warps whose first lanes issue the products.
+// Warps: 4 softmax warps per 32 (or 16) rows, a producer (TMA, through the page table, into
+// rings of 32 KiB slots), and two warps whose first lanes issue the products.
 #include "tree_tc.cuh"
 
 namespace gqa {
@@ -36,17 +35,18 @@ struct Cfg {
   static constexpr int kParts = kN / kCols;
   static constexpr int kSoftWarps = 4 * kParts;
   static constexpr int kNN = kFp8 ? 2 * kN : kN;            // N of a product: e4m3 pieces lie side by side
-  static constexpr int kItems = kFp8 ? 2 : 4;               // slots of a tile
+  static constexpr int kPer = kFp8 ? 1 : 2;                 // slots of a tile's keys, and of its values
   static constexpr int kQBytes = kN * 512;                  // bf16, or two e4m3 pieces
   static constexpr int kPBytes = kChunk;
-  static constexpr int kSlots = kN > 32 ? 5 : 6;  // what shared memory has room for
-  static constexpr int kIssuer = kSoftWarps + kSlots;           // the S issuer's warp; the O issuer's is the next
+  static constexpr int kKSlots = kN > 32 ? 2 : 3, kVSlots = 3;  // what shared memory has room for
+  static constexpr int kIssuer = kSoftWarps + 1;  // the S issuer's warp, after the producer; then the O issuer's
   static constexpr int kWarps = kIssuer + 2;
   static constexpr int kThreads = 32 * kWarps;
   static constexpr int kOffQ = 0;
   static constexpr int kOffP = kOffQ + kQBytes;
-  static constexpr int kOffRing = kOffP + kPBytes;
-  static constexpr int kOffBar = kOffRing + kSlots * kSlotBytes;
+  static constexpr int kOffK = kOffP + kPBytes;
+  static constexpr int kOffV = kOffK + kKSlots * kSlotBytes;
+  static constexpr int kOffBar = kOffV + kVSlots * kSlotBytes;
   static constexpr int kOffM = kOffBar + 256;     // [kN] maxima
   static constexpr int kOffF = kOffM + kN * 4;    // [kN] factor of a row's scores (e4m3 pages)
   static constexpr int kOffBad = kOffF + kN * 4;  // 32 words: drafted tokens with a value that is not finite
@@ -55,8 +55,19 @@ struct Cfg {
   static constexpr uint32_t kTmem = 4 * kNN;
   static_assert(kSmem <= 232448 - 1024, "shared memory per block");
 };
-// Barriers: S^T, its release, P and O per parity of the tile; the ring's slots.
-enum { kBarQ = 0, kBarS = 1, kBarSFree = 3, kBarP = 5, kBarPV = 7, kBarDrain = 9, kBarFull = 10, kBarEmpty = 16 };
+// Barriers: S^T, its release, P and O per parity of the tile; the rings' slots.
+enum {
+  kBarQ = 0,
+  kBarS = 1,
+  kBarSFree = 3,
+  kBarP = 5,
+  kBarPV = 7,
+  kBarDrain = 9,
+  kBarKFull = 10,
+  kBarKEmpty = 13,
+  kBarVFull = 16,
+  kBarVEmpty = 19
+};
 
 // Sum or maximum over the 32 lanes of each of 16 values: lane l ends with value l / 2.  A
 // lane sends the half that it does not keep.
@@ -79,7 +90,8 @@ __device__ __forceinline__ float lanes_reduce(float (&v)[16]) {
 }
 
 template <int kN, bool kFp8>
-__global__ void __launch_bounds__(Cfg<kN, kFp8>::kThreads, 1) tree_tc_kernel(const __grid_constant__ TreeParams p) {
+__global__ void __launch_bounds__(Cfg<kN, kFp8>::kThreads, 1) tree_tc_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v,
+               const __grid_constant__ TreeParams p) {
   using F = Cfg<kN, kFp8>;
   constexpr int C = F::kCols;
   extern __shared__ __align__(1024) char smem_raw[];
@@ -87,7 +99,7 @@ __global__ void __launch_bounds__(Cfg<kN, kFp8>::kThreads, 1) tree_tc_kernel(con
   __shared__ uint32_t tmem_slot;
   const uint32_t sbase = smem_u32(smem_raw);
   const bool misaligned = (sbase & 1023u) != 0;  // the swizzle needs it; never expected to fail
-  const uint32_t sQ = sbase + F::kOffQ, sP = sbase + F::kOffP, sRing = sbase + F::kOffRing;
+  const uint32_t sQ = sbase + F::kOffQ, sP = sbase + F::kOffP, sK = sbase + F::kOffK, sV = sbase + F::kOffV;
   auto bar = [&](int i) { return sbase + F::kOffBar + 8u * uint32_t(i); };
   float* sh_m = reinterpret_cast<float*>(smem_raw + F::kOffM);
   float* sh_f = reinterpret_cast<float*>(smem_raw + F::kOffF);
@@ -109,9 +121,13 @@ __global__ void __launch_bounds__(Cfg<kN, kFp8>::kThreads, 1) tree_tc_kernel(con
         mbar_init(bar(kBarPV + i), 1);
       }
       mbar_init(bar(kBarDrain), 2);
-      for (int i = 0; i < F::kSlots; ++i) {
-        mbar_init(bar(kBarFull + i), 1);
-        mbar_init(bar(kBarEmpty + i), 1);
+      for (int i = 0; i < F::kKSlots; ++i) {
+        mbar_init(bar(kBarKFull + i), 1);
+        mbar_init(bar(kBarKEmpty + i), 1);
+      }
+      for (int i = 0; i < F::kVSlots; ++i) {
+        mbar_init(bar(kBarVFull + i), 1);
+        mbar_init(bar(kBarVEmpty + i), 1);
       }
       fence_barrier_init();
       if (misaligned) set_status(status, GQA_ERR_LAUNCH);
@@ -127,67 +143,12 @@ __global__ void __launch_bounds__(Cfg<kN, kFp8>::kThreads, 1) tree_tc_kernel(con
 
   if (misaligned) {
     // no role
-  } else if (warp >= F::kSoftWarps && warp < F::kIssuer) {
-    // ---------------------------------------------------------------- producers
-    // This warp fills slot `s`: items s, s + kSlots, ... of the tiles' list.  A bf16 tile is
-    // four items (key columns 0 - 127, 128 - 255, the same of the values), an e4m3 tile two.
-    // Image of an item: two column blocks of 128 bytes, [128 keys][128 bytes] each, 16-byte
-    // units at unit ^ (key & 7).  Keys past the end are zeros.
-    const int s = warp - F::kSoftWarps;
-    const uint32_t slot = sRing + uint32_t(s) * kSlotBytes;
-    const int unit = lane & 15, odd = lane >> 4;
-    constexpr int kEs = kFp8 ? 1 : 2;
-    const uint32_t slot_mask = (1u << p.c.page_shift) - 1;
-    const int64_t row_bytes = p.c.st * kEs;
-    uint32_t dst[4];  // this lane's units of rows 0 / 1, 2 / 3, 4 / 5 and 6 / 7 of a group
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-      dst[i] = slot + uint32_t(unit >> 3) * kChunk + uint32_t(2 * i + odd) * 128u +
-               uint32_t(((unit & 7) ^ (2 * i + odd)) << 4);
-    int idx = s;
-    bool live = tree_next(p, cur, &g);
-    // The page of each group of eight keys of this item, in lanes 0 .. 15.
-    auto pages = [&]() {
-      while (live && idx >= (g.t1 - g.t0) * F::kItems) {
-        idx -= (g.t1 - g.t0) * F::kItems;
-        live = tree_next(p, cur, &g);
-      }
-      if (!live) return -1;
-      const uint32_t j = uint32_t(g.t0 + idx / F::kItems) * kTreeTile + lane * 8;
-      return lane < 16 && j < g.s.keys ? page_of(p.c, p.table + int64_t(g.b) * p.max_pages, p.max_pages, j) : -1;
-    };
-    int pg = pages();
-    for (uint32_t n = 0; live; ++n) {
-      if (!warp_wait(bar(kBarEmpty + s), (n & 1u) ^ 1u, budget, status)) break;
-      const int item = idx % F::kItems;
-      const uint32_t j0 = uint32_t(g.t0 + idx / F::kItems) * kTreeTile;
-      const char* pool = (item >= F::kItems / 2 ? p.c.v : p.c.k) + int64_t(g.h) * p.c.sh * kEs;
-      const char* lane_src = pool + (kFp8 ? 0 : (item & 1) * 256) + unit * 16 + odd * row_bytes;
-      const int left = int(min(uint32_t(kTreeTile), g.s.keys - j0));
-#pragma unroll 2
-      for (int grp = 0; grp < 16; ++grp) {
-        const int page = __shfl_sync(0xffffffffu, pg, grp);
-        const char* src = lane_src + (int64_t(page) * p.c.sp + ((j0 + grp * 8) & slot_mask) * p.c.st) * kEs;
-        if (page >= 0 && left >= grp * 8 + 8) {
-#pragma unroll
-          for (int i = 0; i < 4; ++i) cp_async16(dst[i] + uint32_t(grp) * 1024u, src + 2 * i * row_bytes, 16u);
-        } else {
-          const int rows = page < 0 ? 0 : left - grp * 8;
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const bool there = 2 * i + odd < rows;
-            cp_async16(dst[i] + uint32_t(grp) * 1024u, there ? src + 2 * i * row_bytes : pool, there ? 16u : 0u);
-          }
-        }
-      }
-      idx += F::kSlots;
-      pg = pages();  // the next item's, while this one's copies are under way
-      asm volatile("cp.async.wait_all;" ::: "memory");
-      fence_proxy_async_smem();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(bar(kBarFull + s));
-    }
-    asm volatile("cp.async.wait_all;" ::: "memory");
+  } else if (warp == F::kSoftWarps) {
+    Feed<kFp8, false, F::kKSlots> k;
+    Feed<kFp8, false, F::kVSlots> v;
+    k.begin(p, cur, &map_k, sK, bar(kBarKFull), bar(kBarKEmpty));
+    v.begin(p, cur, &map_v, sV, bar(kBarVFull), bar(kBarVEmpty));
+    produce(p, k, v);
   } else if (warp >= F::kIssuer) {
     // ---------------------------------------------------------------- MMA issuers
     // One thread issues every S^T = K Q^T, another every O^T += V^T P^T, so that neither
@@ -209,15 +170,15 @@ __global__ void __launch_bounds__(Cfg<kN, kFp8>::kThreads, 1) tree_tc_kernel(con
             ok = tt < 2 || mbar_wait_inline(bar(kBarSFree + int(b)), ph ^ 1u, budget, status);
           else
             ok = mbar_wait_inline(bar(kBarP + int(b)), ph, budget, status);
-          const uint32_t first = tt * F::kItems + (is_s ? 0 : F::kItems / 2);
+          const uint32_t slots = is_s ? F::kKSlots : F::kVSlots;
+          const uint32_t full = bar(is_s ? kBarKFull : kBarVFull), empty = bar(is_s ? kBarKEmpty : kBarVEmpty);
 #pragma unroll
           for (int part = 0; part < 2; ++part) {  // halves of the key's columns, or of the value's
-            const uint32_t item = kFp8 ? first : first + part, slot = item % F::kSlots;
-            if ((!kFp8 || part == 0) && ok)
-              ok = mbar_wait_inline(bar(kBarFull + int(slot)), (item / F::kSlots) & 1u, budget, status);
+            const uint32_t item = kFp8 ? tt : 2 * tt + part, slot = item % slots;
+            if ((!kFp8 || part == 0) && ok) ok = mbar_wait_inline(full + 8u * slot, (item / slots) & 1u, budget, status);
             if (!ok) break;
             umma::fence_after_sync();
-            const uint32_t base = sRing + slot * uint32_t(kSlotBytes);
+            const uint32_t base = (is_s ? sK : sV) + slot * uint32_t(kSlotBytes);
             if (is_s) {
               const uint64_t dk = umma::smem_desc(base, 16, 1024);
 #pragma unroll
@@ -236,7 +197,7 @@ __global__ void __launch_bounds__(Cfg<kN, kFp8>::kThreads, 1) tree_tc_kernel(con
                           tile > g.t0 || k != 0);
               }
             }
-            if (!kFp8 || part == 1) umma::commit(bar(kBarEmpty + int(slot)));
+            if (!kFp8 || part == 1) umma::commit(empty + 8u * slot);
           }
           if (ok) umma::commit(bar((is_s ? kBarS : kBarPV) + int(b)));
         }
@@ -338,19 +299,22 @@ __global__ void __launch_bounds__(Cfg<kN, kFp8>::kThreads, 1) tree_tc_kernel(con
       for (int tile = g.t0; tile < g.t1; ++tile, ++tt) {
         const uint32_t sb = tt & 1u, ph = (tt >> 1) & 1u;
         const uint32_t j = uint32_t(tile) * kTreeTile + key;
-        const uint32_t v_item = tt * F::kItems + F::kItems / 2;  // this tile's values in the ring
+        // The product of the tile before: P's last reader, and what O holds.
+        auto last_product = [&]() {
+          return tt == 0 || warp_wait(bar(kBarPV + int((tt - 1) & 1u)), ((tt - 1) >> 1) & 1u, budget, status);
+        };
+        // This tile's values are in their slots.  The product before is over first, so that the
+        // barriers stand at no earlier use of the slots.
         auto values_there = [&]() {
-          bool there = true;
+          bool there = last_product();
 #pragma unroll
-          for (int i = 0; i < F::kItems / 2; ++i)
-            there = warp_wait(bar(kBarFull + int((v_item + i) % F::kSlots)), ((v_item + i) / F::kSlots) & 1u, budget,
-                              status) &&
-                    there;
+          for (uint32_t it = F::kPer * tt; it < F::kPer * tt + F::kPer; ++it)
+            there = there && warp_wait(bar(kBarVFull + int(it % F::kVSlots)), (it / F::kVSlots) & 1u, budget, status);
           return there;
         };
         auto value_unit = [&](int c) {  // 16-byte unit c of the key's values, in any order
-          return sRing + ((v_item + uint32_t(c >> 4)) % F::kSlots) * uint32_t(kSlotBytes) + uint32_t((c >> 3) & 1) * kChunk +
-                 uint32_t(key) * 128u + uint32_t(((c ^ key) & 7) << 4);
+          return sV + ((F::kPer * tt + uint32_t(c >> 4)) % F::kVSlots) * uint32_t(kSlotBytes) +
+                 uint32_t((c >> 3) & 1) * kChunk + uint32_t(key) * 128u + uint32_t(((c ^ key) & 7) << 4);
         };
         const float ks = kFp8 ? (page < 0 ? 0.f : ks_next) : p.scale_log2;
         float vs = kFp8 && page >= 0 ? vs_next : 1.f, lvs = 0.f, inv_vs = 1.f;
@@ -391,26 +355,15 @@ __global__ void __launch_bounds__(Cfg<kN, kFp8>::kThreads, 1) tree_tc_kernel(con
           lvs = log2f(vs);
           inv_vs = 1.f / vs;
         }
-        // Values that some row must not see: elements that are not finite would reach it as 0 x
-        // infinity.  They are cleared in the tile, and added at the end for the rows that see them.
-        if (p.T > 1 && part == 0 && __any_sync(0xffffffffu, drafted)) {
+        // Values that take no part reach a row as 0 x what they are, NaN if that is not finite: those
+        // of keys that are not there (a page's rest) are cleared in the tile, and those elements of
+        // drafted tokens, which some row may not see; they are added at the end for the rows that do.
+        if (part == 0 && __any_sync(0xffffffffu, page_now < 0 || (drafted && p.T > 1))) {
           fine = values_there() && fine;
-          if (fine && drafted) {
+          if (fine && (page_now < 0 || (drafted && p.T > 1))) {
             uint32_t bad = 0;
 #pragma unroll 1
-            for (int c = 0; c < 8 * F::kItems; ++c) {
-              const uint4 v = lds16(value_unit(c));
-              uint32_t w[4] = {v.x, v.y, v.z, v.w}, hit = 0;
-#pragma unroll
-              for (int k = 0; k < 4; ++k) {
-                const uint32_t m = kFp8 ? __vcmpeq4(w[k] & 0x7f7f7f7fu, 0x7f7f7f7fu)  // e4m3 has NaN alone
-                                        : __vcmpeq2(w[k] & 0x7f807f80u, 0x7f807f80u);
-                hit |= m;
-                w[k] &= ~m;
-              }
-              if (hit) sts16(value_unit(c), make_uint4(w[0], w[1], w[2], w[3]));
-              bad |= hit;
-            }
+            for (int c = 0; c < 16 * F::kPer; ++c) bad |= mend_unit<kFp8>(value_unit(c), page_now < 0);
             const int u = int(j - g.s.ctx);
             if (bad) atomicOr(&sh_bad[u >> 5], 1u << (u & 31));
           }
@@ -419,10 +372,6 @@ __global__ void __launch_bounds__(Cfg<kN, kFp8>::kThreads, 1) tree_tc_kernel(con
         }
         fine = warp_wait(bar(kBarS + int(sb)), ph, budget, status) && fine;
         umma::fence_after_sync();
-        // The product of the tile before: P's last reader, and what O holds.
-        auto last_product = [&]() {
-          return tt == 0 || warp_wait(bar(kBarPV + int((tt - 1) & 1u)), ((tt - 1) >> 1) & 1u, budget, status);
-        };
         bool stop = false;
 #pragma unroll
         for (int c0 = 0; c0 < C; c0 += 16) {
@@ -653,21 +602,24 @@ __global__ void __launch_bounds__(Cfg<kN, kFp8>::kThreads, 1) tree_tc_kernel(con
 }
 
 template <int kN, bool kFp8>
-int launch_n(const TreeParams& p, cudaStream_t stream) {
+int launch_n(const TreeParams& p, const CUtensorMap& mk, const CUtensorMap& mv, cudaStream_t stream) {
   using F = Cfg<kN, kFp8>;
   if (cudaFuncSetAttribute(tree_tc_kernel<kN, kFp8>, cudaFuncAttributeMaxDynamicSharedMemorySize, F::kSmem) !=
       cudaSuccess)
     return GQA_ERR_LAUNCH;
-  tree_tc_kernel<kN, kFp8><<<unsigned(p.workers) * unsigned(p.row_tiles), F::kThreads, F::kSmem, stream>>>(p);
+  tree_tc_kernel<kN, kFp8><<<unsigned(p.workers) * unsigned(p.row_tiles), F::kThreads, F::kSmem, stream>>>(mk, mv, p);
   return cudaGetLastError() == cudaSuccess ? GQA_OK : GQA_ERR_LAUNCH;
 }
 
 template <bool kFp8>
 int launch_type(const TreeParams& p, int rows, cudaStream_t stream) {
+  CUtensorMap mk, mv;
+  const int box = 1 << (p.c.page_shift < 7 ? p.c.page_shift : 7);
+  if (!encode_pages(&mk, p.c, p.c.k, box) || !encode_pages(&mv, p.c, p.c.v, box)) return GQA_ERR_LAUNCH;
   switch (rows) {
-    case 16: return launch_n<16, kFp8>(p, stream);
-    case 32: return launch_n<32, kFp8>(p, stream);
-    default: return launch_n<64, kFp8>(p, stream);
+    case 16: return launch_n<16, kFp8>(p, mk, mv, stream);
+    case 32: return launch_n<32, kFp8>(p, mk, mv, stream);
+    default: return launch_n<64, kFp8>(p, mk, mv, stream);
   }
 }
 

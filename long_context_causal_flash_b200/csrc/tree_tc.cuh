@@ -47,10 +47,6 @@ __device__ __forceinline__ uint32_t pack_bf16x2(float lo, float hi) {
   return *reinterpret_cast<uint32_t*>(&h);
 }
 
-__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, uint32_t bytes) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
-}
-
 __device__ __forceinline__ void sts16(uint32_t a, uint4 v) {
   asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(a), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
 }
@@ -112,6 +108,184 @@ __device__ __noinline__ float hidden_values(const TreeParams& p, const TreeSegme
     }
   }
   return sum;
+}
+
+// 5-D tiled TMA load global -> shared, completion counted on `bar` in bytes.  No multicast.
+__device__ __forceinline__ void tma_load_5d(uint32_t dst, const CUtensorMap* map, uint32_t bar, int c0, int c1, int c2,
+                                            int c3, int c4) {
+  asm volatile(
+      "cp.async.bulk.tensor.5d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%3, %4, %5, %6, %7}], [%2];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(c0), "r"(c1), "r"(c2), "r"(c3), "r"(c4)
+      : "memory");
+}
+
+// mbarrier phase `parity` is over; does not wait.
+__device__ __forceinline__ bool mbar_test(uint32_t bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(bar), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
+
+// The keys' or the values' way into shared memory, kept by one whole warp.  They have a ring
+// of slots each: their readers wait on a slot's barrier by the parity of its uses, so a
+// reader has to wait for every use of the slot, and in a ring that both share one could take
+// the use before last for its own.  A tile is kPer items; an item is column blocks of 128
+// bytes, [keys][128 bytes] each, 128-byte swizzled.  bf16: two items of two blocks of all 128
+// keys, or with kSplit two of four blocks of 64 keys; e4m3: one of two blocks of 128 keys.
+// One TMA box per column block and page (or part of a page): on B200 a 32 KiB slot takes
+// 435 - 450 cycles in boxes of 32 keys or more and 530 in boxes of 16, all 148 SMs loading
+// from L2 at once.  cp.async by a warp per slot has the same rate, but takes about 2,000
+// cycles of a warp and their latency before the slot is full.
+// Whole boxes are loaded: rows of a page past the last key hold what the page holds, pages
+// that are not there leave the slot as it was.  The softmax warps hide those keys' scores
+// and clear their values.
+template <bool kFp8, bool kSplit, int kSlots>
+struct Feed {
+  static constexpr int kPer = kFp8 ? 1 : 2;
+  static constexpr int kKeys = kSplit ? 64 : 128, kBlocks = kSplit ? 4 : 2;
+  const CUtensorMap* map;
+  uint32_t ring, bar_full, bar_empty;
+  TreeCursor cur;
+  TreeSegment g;
+  uint32_t item = 0;
+  int tile = 0, half = 0, page = -1, page_next = -1;
+  bool live = false;
+
+  // The page of each group of eight keys of a tile, in lanes 0 .. 15.
+  __device__ __forceinline__ int pages(const TreeParams& p, int t) const {
+    const int lane = threadIdx.x & 31;
+    const uint32_t j = uint32_t(t) * kTreeTile + lane * 8;
+    return t < g.t1 && lane < 16 && j < g.s.keys ? page_of(p.c, p.table + int64_t(g.b) * p.max_pages, p.max_pages, j) : -1;
+  }
+  __device__ __forceinline__ void segment(const TreeParams& p) {
+    live = tree_next(p, cur, &g);
+    if (!live) return;
+    tile = g.t0;
+    half = 0;
+    page = pages(p, tile);
+    page_next = pages(p, tile + 1);
+  }
+  __device__ __forceinline__ void begin(const TreeParams& p, const TreeCursor& start, const CUtensorMap* m, uint32_t r,
+                                        uint32_t full, uint32_t empty) {
+    map = m, ring = r, bar_full = full, bar_empty = empty, cur = start;
+    if ((threadIdx.x & 31) == 0) tma_prefetch_desc(map);
+    segment(p);
+  }
+  // The next item's slot is free.
+  __device__ __forceinline__ bool ready() const {
+    return live && __all_sync(0xffffffffu, mbar_test(bar_empty + 8u * (item % kSlots), ((item / kSlots) & 1u) ^ 1u));
+  }
+  __device__ __forceinline__ void issue(const TreeParams& p) {
+    const int lane = threadIdx.x & 31;
+    // Boxes: `rows` keys each, `per` per column block.  Box n = 32 round + lane is part n % per
+    // of column block n / per.
+    const int shift = min(p.c.page_shift, kSplit ? 6 : 7), rows = 1 << shift, per = kKeys >> shift;
+    const int boxes = per * kBlocks, rounds = (boxes + 31) / 32;
+    const uint32_t slot = item % kSlots, full = bar_full + 8u * slot;
+    const int first = kSplit ? half * 64 : 0;  // key of the tile the item starts with
+    uint32_t there = 0;
+    for (int round = 0; round < rounds; ++round) {
+      const int n = round * 32 + lane, k = first + (n & (per - 1)) * rows;
+      const int pg = __shfl_sync(0xffffffffu, page, (k >> 3) & 15);
+      there += __popc(__ballot_sync(0xffffffffu, n < boxes && pg >= 0));
+    }
+    if (lane == 0) mbar_arrive_expect_tx(full, there * uint32_t(rows) * 128u);
+    __syncwarp();
+    for (int round = 0; round < rounds; ++round) {
+      const int n = round * 32 + lane, k = first + (n & (per - 1)) * rows, block = n >> ((kSplit ? 6 : 7) - shift);
+      const int pg = __shfl_sync(0xffffffffu, page, (k >> 3) & 15);
+      if (n < boxes && pg >= 0) {
+        const uint32_t j = uint32_t(tile) * kTreeTile + uint32_t(k);
+        tma_load_5d(ring + slot * uint32_t(kSlotBytes) + uint32_t(block * kKeys + (k - first)) * 128u, map, full, 0,
+                    int(j & ((1u << p.c.page_shift) - 1)), kSplit ? block : 2 * half + block, g.h, pg);
+      }
+    }
+    __syncwarp();
+    ++item;
+    if (++half == kPer) {
+      half = 0;
+      page = page_next;
+      if (++tile < g.t1)
+        page_next = pages(p, tile + 1);
+      else
+        segment(p);
+    }
+  }
+  // No copy may be in flight when the CTA ends.
+  __device__ __forceinline__ void drain(const TreeParams& p) const {
+    for (uint32_t i = item > uint32_t(kSlots) ? item - kSlots : 0u; i < item; ++i)
+      warp_wait(bar_full + 8u * (i % kSlots), (i / kSlots) & 1u, p.wait_budget_ns, p.c.status);
+  }
+};
+
+// The producer warp: fills whichever ring has a free slot.
+template <class K, class V>
+__device__ __forceinline__ void produce(const TreeParams& p, K& k, V& v) {
+  uint64_t since = global_timer_ns();
+  while (k.live || v.live) {
+    bool moved = false;
+    if (k.ready()) {
+      k.issue(p);
+      moved = true;
+    }
+    if (v.ready()) {
+      v.issue(p);
+      moved = true;
+    }
+    const uint64_t now = global_timer_ns();
+    if (moved) {
+      since = now;
+    } else if (__any_sync(0xffffffffu, int64_t(now - since) > p.wait_budget_ns)) {
+      set_status(p.c.status, GQA_ERR_DEVICE_TIMEOUT);
+      break;
+    }
+  }
+  k.drain(p);
+  v.drain(p);
+}
+
+// The tensor map of a pool's keys or values: (64 or 128 columns of a 128-byte block, token of
+// the page, block, head, page), boxes of one block and `rows` tokens.
+inline bool encode_pages(CUtensorMap* m, const CacheView& c, const char* pool, int rows) {
+  EncodeTiledFn enc = encode_tiled_fn();
+  if (!enc) return false;
+  const bool fp8 = c.dtype == GQA_E4M3;
+  const cuuint64_t es = fp8 ? 1 : 2;
+  const cuuint64_t dims[5] = {128 / es, cuuint64_t(1) << c.page_shift, 2 * es, cuuint64_t(c.Hkv), cuuint64_t(c.n_pages)};
+  // A dimension of one has no stride of its own (views may carry any number there).
+  const cuuint64_t strides[4] = {cuuint64_t(c.st) * es, 128, c.Hkv > 1 ? cuuint64_t(c.sh) * es : 16,
+                                 c.n_pages > 1 ? cuuint64_t(c.sp) * es : 16};
+  const cuuint32_t box[5] = {cuuint32_t(128 / es), cuuint32_t(rows), 1, 1, 1}, estr[5] = {1, 1, 1, 1, 1};
+  return enc(m, fp8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 5, const_cast<char*>(pool), dims,
+             strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// One 16-byte unit of a value in shared memory: cleared whole, or its elements that are not
+// finite (e4m3 has NaN alone); returns whether it had any of the latter.
+template <bool kFp8>
+__device__ __forceinline__ uint32_t mend_unit(uint32_t a, bool whole) {
+  if (whole) {
+    sts16(a, make_uint4(0, 0, 0, 0));
+    return 0;
+  }
+  const uint4 v = lds16(a);
+  uint32_t w[4] = {v.x, v.y, v.z, v.w}, hit = 0;
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    const uint32_t m = kFp8 ? __vcmpeq4(w[k] & 0x7f7f7f7fu, 0x7f7f7f7fu) : __vcmpeq2(w[k] & 0x7f807f80u, 0x7f807f80u);
+    hit |= m;
+    w[k] &= ~m;
+  }
+  if (hit) sts16(a, make_uint4(w[0], w[1], w[2], w[3]));
+  return hit;
 }
 
 // One warp: row r of an e4m3 Q operand, both pieces of the row's eight columns per lane.

@@ -74,17 +74,21 @@ def tree_attention(q, k, v, context, drafted, mask=None):
     q, k, v = _as_f64(q), _as_f64(k), _as_f64(v)
     Hq, T, d = q.shape
     G = Hq // k.shape[0]
+    size = np.abs(v)
     out, spread, lse = np.zeros((Hq, T, d)), np.zeros((Hq, T, d)), np.full((Hq, T), -np.inf)
     for t in range(min(T, drafted)):
-        seen = [u for u in range(drafted) if (u <= t if mask is None else mask[t][u])]
-        keys = np.concatenate([np.arange(context), context + np.array(seen, dtype=np.int64)]).astype(np.int64)
-        if not len(keys):
+        seen = [context + u for u in range(drafted) if (u <= t if mask is None else mask[t][u])]
+        if context + len(seen) == 0:
             continue
-        for h in range(Hq):
-            s = k[h // G][keys] @ q[h, t] / math.sqrt(d)
-            top = s.max()
+        for g in range(k.shape[0]):
+            h = slice(g * G, (g + 1) * G)
+            # the context's rows are used in place, the drafted ones that the row sees are picked out
+            s = np.concatenate([q[h, t] @ k[g, :context].T, q[h, t] @ k[g, seen].T], axis=1) / math.sqrt(d)
+            top = s.max(1, keepdims=True)
             p = np.exp(s - top)
-            out[h, t] = p @ v[h // G][keys] / p.sum()
-            spread[h, t] = p @ np.abs(v[h // G][keys]) / p.sum()
-            lse[h, t] = top + math.log(p.sum())
+            total = p.sum(1, keepdims=True)
+            p /= total
+            out[h, t] = p[:, :context] @ v[g, :context] + p[:, context:] @ v[g, seen]
+            spread[h, t] = p[:, :context] @ size[g, :context] + p[:, context:] @ size[g, seen]
+            lse[h, t] = (top + np.log(total))[:, 0]
     return out, lse, spread

@@ -179,6 +179,18 @@ def test_long_context_of_one_sequence_among_short_ones(cuda_device, dtype, kind)
 
 
 @pytest.mark.parametrize("dtype,kind", PAIRS[:3], ids=IDS[:3])
+@pytest.mark.parametrize("T,page", [(1, 128), (12, 32), (20, 64)])
+def test_long_runs_of_tiles(cuda_device, dtype, kind, T, page):
+    """Eight tiles or more to a worker: every ring of slots goes round several times.  Calls in
+    a row, with nothing between them, give the same bits."""
+    p = Problem(cuda_device, 1, 16, 4, T, [38_000], page, dtype, kind, seed=40 + T)
+    got = [p.attend() for _ in range(12)]
+    p.check(*got[0])
+    for out, lse in got[1:]:
+        assert torch.equal(out, got[0][0]) and torch.equal(lse, got[0][1])
+
+
+@pytest.mark.parametrize("dtype,kind", PAIRS[:3], ids=IDS[:3])
 def test_many_sequences(cuda_device, dtype, kind):
     rng = np.random.default_rng(4)
     ctx = [int(c) for c in rng.integers(0, 200, 150)]
@@ -198,6 +210,27 @@ def test_most_tokens(cuda_device, dtype, kind):
         assert np.abs(lse[0, :, t].double().cpu().numpy() - l[:, 0]).max() <= 2e-4
         d = np.abs(out[0, :, t].double().cpu().numpy() - o[:, 0])
         assert np.all(d <= 2.0 ** -8 * (np.abs(o[:, 0]) + spread[:, 0]) + 4e-4 * spread[:, 0])
+
+
+@pytest.mark.parametrize("T", [2, 20])
+def test_rows_of_zeros_among_quantised_values(cuda_device, T):
+    """A value of zeros, which is written with scale 1, takes its weight and nothing else: the
+    other values, of scales about 2^-7, keep their precision.  (A zero scale is as good.)"""
+    p = Problem(cuda_device, 2, 16, 4, T, [1000, 333], 32, BF16, E4M3, seed=50)
+    zero = torch.zeros((2, 4, 1, 256), dtype=BF16, device=cuda_device)
+    for place in (0, 5, 128, 300):
+        at = torch.full((2,), place, dtype=torch.int32, device=cuda_device)
+        k = torch.randn((2, 4, 1, 256), generator=torch.Generator().manual_seed(place)).to(BF16)
+        cache.write(p.pool, k.to(cuda_device), zero, p.table, at)
+        y, s = decode.quantise(k)
+        p.k[:, :, place:place + 1] = torch.as_tensor(y * s[..., None])
+        p.v[:, :, place] = 0.0
+    out, lse = p.attend()
+    p.check(out, lse)
+    for b in range(2):  # the scale of one of them by the user's own rule
+        p.pool.v_scale[p.table[b, 5 // 32], :, 5 % 32] = 0.0
+    again, lse2 = p.attend()
+    p.check(again, lse2)
 
 
 @pytest.mark.parametrize("dtype,kind", PAIRS[:3], ids=IDS[:3])
