@@ -105,16 +105,22 @@ __device__ __forceinline__ float e4m3_row_scale(float amax) {
   return __uint_as_float(uint32_t(e + 127) << 23);
 }
 
-// Page index of token `j`; -1 when the table or the pool does not hold it (recorded).
-__device__ __forceinline__ int page_of(const CacheView& c, const int32_t* table, int64_t max_pages, int64_t j) {
+// Page index of token `j`: the table's entry (-1 outside the table), which page_checked turns
+// into -1 when the pool does not hold it (recorded).  In two steps, so that the entry can be
+// loaded ahead of its use.
+__device__ __forceinline__ int page_entry(const CacheView& c, const int32_t* table, int64_t max_pages, int64_t j) {
   const int64_t slot = j >> c.page_shift;
-  int page = -1;
-  if (j >= 0 && slot < max_pages) page = __ldg(table + slot);
+  return j >= 0 && slot < max_pages ? __ldg(table + slot) : -1;
+}
+__device__ __forceinline__ int page_checked(const CacheView& c, int page) {
   if (page < 0 || page >= c.n_pages) {
     set_status(c.status, GQA_ERR_DEVICE_BOUNDS);
     return -1;
   }
   return page;
+}
+__device__ __forceinline__ int page_of(const CacheView& c, const int32_t* table, int64_t max_pages, int64_t j) {
+  return page_checked(c, page_entry(c, table, max_pages, j));
 }
 
 // cos and sin of the eight pairs of a rotated unit at position p, times m.  p * turns

@@ -12,9 +12,7 @@
 // and probabilities, lazy maxima and values that a mask hides: as in tree_tc.cu.
 //
 // Warps: 16 for the softmax (lane quarter x 32 keys), a producer, one that fetches the keys'
-// scales, two issuers.  A bf16 tile is four slots: the keys' columns 0 - 127 and 128 - 255 ([2][128
-// keys][128 bytes]), then the values of keys 0 - 63 and 64 - 127 ([4][64 keys][128 bytes]),
-// so that one product spans all 256 columns; an e4m3 tile is two ([2][128 keys][128 bytes]).
+// scales, two issuers.
 #include "tree_tc.cuh"
 
 namespace gqa {
@@ -25,16 +23,15 @@ constexpr int kSoftWarps = 16;
 
 template <bool kFp8>
 struct RowsCfg {
-  static constexpr int kPer = kFp8 ? 1 : 2;                        // slots of a tile's keys, and of its values
-  static constexpr int kKSlots = 2, kVSlots = kFp8 ? 2 : 3;        // what shared memory has room for
-  static constexpr int kIssuer = kSoftWarps + 2;                   // after the producer and the keys' warp: 20 warps
-                                                                   // leave 96 registers a thread, 21 only 80
+  static constexpr int kKSlots = kFp8 ? 4 : 5, kVSlots = 5;  // what shared memory has room for
+  static constexpr int kIssuer = kSoftWarps + 2;  // after the producer and the keys' warp: 20 warps leave 96
+                                                  // registers a thread, 21 only 80
   static constexpr int kThreads = 32 * (kIssuer + 2);
   static constexpr int kOffQ = 0;  // bf16 [4][128 rows][128 bytes], or e4m3 [2 pieces][2][128 rows][128 bytes]
   static constexpr int kOffK = kRows * 512;
   static constexpr int kOffV = kOffK + kKSlots * kSlotBytes;
   static constexpr int kOffBar = kOffV + kVSlots * kSlotBytes;
-  static constexpr int kOffStart = kOffBar + 8 * 22;  // the worker's cursor, the TMEM address
+  static constexpr int kOffStart = kOffBar + 8 * 32;  // the worker's cursor, the TMEM address
   static constexpr int kOffBad = kOffStart + 48;      // 32 words: drafted tokens with a value that is not finite
   static constexpr int kOffThere = kOffBad + 128;     // [2][4] words: which keys of the tile are there
   static constexpr int kOffRed = kOffThere + 32;      // [4 parts][128 rows] exchange
@@ -54,9 +51,9 @@ enum {
   kRBarKeys = 7,
   kRBarDrain = 9,
   kRBarKFull = 10,
-  kRBarKEmpty = 13,
-  kRBarVFull = 16,
-  kRBarVEmpty = 19
+  kRBarKEmpty = 15,
+  kRBarVFull = 20,
+  kRBarVEmpty = 25
 };
 
 // Eight consecutive 32-bit columns of raw words into this thread's TMEM lane.
@@ -70,6 +67,7 @@ template <bool kFp8>
 __global__ void __launch_bounds__(RowsCfg<kFp8>::kThreads, 1) tree_rows_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v,
                  const __grid_constant__ TreeParams p) {
   using F = RowsCfg<kFp8>;
+  using I = Items<kFp8>;
   extern __shared__ __align__(1024) char smem_raw[];
   const uint32_t sbase = smem_u32(smem_raw);
   const bool misaligned = (sbase & 1023u) != 0;  // the swizzle needs it; never expected to fail
@@ -120,11 +118,8 @@ __global__ void __launch_bounds__(RowsCfg<kFp8>::kThreads, 1) tree_rows_kernel(c
   if (misaligned) {
     // no role
   } else if (warp == kSoftWarps) {
-    Feed<kFp8, false, F::kKSlots> k;
-    Feed<kFp8, !kFp8, F::kVSlots> v;
-    k.begin(p, cur, &map_k, sK, bar(kRBarKFull), bar(kRBarKEmpty));
-    v.begin(p, cur, &map_v, sV, bar(kRBarVFull), bar(kRBarVEmpty));
-    produce(p, k, v);
+    produce<Feed<kFp8, false, F::kKSlots>, Feed<kFp8, true, F::kVSlots>>(
+        p, cur, &map_k, &map_v, sK, sV, bar(kRBarKFull), bar(kRBarKEmpty), bar(kRBarVFull), bar(kRBarVEmpty));
   } else if (warp == kSoftWarps + 1) {
     // ---------------------------------------------------------------- keys
     // Lane i looks after keys i, 32 + i, 64 + i and 96 + i of each tile: which are there, and
@@ -134,30 +129,37 @@ __global__ void __launch_bounds__(RowsCfg<kFp8>::kThreads, 1) tree_rows_kernel(c
     bool ok = true;
     while (ok && tree_next(p, cur, &g)) {
       const int32_t* table = p.table + int64_t(g.b) * p.max_pages;
-      int page[4], page_next[4];
+      int page[4], entry_next[4];
       float ks[4], vs[4];
-      auto pages_at = [&](int tile, int (&pg)[4]) {
+      auto entries_at = [&](int tile, int (&e)[4]) {
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           const uint32_t j = uint32_t(tile) * kTreeTile + i * 32 + lane;
-          pg[i] = tile < g.t1 && j < g.s.keys ? page_of(p.c, table, p.max_pages, j) : -1;
+          e[i] = tile < g.t1 && j < g.s.keys ? page_entry(p.c, table, p.max_pages, j) : -1;
         }
       };
-      auto scales_at = [&](int tile, const int (&pg)[4]) {
+      auto checked = [&](int tile, const int (&e)[4]) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          page[i] =
+              tile < g.t1 && uint32_t(tile) * kTreeTile + i * 32 + lane < g.s.keys ? page_checked(p.c, e[i]) : -1;
+      };
+      auto scales_at = [&](int tile) {
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           ks[i] = 0.f, vs[i] = 1.f;
-          if (kFp8 && pg[i] >= 0) {
-            const int64_t at = (int64_t(pg[i]) * p.c.Hkv + g.h) * (slot_mask + 1) +
+          if (kFp8 && page[i] >= 0) {
+            const int64_t at = (int64_t(page[i]) * p.c.Hkv + g.h) * (slot_mask + 1) +
                                ((uint32_t(tile) * kTreeTile + i * 32 + lane) & slot_mask);
             ks[i] = p.c.ks[at];
             vs[i] = p.c.vs[at];
           }
         }
       };
-      pages_at(g.t0, page);
-      pages_at(g.t0 + 1, page_next);
-      scales_at(g.t0, page);
+      entries_at(g.t0, entry_next);
+      checked(g.t0, entry_next);
+      entries_at(g.t0 + 1, entry_next);
+      scales_at(g.t0);
       for (int tile = g.t0; tile < g.t1; ++tile, ++tt) {
         const uint32_t b = tt & 1u;
         float k_now[4], v_now[4];
@@ -169,10 +171,9 @@ __global__ void __launch_bounds__(RowsCfg<kFp8>::kThreads, 1) tree_rows_kernel(c
         }
         const bool one = kFp8 && ((page[0] >= 0 && vs[0] == 1.f) || (page[1] >= 0 && vs[1] == 1.f) ||
                                   (page[2] >= 0 && vs[2] == 1.f) || (page[3] >= 0 && vs[3] == 1.f));
-#pragma unroll
-        for (int i = 0; i < 4; ++i) page[i] = page_next[i];
-        scales_at(tile + 1, page);
-        pages_at(tile + 2, page_next);
+        checked(tile + 1, entry_next);
+        scales_at(tile + 1);
+        entries_at(tile + 2, entry_next);
         // The softmax has read what the buffer held for tile t - 2.
         if (tt >= 2) ok = warp_wait(bar(kRBarP + int(b)), ((tt - 2) >> 1) & 1u, budget, status);
         if constexpr (kFp8) {
@@ -182,18 +183,20 @@ __global__ void __launch_bounds__(RowsCfg<kFp8>::kThreads, 1) tree_rows_kernel(c
             // and the one two before that, which the same barrier counts.
             if (tt >= 3) ok = warp_wait(bar(kRBarPV + int((tt - 3) & 1u)), ((tt - 3) >> 1) & 1u, budget, status) && ok;
             if (tt > 0) ok = warp_wait(bar(kRBarPV + int((tt - 1) & 1u)), ((tt - 1) >> 1) & 1u, budget, status) && ok;
-            ok = ok && warp_wait(bar(kRBarVFull + int(tt % F::kVSlots)), (tt / F::kVSlots) & 1u, budget, status);
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
+            for (int i = 0; i < 4; ++i) {
+              const uint32_t it = I::kTile * tt + uint32_t(i * 32 / I::kVKeys), slot = it % F::kVSlots;
+              ok = ok && warp_wait(bar(kRBarVFull + int(slot)), (it / F::kVSlots) & 1u, budget, status);
               if (ok && v_now[i] == 1.f && ((there[i] >> lane) & 1u)) {
                 uint32_t any = 0;
                 for (int c = 0; c < 16; ++c) {
-                  const uint4 v = lds16(sV + (tt % F::kVSlots) * uint32_t(kSlotBytes) + uint32_t(c >> 3) * kChunk +
-                                        uint32_t(i * 32 + lane) * 128u + uint32_t((c & 7) << 4));
+                  const uint4 v = lds16(sV + slot * uint32_t(kSlotBytes) + uint32_t(c >> 3) * I::kVBlock +
+                                        uint32_t((i * 32 + lane) % I::kVKeys) * 128u + uint32_t((c & 7) << 4));
                   any |= (v.x | v.y | v.z | v.w) & 0x7f7f7f7fu;
                 }
                 if (any == 0) v_now[i] = 0.f;
               }
+            }
             __syncwarp();
           }
           float* sc = sh_scale + b * 384;
@@ -232,33 +235,31 @@ __global__ void __launch_bounds__(RowsCfg<kFp8>::kThreads, 1) tree_rows_kernel(c
           const uint32_t slots = is_s ? F::kKSlots : F::kVSlots;
           const uint32_t full = bar(is_s ? kRBarKFull : kRBarVFull), empty = bar(is_s ? kRBarKEmpty : kRBarVEmpty);
           const uint32_t sbuf = tmem + 256u + b * 128u;
-#pragma unroll
-          for (int part = 0; part < F::kPer; ++part) {
-            const uint32_t item = F::kPer * tt + part, slot = item % slots;
+#pragma unroll 1
+          for (uint32_t i = 0; i < I::kTile; ++i) {
+            const uint32_t item = I::kTile * tt + i, slot = item % slots;
             ok = ok && mbar_wait_inline(full + 8u * slot, (item / slots) & 1u, budget, status);
             if (!ok) break;
             umma::fence_after_sync();
             const uint32_t base = (is_s ? sK : sV) + slot * uint32_t(kSlotBytes);
             if (is_s) {
+              // column block i of Q against that of the keys: four steps of 32 bytes
               const uint64_t dk = umma::smem_desc(base, 16, 1024);
 #pragma unroll
-              for (int k = 0; k < 8; ++k) {
-                const uint32_t a = uint32_t(k >> 2) * kChunk + uint32_t(k & 3) * 32u;
+              for (uint32_t k = 0; k < 4; ++k)
 #pragma unroll
-                for (int piece = 0; piece < (kFp8 ? 2 : 1); ++piece)
-                  mma<kFp8>(sbuf, umma::desc_add(dq, a + uint32_t(kFp8 ? piece : part) * (2 * kChunk)),
-                            umma::desc_add(dk, a), id_s, (part | k | piece) != 0);
-              }
+                for (uint32_t piece = 0; piece < (kFp8 ? 2 : 1); ++piece)
+                  mma<kFp8>(sbuf, umma::desc_add(dq, (i + 2 * piece) * (kRows * 128u) + k * 32u),
+                            umma::desc_add(dk, k * 32u), id_s, (i | k | piece) != 0);
             } else {
-              const uint64_t dv = umma::smem_desc(base, kFp8 ? kChunk : kSlotBytes / 4, 1024);
+              // the slot's keys in two steps, all columns of the values
+              const uint64_t dv = umma::smem_desc(base, I::kVBlock, 1024);
 #pragma unroll
-              for (int k = 0; k < 4; ++k) {
+              for (uint32_t k = 0; k < 2; ++k)
 #pragma unroll
-                for (int piece = 0; piece < (kFp8 ? 2 : 1); ++piece)
-                  mma_ts<kFp8>(tmem, sbuf + uint32_t(kFp8 ? 32 * piece : 32 * part) + 8u * uint32_t(k),
-                               umma::desc_add(dv, uint32_t(k) * (kFp8 ? 4096u : 2048u)), id_o,
-                               tile > g.t0 || (part | k | piece) != 0);
-              }
+                for (uint32_t piece = 0; piece < (kFp8 ? 2 : 1); ++piece)
+                  mma_ts<kFp8>(tmem, sbuf + 32u * piece + 8u * (2 * i + k), umma::desc_add(dv, k * I::kStep), id_o,
+                               tile > g.t0 || (i | k | piece) != 0);
             }
             umma::commit(empty + 8u * slot);
           }
@@ -309,7 +310,7 @@ __global__ void __launch_bounds__(RowsCfg<kFp8>::kThreads, 1) tree_rows_kernel(c
         for (int i = 0; i < 4; ++i) {
           const int rq = r0 + i * kSoftWarps;
           if constexpr (!kFp8) {
-            sts16(sQ + uint32_t(lane >> 3) * kChunk + uint32_t(rq) * 128u + uint32_t(((lane & 7) ^ (rq & 7)) << 4), u[i]);
+            sts16(sQ + uint32_t(lane >> 3) * (kRows * 128u) + uint32_t(rq) * 128u + uint32_t(((lane & 7) ^ (rq & 7)) << 4), u[i]);
           } else {
             const float f = put_query<kRows, false>(u[i], sQ, rq);
             if (lane == 0) sh_f[rq] = f * p.scale_log2;
@@ -325,22 +326,21 @@ __global__ void __launch_bounds__(RowsCfg<kFp8>::kThreads, 1) tree_rows_kernel(c
       const bool live = t < g.s.drafted;
 
       const int key = part * 32 + lane;  // the key whose values this thread mends (quarter 0)
-      float m = kNoMax, l = 0.f;  // this row's maximum (the same in all parts), this part's share of its sum
+      float m = -1e30f, l = 0.f;  // this row's maximum (the same in all parts), this part's share of its sum
       for (int tile = g.t0; tile < g.t1; ++tile, ++tt) {
         const uint32_t sb = tt & 1u, ph = (tt >> 1) & 1u;
         const uint32_t j0 = uint32_t(tile) * kTreeTile + part * 32;
         bool fine = ok;
-        // Key k's values are in their slot.  The product of the tile before is over first, so that
-        // the barrier stands at no earlier use of the slot.
-        auto value_there = [&](int k) {
+        // The values of keys 32 part .. + 31 are in their slot.  The product of the tile before is over
+        // first, so that the barrier stands at no earlier use of the slot.
+        const uint32_t v_item = I::kTile * tt + uint32_t(part * 32 / I::kVKeys);
+        auto values_there = [&]() {
           if (tt > 0 && !warp_wait(bar(kRBarPV + int((tt - 1) & 1u)), ((tt - 1) >> 1) & 1u, budget, status)) return false;
-          const uint32_t it = F::kPer * tt + (kFp8 ? 0 : uint32_t(k >> 6));
-          return warp_wait(bar(kRBarVFull + int(it % F::kVSlots)), (it / F::kVSlots) & 1u, budget, status);
+          return warp_wait(bar(kRBarVFull + int(v_item % F::kVSlots)), (v_item / F::kVSlots) & 1u, budget, status);
         };
-        auto value_unit = [&](int k, int c) {  // 16-byte unit c of key k's values, in any order
-          const uint32_t it = F::kPer * tt + (kFp8 ? 0 : uint32_t(k >> 6));
-          return sV + (it % F::kVSlots) * uint32_t(kSlotBytes) + uint32_t(c >> 3) * (kFp8 ? kChunk : kSlotBytes / 4) +
-                 uint32_t(kFp8 ? k : k & 63) * 128u + uint32_t(((c ^ k) & 7) << 4);
+        auto value_unit = [&](int c) {  // 16-byte unit c of this thread's key's values, in any order
+          return sV + (v_item % F::kVSlots) * uint32_t(kSlotBytes) + uint32_t(c >> 3) * I::kVBlock +
+                 uint32_t(key % I::kVKeys) * 128u + uint32_t(((c ^ key) & 7) << 4);
         };
         if (idle) {  // its rows of S and O are nobody's; the tiles are counted
           ok = warp_wait(bar(kRBarS + int(sb)), ph, budget, status);
@@ -363,11 +363,11 @@ __global__ void __launch_bounds__(RowsCfg<kFp8>::kThreads, 1) tree_rows_kernel(c
         // Values that take no part, as in tree_tc.cu.  Quarter 0's warps look after the 128 keys.
         const bool gone = !((there >> lane) & 1u), drafted = !gone && p.T > 1 && j0 + lane >= g.s.ctx;
         if (quarter == 0 && __any_sync(0xffffffffu, gone || drafted)) {
-          fine = value_there(part * 32) && fine;
+          fine = values_there() && fine;
           if (fine && (gone || drafted)) {
             uint32_t bad = 0;
 #pragma unroll 1
-            for (int c = 0; c < (kFp8 ? 16 : 32); ++c) bad |= mend_unit<kFp8>(value_unit(key, c), gone);
+            for (int c = 0; c < (kFp8 ? 16 : 32); ++c) bad |= mend_unit<kFp8>(value_unit(c), gone);
             const int u = int(j0 + lane - g.s.ctx);
             if (bad) atomicOr(&sh_bad[u >> 5], 1u << (u & 31));
           }
@@ -532,9 +532,7 @@ template <bool kFp8>
 int launch(const TreeParams& p, cudaStream_t stream) {
   using F = RowsCfg<kFp8>;
   CUtensorMap mk, mv;
-  const int most = kFp8 ? 7 : 6;  // bf16 values come in halves of 64 keys
-  if (!encode_pages(&mk, p.c, p.c.k, 1 << (p.c.page_shift < 7 ? p.c.page_shift : 7)) ||
-      !encode_pages(&mv, p.c, p.c.v, 1 << (p.c.page_shift < most ? p.c.page_shift : most)))
+  if (!encode_pages(&mk, p.c, p.c.k, box_rows(p.c, false)) || !encode_pages(&mv, p.c, p.c.v, box_rows(p.c, true)))
     return GQA_ERR_LAUNCH;
   if (cudaFuncSetAttribute(tree_rows_kernel<kFp8>, cudaFuncAttributeMaxDynamicSharedMemorySize, F::kSmem) != cudaSuccess)
     return GQA_ERR_LAUNCH;

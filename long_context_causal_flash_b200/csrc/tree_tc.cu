@@ -23,7 +23,7 @@
 // to 2^-8 of the first maximum, and is off by at most 2^-14 of it below.
 //
 // Warps: 4 softmax warps per 32 (or 16) rows, a producer (TMA, through the page table, into
-// rings of 32 KiB slots), and two warps whose first lanes issue the products.
+// rings of 16 KiB slots), and two warps whose first lanes issue the products.
 #include "tree_tc.cuh"
 
 namespace gqa {
@@ -34,11 +34,10 @@ struct Cfg {
   static constexpr int kCols = kN < 32 ? kN : 32;  // rows of a softmax thread
   static constexpr int kParts = kN / kCols;
   static constexpr int kSoftWarps = 4 * kParts;
-  static constexpr int kNN = kFp8 ? 2 * kN : kN;            // N of a product: e4m3 pieces lie side by side
-  static constexpr int kPer = kFp8 ? 1 : 2;                 // slots of a tile's keys, and of its values
-  static constexpr int kQBytes = kN * 512;                  // bf16, or two e4m3 pieces
-  static constexpr int kPBytes = kChunk;
-  static constexpr int kKSlots = kN > 32 ? 2 : 3, kVSlots = 3;  // what shared memory has room for
+  static constexpr int kNN = kFp8 ? 2 * kN : kN;  // N of a product: e4m3 pieces lie side by side
+  static constexpr int kQBytes = kN * 512;        // bf16, or two e4m3 pieces
+  static constexpr int kPBytes = 16384;           // [128 keys][128 bytes]
+  static constexpr int kKSlots = kN > 32 ? 5 : 6, kVSlots = 6;  // what shared memory has room for
   static constexpr int kIssuer = kSoftWarps + 1;  // the S issuer's warp, after the producer; then the O issuer's
   static constexpr int kWarps = kIssuer + 2;
   static constexpr int kThreads = 32 * kWarps;
@@ -47,7 +46,7 @@ struct Cfg {
   static constexpr int kOffK = kOffP + kPBytes;
   static constexpr int kOffV = kOffK + kKSlots * kSlotBytes;
   static constexpr int kOffBar = kOffV + kVSlots * kSlotBytes;
-  static constexpr int kOffM = kOffBar + 256;     // [kN] maxima
+  static constexpr int kOffM = kOffBar + 288;     // [kN] maxima
   static constexpr int kOffF = kOffM + kN * 4;    // [kN] factor of a row's scores (e4m3 pages)
   static constexpr int kOffBad = kOffF + kN * 4;  // 32 words: drafted tokens with a value that is not finite
   static constexpr int kSmem = kOffBad + 128;
@@ -55,6 +54,7 @@ struct Cfg {
   static constexpr uint32_t kTmem = 4 * kNN;
   static_assert(kSmem <= 232448 - 1024, "shared memory per block");
 };
+
 // Barriers: S^T, its release, P and O per parity of the tile; the rings' slots.
 enum {
   kBarQ = 0,
@@ -64,9 +64,9 @@ enum {
   kBarPV = 7,
   kBarDrain = 9,
   kBarKFull = 10,
-  kBarKEmpty = 13,
-  kBarVFull = 16,
-  kBarVEmpty = 19
+  kBarKEmpty = 16,
+  kBarVFull = 22,
+  kBarVEmpty = 28
 };
 
 // Sum or maximum over the 32 lanes of each of 16 values: lane l ends with value l / 2.  A
@@ -89,10 +89,21 @@ __device__ __forceinline__ float lanes_reduce(float (&v)[16]) {
   return kMax ? fmaxf(v[0], got) : v[0] + got;
 }
 
+// Four consecutive fp32 columns of this thread's TMEM lane (warp-collective).
+__device__ __forceinline__ void tmem_ld4(uint32_t taddr, float (&v)[4]) {
+  uint32_t r[4];
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x4.b32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(taddr));
+#pragma unroll
+  for (int i = 0; i < 4; ++i) v[i] = __uint_as_float(r[i]);
+}
+
 template <int kN, bool kFp8>
 __global__ void __launch_bounds__(Cfg<kN, kFp8>::kThreads, 1) tree_tc_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v,
                const __grid_constant__ TreeParams p) {
   using F = Cfg<kN, kFp8>;
+  using I = Items<kFp8>;
   constexpr int C = F::kCols;
   extern __shared__ __align__(1024) char smem_raw[];
   __shared__ TreeCursor start;
@@ -144,11 +155,8 @@ __global__ void __launch_bounds__(Cfg<kN, kFp8>::kThreads, 1) tree_tc_kernel(con
   if (misaligned) {
     // no role
   } else if (warp == F::kSoftWarps) {
-    Feed<kFp8, false, F::kKSlots> k;
-    Feed<kFp8, false, F::kVSlots> v;
-    k.begin(p, cur, &map_k, sK, bar(kBarKFull), bar(kBarKEmpty));
-    v.begin(p, cur, &map_v, sV, bar(kBarVFull), bar(kBarVEmpty));
-    produce(p, k, v);
+    produce<Feed<kFp8, false, F::kKSlots>, Feed<kFp8, true, F::kVSlots>>(
+        p, cur, &map_k, &map_v, sK, sV, bar(kBarKFull), bar(kBarKEmpty), bar(kBarVFull), bar(kBarVEmpty));
   } else if (warp >= F::kIssuer) {
     // ---------------------------------------------------------------- MMA issuers
     // One thread issues every S^T = K Q^T, another every O^T += V^T P^T, so that neither
@@ -156,8 +164,7 @@ __global__ void __launch_bounds__(Cfg<kN, kFp8>::kThreads, 1) tree_tc_kernel(con
     if (lane == 0) {
       const bool is_s = warp == F::kIssuer;
       constexpr uint32_t id_s = idesc<kFp8>(F::kNN, 0, 0), id_o = idesc<kFp8>(F::kNN, 1, 1);
-      constexpr int kRowSteps = kFp8 ? 4 : 8;  // K steps of O: 32 or 16 keys each
-      const uint64_t dq = umma::smem_desc(sQ, 16, 1024), dp = umma::smem_desc(sP, kChunk, 1024);
+      const uint64_t dq = umma::smem_desc(sQ, 16, 1024), dp = umma::smem_desc(sP, 16384, 1024);
       uint32_t tt = 0, segs = 0;  // tiles issued
       bool ok = true;
       while (ok && tree_next(p, cur, &g)) {
@@ -172,32 +179,32 @@ __global__ void __launch_bounds__(Cfg<kN, kFp8>::kThreads, 1) tree_tc_kernel(con
             ok = mbar_wait_inline(bar(kBarP + int(b)), ph, budget, status);
           const uint32_t slots = is_s ? F::kKSlots : F::kVSlots;
           const uint32_t full = bar(is_s ? kBarKFull : kBarVFull), empty = bar(is_s ? kBarKEmpty : kBarVEmpty);
-#pragma unroll
-          for (int part = 0; part < 2; ++part) {  // halves of the key's columns, or of the value's
-            const uint32_t item = kFp8 ? tt : 2 * tt + part, slot = item % slots;
-            if ((!kFp8 || part == 0) && ok) ok = mbar_wait_inline(full + 8u * slot, (item / slots) & 1u, budget, status);
+#pragma unroll 1
+          for (uint32_t i = 0; i < I::kTile; ++i) {
+            const uint32_t item = I::kTile * tt + i, slot = item % slots;
+            ok = ok && mbar_wait_inline(full + 8u * slot, (item / slots) & 1u, budget, status);
             if (!ok) break;
             umma::fence_after_sync();
             const uint32_t base = (is_s ? sK : sV) + slot * uint32_t(kSlotBytes);
             if (is_s) {
+              // column block i of the keys against that of Q: four steps of 32 bytes
               const uint64_t dk = umma::smem_desc(base, 16, 1024);
 #pragma unroll
-              for (int k = kFp8 ? 4 * part : 0; k < (kFp8 ? 4 * part + 4 : 8); ++k) {
-                // 32-byte step k & 3 of column block k / 4
-                const uint32_t a = uint32_t(k >> 2) * kChunk + uint32_t(k & 3) * 32u;
-                const uint32_t q = uint32_t((kFp8 ? 0 : 2 * part) + (k >> 2)) * (F::kNN * 128u) + uint32_t(k & 3) * 32u;
-                mma<kFp8>(tmem + b * F::kNN, umma::desc_add(dk, a), umma::desc_add(dq, q), id_s, (part | k) != 0);
-              }
+              for (uint32_t k = 0; k < 4; ++k)
+                mma<kFp8>(tmem + b * F::kNN, umma::desc_add(dk, k * 32u), umma::desc_add(dq, i * (F::kNN * 128u) + k * 32u),
+                          id_s, (i | k) != 0);
             } else {
-              const uint64_t dv = umma::smem_desc(base + (kFp8 ? uint32_t(part) * kChunk : 0u), kChunk, 1024);
+              // the slot's keys, in two steps, for both halves of the values' columns
 #pragma unroll
-              for (int k = 0; k < kRowSteps; ++k) {
-                const uint32_t rows = uint32_t(k) * (kFp8 ? 4096u : 2048u);
-                mma<kFp8>(tmem + uint32_t(2 + part) * F::kNN, umma::desc_add(dv, rows), umma::desc_add(dp, rows), id_o,
-                          tile > g.t0 || k != 0);
+              for (uint32_t half = 0; half < 2; ++half) {
+                const uint64_t dv = umma::smem_desc(base + half * (kSlotBytes / 2), I::kVBlock, 1024);
+#pragma unroll
+                for (uint32_t k = 0; k < 2; ++k)
+                  mma<kFp8>(tmem + (2 + half) * F::kNN, umma::desc_add(dv, k * I::kStep),
+                            umma::desc_add(dp, (2 * i + k) * I::kStep), id_o, tile > g.t0 || (i | k) != 0);
               }
             }
-            if (!kFp8 || part == 1) umma::commit(empty + 8u * slot);
+            umma::commit(empty + 8u * slot);
           }
           if (ok) umma::commit(bar((is_s ? kBarS : kBarPV) + int(b)));
         }
@@ -267,7 +274,7 @@ __global__ void __launch_bounds__(Cfg<kN, kFp8>::kThreads, 1) tree_tc_kernel(con
           }
         }
       }
-      if (quarter == 0 && lane < C) sh_m[n0 + lane] = kNoMax;
+      if (quarter == 0 && lane < C) sh_m[n0 + lane] = 0.f;
       if (warp == 0) sh_bad[lane] = 0;
       fence_proxy_async_smem();
       __syncwarp();
@@ -278,13 +285,15 @@ __global__ void __launch_bounds__(Cfg<kN, kFp8>::kThreads, 1) tree_tc_kernel(con
 #pragma unroll
       for (int i = 0; i < C; ++i) l[i] = 0.f;
 
-      // The key's page two tiles ahead and its scales one tile ahead of their use: neither
-      // load, the second through the first, is waited for.
-      auto page_at = [&](int tile) {
+      // The key's page table entry two tiles ahead and its scales one tile ahead of their use:
+      // neither load, the second through the first, is waited for.
+      auto entry_at = [&](int tile) {
         const uint32_t j = uint32_t(tile) * kTreeTile + key;
-        return tile < g.t1 && j < g.s.keys ? page_of(p.c, table, p.max_pages, j) : -1;
+        return tile < g.t1 && j < g.s.keys ? page_entry(p.c, table, p.max_pages, j) : -1;
       };
-      int page = page_at(g.t0), page_next = page_at(g.t0 + 1);
+      auto checked = [&](int tile, int entry) {
+        return tile < g.t1 && uint32_t(tile) * kTreeTile + key < g.s.keys ? page_checked(p.c, entry) : -1;
+      };
       auto scales_at = [&](int tile, int page, float* ks, float* vs) {
         if (kFp8 && page >= 0) {
           const int64_t at =
@@ -293,9 +302,13 @@ __global__ void __launch_bounds__(Cfg<kN, kFp8>::kThreads, 1) tree_tc_kernel(con
           *vs = p.c.vs[at];
         }
       };
+      int page = checked(g.t0, entry_at(g.t0)), entry_next = entry_at(g.t0 + 1);
       float ks_next = 0.f, vs_next = 1.f;
       scales_at(g.t0, page, &ks_next, &vs_next);
+      uint32_t fresh = (1u << (C / 16)) - 1;  // sixteens of rows, some of which have seen no key yet
+      uint32_t has = 0;                       // lane n: whether row 16 i + n has, bit i
 
+#pragma unroll 1
       for (int tile = g.t0; tile < g.t1; ++tile, ++tt) {
         const uint32_t sb = tt & 1u, ph = (tt >> 1) & 1u;
         const uint32_t j = uint32_t(tile) * kTreeTile + key;
@@ -303,25 +316,23 @@ __global__ void __launch_bounds__(Cfg<kN, kFp8>::kThreads, 1) tree_tc_kernel(con
         auto last_product = [&]() {
           return tt == 0 || warp_wait(bar(kBarPV + int((tt - 1) & 1u)), ((tt - 1) >> 1) & 1u, budget, status);
         };
-        // This tile's values are in their slots.  The product before is over first, so that the
-        // barriers stand at no earlier use of the slots.
+        // The values of this warp's keys are in their slot.  The product before is over first, so
+        // that the barrier stands at no earlier use of the slot.
+        const uint32_t v_item = I::kTile * tt + uint32_t(quarter * 32 / I::kVKeys);
         auto values_there = [&]() {
-          bool there = last_product();
-#pragma unroll
-          for (uint32_t it = F::kPer * tt; it < F::kPer * tt + F::kPer; ++it)
-            there = there && warp_wait(bar(kBarVFull + int(it % F::kVSlots)), (it / F::kVSlots) & 1u, budget, status);
-          return there;
+          return last_product() &&
+                 warp_wait(bar(kBarVFull + int(v_item % F::kVSlots)), (v_item / F::kVSlots) & 1u, budget, status);
         };
         auto value_unit = [&](int c) {  // 16-byte unit c of the key's values, in any order
-          return sV + ((F::kPer * tt + uint32_t(c >> 4)) % F::kVSlots) * uint32_t(kSlotBytes) +
-                 uint32_t((c >> 3) & 1) * kChunk + uint32_t(key) * 128u + uint32_t(((c ^ key) & 7) << 4);
+          return sV + (v_item % F::kVSlots) * uint32_t(kSlotBytes) + uint32_t(c >> 3) * I::kVBlock +
+                 uint32_t(key % I::kVKeys) * 128u + uint32_t(((c ^ key) & 7) << 4);
         };
         const float ks = kFp8 ? (page < 0 ? 0.f : ks_next) : p.scale_log2;
         float vs = kFp8 && page >= 0 ? vs_next : 1.f, lvs = 0.f, inv_vs = 1.f;
         const int page_now = page;
-        page = page_next;
+        page = checked(tile + 1, entry_next);
         scales_at(tile + 1, page, &ks_next, &vs_next);
-        page_next = page_at(tile + 2);
+        entry_next = entry_at(tile + 2);
         // Which of this thread's rows see the key: all, unless it is not there or is drafted.
         const bool drafted = page_now >= 0 && j >= g.s.ctx;
         uint32_t vis = page_now >= 0 ? 0xffffffffu : 0u;
@@ -363,7 +374,7 @@ __global__ void __launch_bounds__(Cfg<kN, kFp8>::kThreads, 1) tree_tc_kernel(con
           if (fine && (page_now < 0 || (drafted && p.T > 1))) {
             uint32_t bad = 0;
 #pragma unroll 1
-            for (int c = 0; c < 16 * F::kPer; ++c) bad |= mend_unit<kFp8>(value_unit(c), page_now < 0);
+            for (int c = 0; c < (kFp8 ? 16 : 32); ++c) bad |= mend_unit<kFp8>(value_unit(c), page_now < 0);
             const int u = int(j - g.s.ctx);
             if (bad) atomicOr(&sh_bad[u >> 5], 1u << (u & 31));
           }
@@ -375,79 +386,72 @@ __global__ void __launch_bounds__(Cfg<kN, kFp8>::kThreads, 1) tree_tc_kernel(con
         bool stop = false;
 #pragma unroll
         for (int c0 = 0; c0 < C; c0 += 16) {
-          // Scores of the rows n0 + c0 .. + 15, in powers of two.
-          auto scores = [&](float (&x)[16]) {
-            umma::tmem_ld16(lane_addr + sb * F::kNN + uint32_t(c0), x);
+          // Scores of the rows n0 + c0 .. + 15 less their maxima so far, in powers of two.  The code is
+          // written to be short: a CTA runs it first from a cold instruction cache.
+          float x[16];
+          umma::tmem_ld16(lane_addr + sb * F::kNN + uint32_t(c0), x);
+          if constexpr (kFp8) {
+            float y[16];
+            umma::tmem_ld16(lane_addr + sb * F::kNN + kN + uint32_t(c0), y);
+            umma::tmem_wait_ld();
+#pragma unroll
+            for (int i = 0; i < 16; ++i) x[i] += y[i];
+          } else {
+            umma::tmem_wait_ld();
+          }
+          float top[4];
+#pragma unroll
+          for (int i = 0; i < 16; i += 4) {
+            const float4 m = *reinterpret_cast<const float4*>(sh_m + n0 + c0 + i);
+            const float m4[4] = {m.x, m.y, m.z, m.w};
             if constexpr (kFp8) {
-              float y[16];
-              umma::tmem_ld16(lane_addr + sb * F::kNN + kN + uint32_t(c0), y);
-              umma::tmem_wait_ld();
+              const float4 f = *reinterpret_cast<const float4*>(sh_f + n0 + c0 + i);
+              const float f4[4] = {f.x, f.y, f.z, f.w};
 #pragma unroll
-              for (int i = 0; i < 16; ++i) x[i] += y[i];
+              for (int k = 0; k < 4; ++k) x[i + k] = fmaf(x[i + k], ks * f4[k], lvs - m4[k]);
             } else {
-              umma::tmem_wait_ld();
-            }
 #pragma unroll
-            for (int i = 0; i < 16; i += 4) {
-              if constexpr (kFp8) {
-                const float4 f = *reinterpret_cast<const float4*>(sh_f + n0 + c0 + i);
-                x[i] = fmaf(x[i], ks * f.x, lvs);
-                x[i + 1] = fmaf(x[i + 1], ks * f.y, lvs);
-                x[i + 2] = fmaf(x[i + 2], ks * f.z, lvs);
-                x[i + 3] = fmaf(x[i + 3], ks * f.w, lvs);
-              } else {
-#pragma unroll
-                for (int k = 0; k < 4; ++k) x[i + k] *= ks;
-              }
+              for (int k = 0; k < 4; ++k) x[i + k] = fmaf(x[i + k], ks, -m4[k]);
             }
             if (masked) {
 #pragma unroll
-              for (int i = 0; i < 16; ++i)
-                if (!((vis >> (c0 + i)) & 1u)) x[i] = -INFINITY;
+              for (int k = 0; k < 4; ++k)
+                if (!((vis >> (c0 + i + k)) & 1u)) x[i + k] = -INFINITY;
             }
-          };
-          // 2^(x - m) with the maxima so far; the largest exponent.
-          float x[16];
-          auto weights = [&]() {
-            float top[4];
 #pragma unroll
-            for (int i = 0; i < 16; i += 4) {
-              const float4 m = *reinterpret_cast<const float4*>(sh_m + n0 + c0 + i);
-              x[i] -= m.x, x[i + 1] -= m.y, x[i + 2] -= m.z, x[i + 3] -= m.w;
-#pragma unroll
-              for (int k = 0; k < 4; ++k) top[k] = i == 0 ? x[k] : fmaxf(top[k], x[i + k]);
-            }
-            const float z = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
-#pragma unroll
-            for (int i = 0; i < 16; ++i) x[i] = ex2(x[i]);
-            return z;
-          };
-          scores(x);
-          const bool raise = weights() > F::kSlack;
-          if (any_thread(part_bar, 128, raise || !fine)) {
+            for (int k = 0; k < 4; ++k) top[k] = i == 0 ? x[k] : fmaxf(top[k], x[i + k]);
+          }
+          const bool raise = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) > F::kSlack;
+          if (any_thread(part_bar, 128, raise || !fine || ((fresh >> (c0 / 16)) & 1u))) {
             fine = last_product() && fine;
             if (any_thread(part_bar, 128, !fine)) {
               stop = true;
               break;
             }
             umma::fence_after_sync();
-            scores(x);
-            const float mx = lanes_reduce<true>(x);  // lane l: row c0 + l / 2
+            float y[16];
+#pragma unroll
+            for (int i = 0; i < 16; ++i) y[i] = x[i];
+            const float mx = lanes_reduce<true>(y);  // lane l: row c0 + l / 2
             const float v = __shfl_sync(0xffffffffu, mx, (2 * lane) & 31);
             if (lane < 16) put(c0, v);  // lane n of the quarter: row c0 + n
             sync_threads(part_bar, 128);
-            float top = 0.f, m_old = 0.f;
-            if (lane < 16) {
-              top = fmaxf(fmaxf(get(c0, 0, lane), get(c0, 1, lane)), fmaxf(get(c0, 2, lane), get(c0, 3, lane)));
-              m_old = sh_m[n0 + c0 + lane];
-            }
-            const bool up = lane < 16 && top > m_old + F::kSlack;
-            const float alpha = up ? ex2(m_old - top) : 1.f;
+            float up = -INFINITY;  // the row's largest score, above its maximum so far
+            if (lane < 16) up = fmaxf(fmaxf(get(c0, 0, lane), get(c0, 1, lane)), fmaxf(get(c0, 2, lane), get(c0, 3, lane)));
+            // The first score a row sees sets its maximum, later ones raise it.
+            const bool first = !((has >> (c0 / 16)) & 1u), rise = first ? up > -INFINITY : up > F::kSlack;
+            const float delta = rise ? up : 0.f, alpha = rise && !first ? ex2(-up) : 1.f;
+            if (rise) has |= 1u << (c0 / 16);
+            fresh &= ~(1u << (c0 / 16));
+            if (__any_sync(0xffffffffu, lane < 16 && !((has >> (c0 / 16)) & 1u))) fresh |= 1u << (c0 / 16);
             sync_threads(part_bar, 128);  // all have read the old maxima and the exchange
-            if (quarter == 0 && up) sh_m[n0 + c0 + lane] = top;
-            if (__any_sync(0xffffffffu, up)) {  // the same in the part's four warps
+            if (quarter == 0 && rise) sh_m[n0 + c0 + lane] += delta;
+            if (__any_sync(0xffffffffu, rise)) {  // the same in the part's four warps
 #pragma unroll
-              for (int i = 0; i < 16; ++i) l[c0 + i] *= __shfl_sync(0xffffffffu, alpha, i);
+              for (int i = 0; i < 16; ++i) {
+                x[i] -= __shfl_sync(0xffffffffu, delta, i);
+                l[c0 + i] *= __shfl_sync(0xffffffffu, alpha, i);
+              }
               if (tile > g.t0) {
 #pragma unroll 1
                 for (int block = 0; block < (kFp8 ? 4 : 2); ++block) {  // halves of O, and pieces
@@ -463,10 +467,10 @@ __global__ void __launch_bounds__(Cfg<kN, kFp8>::kThreads, 1) tree_tc_kernel(con
                 umma::tmem_wait_st();
               }
             }
-            sync_threads(part_bar, 128);
-            scores(x);
-            weights();
+            sync_threads(part_bar, 128);  // the new maxima are there
           }
+#pragma unroll
+          for (int i = 0; i < 16; ++i) x[i] = ex2(x[i]);
           if (c0 + 16 == C) {  // the last read of S
             umma::fence_before_sync();
             __syncwarp();
@@ -550,40 +554,36 @@ __global__ void __launch_bounds__(Cfg<kN, kFp8>::kThreads, 1) tree_tc_kernel(con
           }
         }
 #pragma unroll 1
-        for (int c0 = 0; c0 < C; c0 += 16) {
+        for (int c0 = 0; c0 < C; c0 += 4) {
           if (row0 + n0 + c0 >= rows_all) break;
-#pragma unroll 1
+          float o[2][4];
+#pragma unroll
           for (int half = 0; half < 2; ++half) {
-            float o[16];
             const uint32_t a = lane_addr + uint32_t((2 + half) * F::kNN + c0);
-            umma::tmem_ld16(a, o);
+            tmem_ld4(a, o[half]);
             if constexpr (kFp8) {
-              float y[16];
-              umma::tmem_ld16(a + kN, y);
+              float y[4];
+              tmem_ld4(a + kN, y);
               umma::tmem_wait_ld();
 #pragma unroll
-              for (int i = 0; i < 16; ++i) o[i] += y[i];
-            } else {
-              umma::tmem_wait_ld();
+              for (int i = 0; i < 4; ++i) o[half][i] += y[i];
             }
-            const int d = half * 128 + key;
+          }
+          umma::tmem_wait_ld();
 #pragma unroll
-            for (int i = 0; i < 16; ++i) {
-              const int n = c0 + i, row = row0 + n0 + n, t = row >> g_shift;
-              const float f = __shfl_sync(0xffffffffu, inv, n);
-              float v = f == 0.f ? 0.f : o[i] * f;
-              if (bad && f != 0.f) v += hidden_values<kFp8>(p, g, table, sh_bad, t, d);
-              if (row < rows_all) {
-                if (!whole) {
-                  p.o_part[(part_at + n0 + n) * kHeadDim + d] = v;
-                } else {
-                  const int64_t at = ((head_row + (row & (p.G - 1))) * p.T + t) * kHeadDim + d;
-                  if (p.out_bf16)
-                    static_cast<__nv_bfloat16*>(p.out)[at] = __float2bfloat16_rn(v);
-                  else
-                    static_cast<float*>(p.out)[at] = v;
-                }
-              }
+          for (int i = 0; i < 4; ++i) {
+            const int row = row0 + n0 + c0 + i, t = row >> g_shift;
+            const float f = __shfl_sync(0xffffffffu, inv, c0 + i);
+            const int64_t at = (whole ? (head_row + (row & (p.G - 1))) * p.T + t : part_at + n0 + c0 + i) * kHeadDim + key;
+#pragma unroll
+            for (int half = 0; half < 2; ++half) {
+              float v = f == 0.f ? 0.f : o[half][i] * f;
+              if (bad && f != 0.f) v += hidden_values<kFp8>(p, g, table, sh_bad, t, half * 128 + key);
+              if (row >= rows_all) continue;
+              if (whole)
+                static_cast<__nv_bfloat16*>(p.out)[at + half * 128] = __float2bfloat16_rn(v);
+              else
+                p.o_part[at + half * 128] = v;
             }
           }
         }
@@ -614,8 +614,8 @@ int launch_n(const TreeParams& p, const CUtensorMap& mk, const CUtensorMap& mv, 
 template <bool kFp8>
 int launch_type(const TreeParams& p, int rows, cudaStream_t stream) {
   CUtensorMap mk, mv;
-  const int box = 1 << (p.c.page_shift < 7 ? p.c.page_shift : 7);
-  if (!encode_pages(&mk, p.c, p.c.k, box) || !encode_pages(&mv, p.c, p.c.v, box)) return GQA_ERR_LAUNCH;
+  if (!encode_pages(&mk, p.c, p.c.k, box_rows(p.c, false)) || !encode_pages(&mv, p.c, p.c.v, box_rows(p.c, true)))
+    return GQA_ERR_LAUNCH;
   switch (rows) {
     case 16: return launch_n<16, kFp8>(p, mk, mv, stream);
     case 32: return launch_n<32, kFp8>(p, mk, mv, stream);

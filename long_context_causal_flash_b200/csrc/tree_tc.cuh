@@ -10,10 +10,20 @@
 namespace gqa {
 namespace {
 
-constexpr int kSlotBytes = 32768;  // 128 keys x 256 bytes: half of a bf16 tile, a whole e4m3 one
-constexpr int kChunk = 16384;      // 128 keys x 128 bytes, one swizzled column block
-constexpr float kNoMax = -1e30f;   // a row's maximum before its first visible key
+// Slots of the rings, and what lies in them.  Keys: one column block of 128 bytes of a tile's
+// 128 keys, [128 keys][128 bytes].  Values: all column blocks of 32 (bf16) or 64 (e4m3) keys,
+// [4 or 2 blocks][keys][128 bytes].  Small slots refill the rings evenly: with 32 KiB, a tile's
+// keys were two slots of a ring that held no more, and each product waited for a load that
+// could start only when the one before it was over (128 rows, bf16: 5,900 cycles a tile).
+constexpr int kSlotBytes = 16384;
 constexpr float kPScale = 16.f;  // e4m3 probabilities are stored times this: 2^4 above the maximum is 256
+template <bool kFp8>
+struct Items {
+  static constexpr int kTile = kFp8 ? 2 : 4;              // slots of a tile's keys, and of its values
+  static constexpr int kVKeys = 128 / kTile;              // keys of a value slot
+  static constexpr int kVBlock = kVKeys * 128;            // bytes from one of its column blocks to the next
+  static constexpr uint32_t kStep = kFp8 ? 4096u : 2048u;  // bytes of a product's 32 or 16 keys
+};
 
 __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, int64_t budget, int32_t* status) {
   return __all_sync(0xffffffffu, mbar_wait_inline(bar, parity, budget, status));
@@ -136,46 +146,50 @@ __device__ __forceinline__ bool mbar_test(uint32_t bar, uint32_t parity) {
 // The keys' or the values' way into shared memory, kept by one whole warp.  They have a ring
 // of slots each: their readers wait on a slot's barrier by the parity of its uses, so a
 // reader has to wait for every use of the slot, and in a ring that both share one could take
-// the use before last for its own.  A tile is kPer items; an item is column blocks of 128
-// bytes, [keys][128 bytes] each, 128-byte swizzled.  bf16: two items of two blocks of all 128
-// keys, or with kSplit two of four blocks of 64 keys; e4m3: one of two blocks of 128 keys.
-// One TMA box per column block and page (or part of a page): on B200 a 32 KiB slot takes
-// 435 - 450 cycles in boxes of 32 keys or more and 530 in boxes of 16, all 148 SMs loading
-// from L2 at once.  cp.async by a warp per slot has the same rate, but takes about 2,000
-// cycles of a warp and their latency before the slot is full.
+// the use before last for its own.
+// One TMA box per column block and page (or part of a page): on B200 32 KiB take 435 - 450
+// cycles in boxes of 32 keys or more and 530 in boxes of 16, all 148 SMs loading from L2 at
+// once.  cp.async by a warp per slot has the same rate, but takes about 2,000 cycles of a warp
+// and their latency before the slot is full.
 // Whole boxes are loaded: rows of a page past the last key hold what the page holds, pages
 // that are not there leave the slot as it was.  The softmax warps hide those keys' scores
 // and clear their values.
-template <bool kFp8, bool kSplit, int kSlots>
+template <bool kFp8, bool kIsV, int kSlots>
 struct Feed {
-  static constexpr int kPer = kFp8 ? 1 : 2;
-  static constexpr int kKeys = kSplit ? 64 : 128, kBlocks = kSplit ? 4 : 2;
+  using I = Items<kFp8>;
+  static constexpr int kKeys = kIsV ? I::kVKeys : 128, kBlocks = kIsV ? (kFp8 ? 2 : 4) : 1;
+  static constexpr int kMostShift = kIsV ? (kFp8 ? 6 : 5) : 7;  // log2 kKeys
   const CUtensorMap* map;
   uint32_t ring, bar_full, bar_empty;
   TreeCursor cur;
   TreeSegment g;
   uint32_t item = 0;
-  int tile = 0, half = 0, page = -1, page_next = -1;
+  int tile = 0, index = 0, page = -1, page_next = -1;
   bool live = false;
 
-  // The page of each group of eight keys of a tile, in lanes 0 .. 15.
-  __device__ __forceinline__ int pages(const TreeParams& p, int t) const {
+  // The page table's entry for each group of eight keys of a tile, in lanes 0 .. 15.
+  __device__ __forceinline__ int entries(const TreeParams& p, int t) const {
     const int lane = threadIdx.x & 31;
     const uint32_t j = uint32_t(t) * kTreeTile + lane * 8;
-    return t < g.t1 && lane < 16 && j < g.s.keys ? page_of(p.c, p.table + int64_t(g.b) * p.max_pages, p.max_pages, j) : -1;
+    return t < g.t1 && lane < 16 && j < g.s.keys
+               ? page_entry(p.c, p.table + int64_t(g.b) * p.max_pages, p.max_pages, j)
+               : -1;
+  }
+  __device__ __forceinline__ int checked(const TreeParams& p, int t, int entry) const {
+    const int lane = threadIdx.x & 31;
+    return lane < 16 && uint32_t(t) * kTreeTile + lane * 8 < g.s.keys ? page_checked(p.c, entry) : -1;
   }
   __device__ __forceinline__ void segment(const TreeParams& p) {
     live = tree_next(p, cur, &g);
     if (!live) return;
     tile = g.t0;
-    half = 0;
-    page = pages(p, tile);
-    page_next = pages(p, tile + 1);
+    index = 0;
+    page = checked(p, tile, entries(p, tile));
+    page_next = entries(p, tile + 1);
   }
   __device__ __forceinline__ void begin(const TreeParams& p, const TreeCursor& start, const CUtensorMap* m, uint32_t r,
                                         uint32_t full, uint32_t empty) {
     map = m, ring = r, bar_full = full, bar_empty = empty, cur = start;
-    if ((threadIdx.x & 31) == 0) tma_prefetch_desc(map);
     segment(p);
   }
   // The next item's slot is free.
@@ -184,38 +198,32 @@ struct Feed {
   }
   __device__ __forceinline__ void issue(const TreeParams& p) {
     const int lane = threadIdx.x & 31;
-    // Boxes: `rows` keys each, `per` per column block.  Box n = 32 round + lane is part n % per
-    // of column block n / per.
-    const int shift = min(p.c.page_shift, kSplit ? 6 : 7), rows = 1 << shift, per = kKeys >> shift;
-    const int boxes = per * kBlocks, rounds = (boxes + 31) / 32;
+    // Boxes: `rows` keys each, `per` per column block, 32 at most: box `lane` is part lane % per
+    // of column block lane / per.
+    const int shift = min(p.c.page_shift, kMostShift), rows = 1 << shift, per = kKeys >> shift;
     const uint32_t slot = item % kSlots, full = bar_full + 8u * slot;
-    const int first = kSplit ? half * 64 : 0;  // key of the tile the item starts with
-    uint32_t there = 0;
-    for (int round = 0; round < rounds; ++round) {
-      const int n = round * 32 + lane, k = first + (n & (per - 1)) * rows;
-      const int pg = __shfl_sync(0xffffffffu, page, (k >> 3) & 15);
-      there += __popc(__ballot_sync(0xffffffffu, n < boxes && pg >= 0));
-    }
-    if (lane == 0) mbar_arrive_expect_tx(full, there * uint32_t(rows) * 128u);
+    const int first = kIsV ? index * kKeys : 0;  // key of the tile the item starts with
+    const int k = first + (lane & (per - 1)) * rows, block = lane >> (kMostShift - shift);
+    const int pg = __shfl_sync(0xffffffffu, page, (k >> 3) & 15);
+    const bool mine = lane < per * kBlocks && pg >= 0;
+    const uint32_t boxes = uint32_t(__popc(__ballot_sync(0xffffffffu, mine)));
+    if (lane == 0) mbar_arrive_expect_tx(full, boxes * uint32_t(rows) * 128u);
     __syncwarp();
-    for (int round = 0; round < rounds; ++round) {
-      const int n = round * 32 + lane, k = first + (n & (per - 1)) * rows, block = n >> ((kSplit ? 6 : 7) - shift);
-      const int pg = __shfl_sync(0xffffffffu, page, (k >> 3) & 15);
-      if (n < boxes && pg >= 0) {
-        const uint32_t j = uint32_t(tile) * kTreeTile + uint32_t(k);
-        tma_load_5d(ring + slot * uint32_t(kSlotBytes) + uint32_t(block * kKeys + (k - first)) * 128u, map, full, 0,
-                    int(j & ((1u << p.c.page_shift) - 1)), kSplit ? block : 2 * half + block, g.h, pg);
-      }
+    if (mine) {
+      const uint32_t j = uint32_t(tile) * kTreeTile + uint32_t(k);
+      tma_load_5d(ring + slot * uint32_t(kSlotBytes) + uint32_t(block * kKeys + (k - first)) * 128u, map, full, 0,
+                  int(j & ((1u << p.c.page_shift) - 1)), kIsV ? block : index, g.h, pg);
     }
     __syncwarp();
     ++item;
-    if (++half == kPer) {
-      half = 0;
-      page = page_next;
-      if (++tile < g.t1)
-        page_next = pages(p, tile + 1);
-      else
+    if (++index == I::kTile) {
+      index = 0;
+      if (++tile < g.t1) {
+        page = checked(p, tile, page_next);
+        page_next = entries(p, tile + 1);
+      } else {
         segment(p);
+      }
     }
   }
   // No copy may be in flight when the CTA ends.
@@ -225,9 +233,20 @@ struct Feed {
   }
 };
 
-// The producer warp: fills whichever ring has a free slot.
+// The producer warp: fills whichever ring has a free slot, the keys' first.
 template <class K, class V>
-__device__ __forceinline__ void produce(const TreeParams& p, K& k, V& v) {
+__device__ __forceinline__ void produce(const TreeParams& p, const TreeCursor& start, const CUtensorMap* map_k,
+                                        const CUtensorMap* map_v, uint32_t ring_k, uint32_t ring_v, uint32_t bar_k,
+                                        uint32_t bar_k_empty, uint32_t bar_v, uint32_t bar_v_empty) {
+  K k;
+  V v;
+  if ((threadIdx.x & 31) == 0) {
+    tma_prefetch_desc(map_k);
+    tma_prefetch_desc(map_v);
+  }
+  k.begin(p, start, map_k, ring_k, bar_k, bar_k_empty);
+  if (k.ready()) k.issue(p);
+  v.begin(p, start, map_v, ring_v, bar_v, bar_v_empty);
   uint64_t since = global_timer_ns();
   while (k.live || v.live) {
     bool moved = false;
@@ -249,6 +268,12 @@ __device__ __forceinline__ void produce(const TreeParams& p, K& k, V& v) {
   }
   k.drain(p);
   v.drain(p);
+}
+
+// log2 of the keys in a box of the keys' and of the values' maps (Feed).
+inline int box_rows(const CacheView& c, bool values) {
+  const int most = !values ? 7 : c.dtype == GQA_E4M3 ? 6 : 5;
+  return 1 << (c.page_shift < most ? c.page_shift : most);
 }
 
 // The tensor map of a pool's keys or values: (64 or 128 columns of a 128-byte block, token of
