@@ -11,8 +11,8 @@
 // shared memory only when a maximum rises.  e4m3 pages, their scales, the pieces of queries
 // and probabilities, lazy maxima and values that a mask hides: as in tree_tc.cu.
 //
-// Warps: 16 for the softmax (lane quarter x 32 keys), a producer, one that fetches the keys'
-// scales, two issuers.
+// Warps: 16 for the softmax (lane quarter x 32 keys), two producers (bf16: keys and values; e4m3,
+// with half the bytes: one for both, and one that fetches the keys' scales), two issuers.
 #include "tree_tc.cuh"
 
 namespace gqa {
@@ -24,8 +24,7 @@ constexpr int kSoftWarps = 16;
 template <bool kFp8>
 struct RowsCfg {
   static constexpr int kKSlots = kFp8 ? 4 : 5, kVSlots = 5;  // what shared memory has room for
-  static constexpr int kIssuer = kSoftWarps + 2;  // after the producer and the keys' warp: 20 warps leave 96
-                                                  // registers a thread, 21 only 80
+  static constexpr int kIssuer = kSoftWarps + 2;  // 20 warps leave 96 registers a thread, 21 only 80
   static constexpr int kThreads = 32 * (kIssuer + 2);
   static constexpr int kOffQ = 0;  // bf16 [4][128 rows][128 bytes], or e4m3 [2 pieces][2][128 rows][128 bytes]
   static constexpr int kOffK = kRows * 512;
@@ -118,12 +117,26 @@ __global__ void __launch_bounds__(RowsCfg<kFp8>::kThreads, 1) tree_rows_kernel(c
   if (misaligned) {
     // no role
   } else if (warp == kSoftWarps) {
-    produce<Feed<kFp8, false, F::kKSlots>, Feed<kFp8, true, F::kVSlots>>(
-        p, cur, &map_k, &map_v, sK, sV, bar(kRBarKFull), bar(kRBarKEmpty), bar(kRBarVFull), bar(kRBarVEmpty));
+    Feed<kFp8, false, F::kKSlots> k;
+    k.begin(p, cur, &map_k, sK, bar(kRBarKFull), bar(kRBarKEmpty));
+    if constexpr (kFp8) {
+      Feed<kFp8, true, F::kVSlots> v;
+      if (k.ready()) k.issue(p);
+      v.begin(p, cur, &map_v, sV, bar(kRBarVFull), bar(kRBarVEmpty));
+      produce(p, k, v);
+    } else {
+      NoFeed none;
+      produce(p, k, none);
+    }
+  } else if (!kFp8 && warp == kSoftWarps + 1) {
+    Feed<kFp8, true, F::kVSlots> v;
+    NoFeed none;
+    v.begin(p, cur, &map_v, sV, bar(kRBarVFull), bar(kRBarVEmpty));
+    produce(p, v, none);
   } else if (warp == kSoftWarps + 1) {
-    // ---------------------------------------------------------------- keys
+    // ---------------------------------------------------------------- keys (e4m3)
     // Lane i looks after keys i, 32 + i, 64 + i and 96 + i of each tile: which are there, and
-    // (e4m3) their scales, in two buffers.  Pages are loaded two tiles ahead, scales one.
+    // their scales, in two buffers.  Page table entries are loaded two tiles ahead, scales one.
     const uint32_t slot_mask = (1u << p.c.page_shift) - 1;
     uint32_t tt = 0;
     bool ok = true;
@@ -148,7 +161,7 @@ __global__ void __launch_bounds__(RowsCfg<kFp8>::kThreads, 1) tree_rows_kernel(c
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           ks[i] = 0.f, vs[i] = 1.f;
-          if (kFp8 && page[i] >= 0) {
+          if (page[i] >= 0) {
             const int64_t at = (int64_t(page[i]) * p.c.Hkv + g.h) * (slot_mask + 1) +
                                ((uint32_t(tile) * kTreeTile + i * 32 + lane) & slot_mask);
             ks[i] = p.c.ks[at];
@@ -169,14 +182,14 @@ __global__ void __launch_bounds__(RowsCfg<kFp8>::kThreads, 1) tree_rows_kernel(c
           k_now[i] = ks[i], v_now[i] = vs[i];
           there[i] = __ballot_sync(0xffffffffu, page[i] >= 0);
         }
-        const bool one = kFp8 && ((page[0] >= 0 && vs[0] == 1.f) || (page[1] >= 0 && vs[1] == 1.f) ||
+        const bool one = ((page[0] >= 0 && vs[0] == 1.f) || (page[1] >= 0 && vs[1] == 1.f) ||
                                   (page[2] >= 0 && vs[2] == 1.f) || (page[3] >= 0 && vs[3] == 1.f));
         checked(tile + 1, entry_next);
         scales_at(tile + 1);
         entries_at(tile + 2, entry_next);
         // The softmax has read what the buffer held for tile t - 2.
         if (tt >= 2) ok = warp_wait(bar(kRBarP + int(b)), ((tt - 2) >> 1) & 1u, budget, status);
-        if constexpr (kFp8) {
+        {
           // A row of zeros (written with scale 1): see tree_tc.cu.
           if (__any_sync(0xffffffffu, one)) {
             // The product before is over first, so that the slot's barrier stands at no earlier use;
@@ -326,6 +339,12 @@ __global__ void __launch_bounds__(RowsCfg<kFp8>::kThreads, 1) tree_rows_kernel(c
       const bool live = t < g.s.drafted;
 
       const int key = part * 32 + lane;  // the key whose values this thread mends (quarter 0)
+      // (bf16) The page table's entry of this lane's key, a tile ahead of its use.
+      auto entry_at = [&](int tile) {
+        const uint32_t j = uint32_t(tile) * kTreeTile + key;
+        return tile < g.t1 && j < g.s.keys ? page_entry(p.c, table, p.max_pages, j) : -1;
+      };
+      int entry = !kFp8 ? entry_at(g.t0) : -1;
       float m = -1e30f, l = 0.f;  // this row's maximum (the same in all parts), this part's share of its sum
       for (int tile = g.t0; tile < g.t1; ++tile, ++tt) {
         const uint32_t sb = tt & 1u, ph = (tt >> 1) & 1u;
@@ -348,9 +367,16 @@ __global__ void __launch_bounds__(RowsCfg<kFp8>::kThreads, 1) tree_rows_kernel(c
           if (lane == 0) mbar_arrive(bar(kRBarP + int(sb)));
           continue;
         }
-        fine = warp_wait(bar(kRBarKeys + int(sb)), ph, budget, status) && fine;
         // Which of the 32 keys are there, and which this row sees.
-        const uint32_t there = sh_there[sb * 4 + part];
+        uint32_t there;
+        if constexpr (kFp8) {
+          fine = warp_wait(bar(kRBarKeys + int(sb)), ph, budget, status) && fine;
+          there = sh_there[sb * 4 + part];
+        } else {
+          const int page = j0 + lane < g.s.keys ? page_checked(p.c, entry) : -1;
+          there = __ballot_sync(0xffffffffu, page >= 0);
+          entry = entry_at(tile + 1);
+        }
         const float* scale = sh_scale + sb * 384 + part * 32;
         uint32_t vis = there;
         const bool drafted_tile = j0 + 32 > g.s.ctx && vis != 0;
@@ -532,8 +558,7 @@ template <bool kFp8>
 int launch(const TreeParams& p, cudaStream_t stream) {
   using F = RowsCfg<kFp8>;
   CUtensorMap mk, mv;
-  if (!encode_pages(&mk, p.c, p.c.k, box_rows(p.c, false)) || !encode_pages(&mv, p.c, p.c.v, box_rows(p.c, true)))
-    return GQA_ERR_LAUNCH;
+  if (!encode_pages(&mk, p.c, false) || !encode_pages(&mv, p.c, true)) return GQA_ERR_LAUNCH;
   if (cudaFuncSetAttribute(tree_rows_kernel<kFp8>, cudaFuncAttributeMaxDynamicSharedMemorySize, F::kSmem) != cudaSuccess)
     return GQA_ERR_LAUNCH;
   tree_rows_kernel<kFp8><<<unsigned(p.workers) * unsigned(p.row_tiles), F::kThreads, F::kSmem, stream>>>(mk, mv, p);

@@ -22,8 +22,9 @@
 // than the largest p, and P is stored as 16 P <= 256: a probability then keeps 8 bits down
 // to 2^-8 of the first maximum, and is off by at most 2^-14 of it below.
 //
-// Warps: 4 softmax warps per 32 (or 16) rows, a producer (TMA, through the page table, into
-// rings of 16 KiB slots), and two warps whose first lanes issue the products.
+// Warps: 4 softmax warps per 32 (or 16) rows, a producer each for keys and values (TMA,
+// through the page table, into rings of 16 KiB slots), and two warps whose first lanes issue
+// the products.
 #include "tree_tc.cuh"
 
 namespace gqa {
@@ -38,7 +39,7 @@ struct Cfg {
   static constexpr int kQBytes = kN * 512;        // bf16, or two e4m3 pieces
   static constexpr int kPBytes = 16384;           // [128 keys][128 bytes]
   static constexpr int kKSlots = kN > 32 ? 5 : 6, kVSlots = 6;  // what shared memory has room for
-  static constexpr int kIssuer = kSoftWarps + 1;  // the S issuer's warp, after the producer; then the O issuer's
+  static constexpr int kIssuer = kSoftWarps + 2;  // the S issuer's warp, after the producers; then the O issuer's
   static constexpr int kWarps = kIssuer + 2;
   static constexpr int kThreads = 32 * kWarps;
   static constexpr int kOffQ = 0;
@@ -155,8 +156,15 @@ __global__ void __launch_bounds__(Cfg<kN, kFp8>::kThreads, 1) tree_tc_kernel(con
   if (misaligned) {
     // no role
   } else if (warp == F::kSoftWarps) {
-    produce<Feed<kFp8, false, F::kKSlots>, Feed<kFp8, true, F::kVSlots>>(
-        p, cur, &map_k, &map_v, sK, sV, bar(kBarKFull), bar(kBarKEmpty), bar(kBarVFull), bar(kBarVEmpty));
+    Feed<kFp8, false, F::kKSlots> feed;
+    NoFeed none;
+    feed.begin(p, cur, &map_k, sK, bar(kBarKFull), bar(kBarKEmpty));
+    produce(p, feed, none);
+  } else if (warp == F::kSoftWarps + 1) {
+    Feed<kFp8, true, F::kVSlots> feed;
+    NoFeed none;
+    feed.begin(p, cur, &map_v, sV, bar(kBarVFull), bar(kBarVEmpty));
+    produce(p, feed, none);
   } else if (warp >= F::kIssuer) {
     // ---------------------------------------------------------------- MMA issuers
     // One thread issues every S^T = K Q^T, another every O^T += V^T P^T, so that neither
@@ -614,8 +622,7 @@ int launch_n(const TreeParams& p, const CUtensorMap& mk, const CUtensorMap& mv, 
 template <bool kFp8>
 int launch_type(const TreeParams& p, int rows, cudaStream_t stream) {
   CUtensorMap mk, mv;
-  if (!encode_pages(&mk, p.c, p.c.k, box_rows(p.c, false)) || !encode_pages(&mv, p.c, p.c.v, box_rows(p.c, true)))
-    return GQA_ERR_LAUNCH;
+  if (!encode_pages(&mk, p.c, false) || !encode_pages(&mv, p.c, true)) return GQA_ERR_LAUNCH;
   switch (rows) {
     case 16: return launch_n<16, kFp8>(p, mk, mv, stream);
     case 32: return launch_n<32, kFp8>(p, mk, mv, stream);

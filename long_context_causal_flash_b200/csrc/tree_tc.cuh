@@ -147,10 +147,11 @@ __device__ __forceinline__ bool mbar_test(uint32_t bar, uint32_t parity) {
 // of slots each: their readers wait on a slot's barrier by the parity of its uses, so a
 // reader has to wait for every use of the slot, and in a ring that both share one could take
 // the use before last for its own.
-// One TMA box per column block and page (or part of a page): on B200 32 KiB take 435 - 450
+// TMA boxes of one column block and page (or part of a page): on B200 32 KiB take 435 - 450
 // cycles in boxes of 32 keys or more and 530 in boxes of 16, all 148 SMs loading from L2 at
 // once.  cp.async by a warp per slot has the same rate, but takes about 2,000 cycles of a warp
-// and their latency before the slot is full.
+// and their latency before the slot is full.  What bounds this warp is its own path per item,
+// so that path is short: about 90 cycles for each box and as much around them.
 // Whole boxes are loaded: rows of a page past the last key hold what the page holds, pages
 // that are not there leave the slot as it was.  The softmax warps hide those keys' scores
 // and clear their values.
@@ -163,9 +164,15 @@ struct Feed {
   uint32_t ring, bar_full, bar_empty;
   TreeCursor cur;
   TreeSegment g;
-  uint32_t item = 0;
+  uint32_t slot = 0, parity = 1;  // of the next item; parity: of the wait for the slot to be empty
+  int issued = 0;                 // items so far, kSlots at most
   int tile = 0, index = 0, page = -1, page_next = -1;
-  bool live = false;
+  bool live = false, whole = false;  // whole: all keys of the tile are there
+  // This lane's box: `rows` keys from key `k` of the item on, column block `block`, at `offset` of
+  // the slot.  Boxes hold one column block, or all of an item's where a page holds its keys.
+  int rows, k, block;
+  uint32_t offset, bytes;
+  bool mine;
 
   // The page table's entry for each group of eight keys of a tile, in lanes 0 .. 15.
   __device__ __forceinline__ int entries(const TreeParams& p, int t) const {
@@ -175,120 +182,126 @@ struct Feed {
                ? page_entry(p.c, p.table + int64_t(g.b) * p.max_pages, p.max_pages, j)
                : -1;
   }
-  __device__ __forceinline__ int checked(const TreeParams& p, int t, int entry) const {
+  __device__ __forceinline__ void check(const TreeParams& p, int entry) {
     const int lane = threadIdx.x & 31;
-    return lane < 16 && uint32_t(t) * kTreeTile + lane * 8 < g.s.keys ? page_checked(p.c, entry) : -1;
+    page = lane < 16 && uint32_t(tile) * kTreeTile + lane * 8 < g.s.keys ? page_checked(p.c, entry) : -1;
+    whole = __all_sync(0xffffffffu, page >= 0 || lane >= 16);
   }
   __device__ __forceinline__ void segment(const TreeParams& p) {
     live = tree_next(p, cur, &g);
     if (!live) return;
     tile = g.t0;
     index = 0;
-    page = checked(p, tile, entries(p, tile));
+    check(p, entries(p, tile));
     page_next = entries(p, tile + 1);
   }
   __device__ __forceinline__ void begin(const TreeParams& p, const TreeCursor& start, const CUtensorMap* m, uint32_t r,
                                         uint32_t full, uint32_t empty) {
     map = m, ring = r, bar_full = full, bar_empty = empty, cur = start;
+    const int lane = threadIdx.x & 31;
+    if (lane == 0) tma_prefetch_desc(map);
+    const int shift = min(p.c.page_shift, kMostShift), per = kKeys >> shift;
+    rows = 1 << shift;
+    k = (lane & (per - 1)) * rows;
+    block = lane >> (kMostShift - shift);
+    mine = lane < (per == 1 ? 1 : per * kBlocks);
+    offset = uint32_t(block * kKeys + k) * 128u;
+    bytes = uint32_t(per == 1 ? kBlocks : 1) * uint32_t(rows) * 128u;
     segment(p);
   }
-  // The next item's slot is free.
+  // The next item's slot is free (lanes may differ in the moment they see it).
   __device__ __forceinline__ bool ready() const {
-    return live && __all_sync(0xffffffffu, mbar_test(bar_empty + 8u * (item % kSlots), ((item / kSlots) & 1u) ^ 1u));
+    return live && __all_sync(0xffffffffu, mbar_test(bar_empty + 8u * slot, parity));
   }
   __device__ __forceinline__ void issue(const TreeParams& p) {
     const int lane = threadIdx.x & 31;
-    // Boxes: `rows` keys each, `per` per column block, 32 at most: box `lane` is part lane % per
-    // of column block lane / per.
-    const int shift = min(p.c.page_shift, kMostShift), rows = 1 << shift, per = kKeys >> shift;
-    const uint32_t slot = item % kSlots, full = bar_full + 8u * slot;
-    const int first = kIsV ? index * kKeys : 0;  // key of the tile the item starts with
-    const int k = first + (lane & (per - 1)) * rows, block = lane >> (kMostShift - shift);
-    const int pg = __shfl_sync(0xffffffffu, page, (k >> 3) & 15);
-    const bool mine = lane < per * kBlocks && pg >= 0;
-    const uint32_t boxes = uint32_t(__popc(__ballot_sync(0xffffffffu, mine)));
-    if (lane == 0) mbar_arrive_expect_tx(full, boxes * uint32_t(rows) * 128u);
+    const uint32_t full = bar_full + 8u * slot;
+    const int at = (kIsV ? index * kKeys : 0) + k;  // key of the tile
+    const int pg = __shfl_sync(0xffffffffu, page, (at >> 3) & 15);
+    const bool send = mine && pg >= 0;
+    uint32_t total = kSlotBytes;
+    if (!whole) total = bytes * uint32_t(__popc(__ballot_sync(0xffffffffu, send)));
+    if (lane == 0) mbar_arrive_expect_tx(full, total);
     __syncwarp();
-    if (mine) {
-      const uint32_t j = uint32_t(tile) * kTreeTile + uint32_t(k);
-      tma_load_5d(ring + slot * uint32_t(kSlotBytes) + uint32_t(block * kKeys + (k - first)) * 128u, map, full, 0,
-                  int(j & ((1u << p.c.page_shift) - 1)), kIsV ? block : index, g.h, pg);
+    if (send) {
+      const uint32_t j = uint32_t(tile) * kTreeTile + uint32_t(at);
+      tma_load_5d(ring + slot * uint32_t(kSlotBytes) + offset, map, full, 0, int(j & ((1u << p.c.page_shift) - 1)),
+                  kIsV ? block : index, g.h, pg);
     }
     __syncwarp();
-    ++item;
+    if (issued < kSlots) ++issued;
+    if (++slot == kSlots) slot = 0, parity ^= 1u;
     if (++index == I::kTile) {
       index = 0;
       if (++tile < g.t1) {
-        page = checked(p, tile, page_next);
+        check(p, page_next);
         page_next = entries(p, tile + 1);
       } else {
         segment(p);
       }
     }
   }
-  // No copy may be in flight when the CTA ends.
+  // No copy may be in flight when the CTA ends: the last use of each slot is complete.
   __device__ __forceinline__ void drain(const TreeParams& p) const {
-    for (uint32_t i = item > uint32_t(kSlots) ? item - kSlots : 0u; i < item; ++i)
-      warp_wait(bar_full + 8u * (i % kSlots), (i / kSlots) & 1u, p.wait_budget_ns, p.c.status);
+    for (int i = 0; i < issued; ++i) {
+      const uint32_t s = slot + kSlots - 1 - i, at = s % kSlots;
+      // slots below `slot` have been used in this round (parity ^ 1 of the wait before), others in the last
+      warp_wait(bar_full + 8u * at, s >= kSlots ? parity ^ 1u : parity, p.wait_budget_ns, p.c.status);
+    }
   }
 };
 
-// The producer warp: fills whichever ring has a free slot, the keys' first.
-template <class K, class V>
-__device__ __forceinline__ void produce(const TreeParams& p, const TreeCursor& start, const CUtensorMap* map_k,
-                                        const CUtensorMap* map_v, uint32_t ring_k, uint32_t ring_v, uint32_t bar_k,
-                                        uint32_t bar_k_empty, uint32_t bar_v, uint32_t bar_v_empty) {
-  K k;
-  V v;
-  if ((threadIdx.x & 31) == 0) {
-    tma_prefetch_desc(map_k);
-    tma_prefetch_desc(map_v);
-  }
-  k.begin(p, start, map_k, ring_k, bar_k, bar_k_empty);
-  if (k.ready()) k.issue(p);
-  v.begin(p, start, map_v, ring_v, bar_v, bar_v_empty);
-  uint64_t since = global_timer_ns();
-  while (k.live || v.live) {
+// A producer warp for two rings (fills whichever has a free slot, the first one's first) or,
+// with NoFeed, for one.
+struct NoFeed {
+  bool live = false;
+  __device__ __forceinline__ bool ready() const { return false; }
+  __device__ __forceinline__ void issue(const TreeParams&) {}
+  __device__ __forceinline__ void drain(const TreeParams&) const {}
+};
+template <class A, class B>
+__device__ __forceinline__ void produce(const TreeParams& p, A& a, B& b) {
+  uint64_t since = 0;
+  int idle = 0;
+  while (a.live || b.live) {
     bool moved = false;
-    if (k.ready()) {
-      k.issue(p);
+    if (a.ready()) {
+      a.issue(p);
       moved = true;
     }
-    if (v.ready()) {
-      v.issue(p);
+    if (b.ready()) {
+      b.issue(p);
       moved = true;
     }
-    const uint64_t now = global_timer_ns();
-    if (moved) {
-      since = now;
-    } else if (__any_sync(0xffffffffu, int64_t(now - since) > p.wait_budget_ns)) {
+    // The clock is read only when nothing has moved for a while.
+    idle = moved ? 0 : idle + 1;
+    if (idle == 256) since = global_timer_ns();
+    if (idle > 256 && (idle & 255) == 0 &&
+        __any_sync(0xffffffffu, int64_t(global_timer_ns() - since) > p.wait_budget_ns)) {
       set_status(p.c.status, GQA_ERR_DEVICE_TIMEOUT);
       break;
     }
   }
-  k.drain(p);
-  v.drain(p);
-}
-
-// log2 of the keys in a box of the keys' and of the values' maps (Feed).
-inline int box_rows(const CacheView& c, bool values) {
-  const int most = !values ? 7 : c.dtype == GQA_E4M3 ? 6 : 5;
-  return 1 << (c.page_shift < most ? c.page_shift : most);
+  a.drain(p);
+  b.drain(p);
 }
 
 // The tensor map of a pool's keys or values: (64 or 128 columns of a 128-byte block, token of
-// the page, block, head, page), boxes of one block and `rows` tokens.
-inline bool encode_pages(CUtensorMap* m, const CacheView& c, const char* pool, int rows) {
+// the page, block, head, page); boxes as Feed takes them.
+inline bool encode_pages(CUtensorMap* m, const CacheView& c, bool values) {
   EncodeTiledFn enc = encode_tiled_fn();
   if (!enc) return false;
   const bool fp8 = c.dtype == GQA_E4M3;
   const cuuint64_t es = fp8 ? 1 : 2;
+  const int most = !values ? 7 : fp8 ? 6 : 5, shift = c.page_shift < most ? c.page_shift : most;
   const cuuint64_t dims[5] = {128 / es, cuuint64_t(1) << c.page_shift, 2 * es, cuuint64_t(c.Hkv), cuuint64_t(c.n_pages)};
   // A dimension of one has no stride of its own (views may carry any number there).
   const cuuint64_t strides[4] = {cuuint64_t(c.st) * es, 128, c.Hkv > 1 ? cuuint64_t(c.sh) * es : 16,
                                  c.n_pages > 1 ? cuuint64_t(c.sp) * es : 16};
-  const cuuint32_t box[5] = {cuuint32_t(128 / es), cuuint32_t(rows), 1, 1, 1}, estr[5] = {1, 1, 1, 1, 1};
-  return enc(m, fp8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 5, const_cast<char*>(pool), dims,
+  const cuuint32_t box[5] = {cuuint32_t(128 / es), cuuint32_t(1) << shift,
+                             cuuint32_t(values && shift == most ? 2 * es : 1), 1, 1},
+                   estr[5] = {1, 1, 1, 1, 1};
+  return enc(m, fp8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 5, values ? c.v : c.k, dims,
              strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
