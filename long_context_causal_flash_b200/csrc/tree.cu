@@ -3,11 +3,15 @@
 //
 // A CTA holds R query rows (R / G tokens of the G heads of one key/value head) and
 // streams its worker's tiles; 8 warps take 16 of a tile's 128 keys each, four keys at a
-// time.  Lane l owns columns 8 l .. 8 l + 7 of q, k, v and of the output.  The 4 R partial
-// dot products of a lane are summed over the lanes by halving exchanges (a lane sends the
-// half it does not keep), which leaves one score per lane, or per pair of lanes at R = 4,
-// where the online softmax runs: the running maximum and sum of a row live in the lanes
-// that hold its scores, and the output is rescaled only when some row's maximum rose.
+// time, through a ring of three groups of its own in shared memory (cp.async), so that no
+// warp waits for another and two groups per warp are under way.  A lane owns eight columns
+// of q, k, v and of the output.  The 4 R partial dot products of a lane (packed FMAs, two
+// columns each) are summed over the lanes by halving exchanges (a lane sends the half it
+// does not keep), which leaves one score per lane, or per pair of lanes at R = 4, where the
+// online softmax runs: the running maximum and sum of a row live in the lanes that hold its
+// scores, and the output is rescaled only when some row's maximum rose.  With R = 8 a group
+// is 256 packed FMAs, 512 cycles of the FMA pipe, and about as many issue slots; with 4 rows
+// fp32 pages are bound by memory, with 8 and more by the FMA pipe.
 #include "internal.h"
 #include "tree.cuh"
 
@@ -16,162 +20,259 @@ namespace {
 
 constexpr int kWarps = 8;
 constexpr int kThreads = 32 * kWarps;
-constexpr int kKeys = 4;  // keys a warp takes at a time (a divisor of every page size)
+constexpr int kKeys = 4;    // keys of a group (a divisor of every page size)
+constexpr int kStages = 3;  // groups of a warp's ring
 constexpr int kKeysPerWarp = kTreeTile / kWarps;
+constexpr int kGroups = kKeysPerWarp / kKeys;  // of a tile, per warp
 constexpr int kB200Sms = 148;
 
-// Eight columns of a cache row; e4m3 codes still want their row's scale.
+// Two floats as the operand of a packed FMA: d += a b.
+__device__ __forceinline__ uint64_t pack2(float lo, float hi) {
+  uint64_t d;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "f"(lo), "f"(hi));
+  return d;
+}
+__device__ __forceinline__ float2 unpack2(uint64_t v) {
+  float2 f;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(f.x), "=f"(f.y) : "l"(v));
+  return f;
+}
+__device__ __forceinline__ void ffma2(uint64_t& d, uint64_t a, uint64_t b) {
+  asm("fma.rn.f32x2 %0, %1, %2, %0;" : "+l"(d) : "l"(a), "l"(b));
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+
+// A lane's columns: eight in a row, but two fours 128 apart of fp32 rows, so that a warp's
+// 16-byte loads are contiguous.
 template <int kCache>
-__device__ __forceinline__ void load_row(const char* pool, int64_t at, float* x) {
+__device__ __forceinline__ int column(int lane, int four) {  // of the lane's columns 4 four .. + 3
+  return kCache == GQA_F32 ? 128 * four + 4 * lane : 8 * lane + 4 * four;
+}
+
+template <int kCache>
+struct RowBytes {
+  static constexpr int value = kHeadDim * (kCache == GQA_F32 ? 4 : kCache == GQA_BF16 ? 2 : 1);
+};
+
+// The lane's eight columns of a staged row, as four pairs; e4m3 codes want their scale still.
+template <int kCache>
+__device__ __forceinline__ void staged(const char* row, int lane, uint64_t (&x)[4]) {
   if constexpr (kCache == GQA_F32) {
-    load8(reinterpret_cast<const float*>(pool) + at, x);
-  } else if constexpr (kCache == GQA_BF16) {
-    load8(reinterpret_cast<const __nv_bfloat16*>(pool) + at, x);
+    const ulonglong2 a = *reinterpret_cast<const ulonglong2*>(row + 16 * lane);
+    const ulonglong2 b = *reinterpret_cast<const ulonglong2*>(row + 512 + 16 * lane);
+    x[0] = a.x, x[1] = a.y, x[2] = b.x, x[3] = b.y;
   } else {
-    const uint2 u = *reinterpret_cast<const uint2*>(pool + at);
-    e4m3_decode4(u.x, x);
-    e4m3_decode4(u.y, x + 4);
+    float f[8];
+    if constexpr (kCache == GQA_BF16) {
+      unpack8(*reinterpret_cast<const uint4*>(row + 16 * lane), f);
+    } else {
+      const uint2 u = *reinterpret_cast<const uint2*>(row + 8 * lane);
+      e4m3_decode4(u.x, f);
+      e4m3_decode4(u.y, f + 4);
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) x[i] = pack2(f[2 * i], f[2 * i + 1]);
   }
 }
 
+__device__ __forceinline__ void load4(const float* p, float* x) {
+  const float4 a = *reinterpret_cast<const float4*>(p);
+  x[0] = a.x, x[1] = a.y, x[2] = a.z, x[3] = a.w;
+}
+__device__ __forceinline__ void load4(const __nv_bfloat16* p, float* x) {
+  const uint2 u = *reinterpret_cast<const uint2*>(p);
+  x[0] = __uint_as_float(u.x << 16), x[1] = __uint_as_float(u.x & 0xffff0000u);
+  x[2] = __uint_as_float(u.y << 16), x[3] = __uint_as_float(u.y & 0xffff0000u);
+}
+__device__ __forceinline__ void store4(float* p, const float* x) {
+  *reinterpret_cast<float4*>(p) = make_float4(x[0], x[1], x[2], x[3]);
+}
+
 template <int R, int kCache, typename QT>
-__global__ void __launch_bounds__(kThreads, R == 4 ? 2 : 1) tree_ffma_kernel(const __grid_constant__ TreeParams p) {
-  extern __shared__ __align__(16) float smem[];  // [warp][R][256] outputs, then [warp][R] maxima and sums
+__global__ void __launch_bounds__(kThreads, 1) tree_ffma_kernel(const __grid_constant__ TreeParams p) {
+  // [warp][stage][k, v][4 keys] rows; at the end of a segment [warp][R][256] outputs in their place.
+  extern __shared__ __align__(16) char smem[];
   __shared__ TreeCursor start;
-  float* sh_m = smem + kWarps * R * kHeadDim;
-  float* sh_l = sh_m + kWarps * R;
+  __shared__ float sh_m[kWarps * R], sh_l[kWarps * R];
+  constexpr int kRow = RowBytes<kCache>::value, kStage = 2 * kKeys * kRow;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int worker = blockIdx.x / p.row_tiles, rt = blockIdx.x % p.row_tiles;
+  char* ring = smem + warp * kStages * kStage;
   if (warp == 0) {
     const TreeCursor c = tree_start(p, worker);
     if (lane == 0) start = c;
   }
   __syncthreads();
+  launch_dependents();
   TreeCursor cur = start;
 
   constexpr int kScores = R * kKeys;  // 32 or 16
   const int idx = kScores == 32 ? lane : lane >> 1;
   const int my_key = idx / R, my_row = idx % R;
-  const int n_mine = rt * R + my_row;  // this lane's query row among the T G of the head
-  const int t_mine = n_mine / p.G;
+  const int t_mine = (rt * R + my_row) / p.G;  // this lane's query row among the T G of the head
+  const uint32_t slot_mask = (1u << p.c.page_shift) - 1;
+  constexpr int kEs = kRow / kHeadDim;
 
   TreeSegment g;
   while (tree_next(p, cur, &g)) {
     const int32_t* table = p.table + int64_t(g.b) * p.max_pages;
-    float q[R][8], o[R][8];
+    uint64_t q[R][4], o[R][4];
 #pragma unroll
     for (int r = 0; r < R; ++r) {
       const int n = rt * R + r, t = n / p.G;
+      float x[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+      if (t < g.s.drafted) {
+        const QT* src = reinterpret_cast<const QT*>(p.q.p) + g.b * p.q.sb + int64_t(g.h * p.G + n % p.G) * p.q.sh + t * p.q.sl;
+        load4(src + column<kCache>(lane, 0), x);
+        load4(src + column<kCache>(lane, 1), x + 4);
+      }
 #pragma unroll
-      for (int i = 0; i < 8; ++i) q[r][i] = 0.f, o[r][i] = 0.f;
-      if (t < g.s.drafted)
-        load8(reinterpret_cast<const QT*>(p.q.p) + g.b * p.q.sb + int64_t(g.h * p.G + n % p.G) * p.q.sh + t * p.q.sl +
-                  8 * lane,
-              q[r]);
+      for (int i = 0; i < 4; ++i) q[r][i] = pack2(x[2 * i], x[2 * i + 1]), o[r][i] = 0;
     }
     float m = -INFINITY, l = 0.f;  // of my_row; l: the share of this lane's keys
-    for (int tile = g.t0; tile < g.t1; ++tile) {
-      for (int k0 = 0; k0 < kKeysPerWarp; k0 += kKeys) {
-        const uint32_t j0 = uint32_t(tile) * kTreeTile + warp * kKeysPerWarp + k0;
-        if (j0 >= g.s.keys) break;
+
+    // Group n of this warp: keys 4 (n % kGroups) .. + 3 of its 16 of tile t0 + n / kGroups.
+    const int groups = (g.t1 - g.t0) * kGroups;
+    auto first_key = [&](int n) {
+      return uint32_t(g.t0 + n / kGroups) * kTreeTile + uint32_t(warp * kKeysPerWarp + n % kGroups * kKeys);
+    };
+    // Its copies, by all lanes; rows that are not there are zeros.  Returns how many keys are.
+    auto fetch = [&](int n) {
+      int live = 0;
+      if (n < groups) {
+        const uint32_t j0 = first_key(n);
+        const int page = j0 < g.s.keys ? page_of(p.c, table, p.max_pages, j0) : -1;
+        live = page < 0 ? 0 : int(min(uint32_t(kKeys), g.s.keys - j0));
+        const int64_t at = (int64_t(max(page, 0)) * p.c.sp + g.h * p.c.sh + (j0 & slot_mask) * p.c.st) * kEs;
+        const uint32_t dst = smem_u32(ring + n % kStages * kStage);
+        constexpr int kUnits = kRow / 16;  // 16-byte units of a row
+        constexpr int kRowsAtOnce = kUnits >= 32 ? 1 : 32 / kUnits;
+#pragma unroll
+        for (int kv = 0; kv < 2; ++kv)
+#pragma unroll
+          for (int i = 0; i < kKeys; i += kRowsAtOnce)
+#pragma unroll
+            for (int u0 = 0; u0 < kUnits; u0 += 32) {
+              const int row = i + (kUnits >= 32 ? 0 : lane / kUnits), unit = u0 + lane % (kUnits >= 32 ? 32 : kUnits);
+              const char* src = (kv ? p.c.v : p.c.k) + at + row * p.c.st * kEs + unit * 16;
+              asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(
+                               dst + uint32_t((kv * kKeys + row) * kRow + unit * 16)),
+                           "l"(row < live ? src : p.c.k), "r"(row < live ? 16 : 0)
+                           : "memory");
+            }
+      }
+      asm volatile("cp.async.commit_group;" ::: "memory");
+      return live;
+    };
+    int live_at[kStages];  // of the groups in the ring, the next one first
+#pragma unroll
+    for (int i = 0; i < kStages - 1; ++i) live_at[i] = fetch(i);
+    for (int n = 0; n < groups; ++n) {
+      __syncwarp();  // the stage to be filled has been read by all lanes
+      live_at[kStages - 1] = fetch(n + kStages - 1);
+      asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 1) : "memory");
+      __syncwarp();
+      const int live = live_at[0];
+#pragma unroll
+      for (int i = 0; i + 1 < kStages; ++i) live_at[i] = live_at[i + 1];
+      if (live == 0) continue;
+      const uint32_t j0 = first_key(n);
+      const char* stage = ring + n % kStages * kStage;
+      float k_scale = 1.f, v_scale = 1.f;
+      if constexpr (kCache == GQA_E4M3) {
         const int page = page_of(p.c, table, p.max_pages, j0);
-        if (page < 0) continue;  // recorded; its keys are absent
-        const int slot = int(j0 & ((1u << p.c.page_shift) - 1));
-        const int live = int(min(uint32_t(kKeys), g.s.keys - j0));
-        const int64_t at = page * p.c.sp + g.h * p.c.sh + slot * p.c.st + 8 * lane;
-        float k[kKeys][8], v[kKeys][8];
+        const int64_t sat = (int64_t(page) * p.c.Hkv + g.h) * (slot_mask + 1) + (j0 & slot_mask);
+        if (my_key < live) k_scale = p.c.ks[sat + my_key], v_scale = p.c.vs[sat + my_key];
+      }
+      float s[kScores];
 #pragma unroll
-        for (int i = 0; i < kKeys; ++i)
-          if (i < live) {
-            load_row<kCache>(p.c.k, at + i * p.c.st, k[i]);
-            load_row<kCache>(p.c.v, at + i * p.c.st, v[i]);
-          } else {
+      for (int i = 0; i < kKeys; ++i) {
+        uint64_t k[4];
+        staged<kCache>(stage + i * kRow, lane, k);
 #pragma unroll
-            for (int c = 0; c < 8; ++c) k[i][c] = 0.f, v[i][c] = 0.f;
-          }
-        float k_scale = 1.f, v_scale = 1.f;
-        if constexpr (kCache == GQA_E4M3) {
-          const int64_t sat = (int64_t(page) * p.c.Hkv + g.h) * (int64_t(1) << p.c.page_shift) + slot;
-          if (my_key < live) k_scale = p.c.ks[sat + my_key], v_scale = p.c.vs[sat + my_key];
+        for (int r = 0; r < R; ++r) {
+          uint64_t a = mul2(q[r][0], k[0]);
+          ffma2(a, q[r][1], k[1]);
+          ffma2(a, q[r][2], k[2]);
+          ffma2(a, q[r][3], k[3]);
+          const float2 f = unpack2(a);
+          s[i * R + r] = f.x + f.y;
         }
-        float s[kScores];
+      }
 #pragma unroll
-        for (int i = 0; i < kKeys; ++i)
+      for (int half = kScores / 2, off = 16; half >= 1; half >>= 1, off >>= 1) {
+        const bool up = (lane & off) != 0;
 #pragma unroll
-          for (int r = 0; r < R; ++r) {
-            float a = 0.f;
-#pragma unroll
-            for (int c = 0; c < 8; ++c) a = fmaf(q[r][c], k[i][c], a);
-            s[i * R + r] = a;
+        for (int i = 0; i < kScores / 2; ++i)
+          if (i < half) {
+            const float keep = up ? s[i + half] : s[i], send = up ? s[i] : s[i + half];
+            s[i] = keep + __shfl_xor_sync(0xffffffffu, send, off);
           }
+      }
+      if (kScores == 16) s[0] += __shfl_xor_sync(0xffffffffu, s[0], 1);
+      // Visible: any key of the context; a drafted one by the mask.  Rows past the tile's
+      // last (t >= T) are nobody's and see all, so that they ask for no masked path.
+      const uint32_t j = j0 + my_key;
+      bool vis = my_key < live && (t_mine < g.s.drafted || t_mine >= p.T);
+      if (vis && j >= g.s.ctx && t_mine < p.T) vis = tree_sees(p, g.b, t_mine, int(j - g.s.ctx));
+      const float x = vis ? s[0] * k_scale * p.scale_log2 : -INFINITY;
+      const unsigned seen = __ballot_sync(0xffffffffu, vis);
+      float mx = x;
+      mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
+      mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
+      const float m_new = fmaxf(m, mx);
+      const float ref = m_new == -INFINITY ? 0.f : m_new;
+      if (__any_sync(0xffffffffu, m_new > m)) {
+        const float alpha = exp2f(m - ref);  // 0 for the first visible key
+        l *= alpha;
 #pragma unroll
-        for (int half = kScores / 2, off = 16; half >= 1; half >>= 1, off >>= 1) {
-          const bool up = (lane & off) != 0;
+        for (int r = 0; r < R; ++r) {
+          const float a = __shfl_sync(0xffffffffu, alpha, kScores == 32 ? r : 2 * r);
+          const uint64_t a2 = pack2(a, a);
 #pragma unroll
-          for (int i = 0; i < kScores / 2; ++i)
-            if (i < half) {
-              const float keep = up ? s[i + half] : s[i], send = up ? s[i] : s[i + half];
-              s[i] = keep + __shfl_xor_sync(0xffffffffu, send, off);
-            }
+          for (int c = 0; c < 4; ++c) o[r][c] = mul2(o[r][c], a2);
         }
-        if (kScores == 16) s[0] += __shfl_xor_sync(0xffffffffu, s[0], 1);
-        // Visible: any key of the context; a drafted one by the mask.  Rows past the tile's
-        // last (t >= T) are nobody's and see all, so that they ask for no masked path.
-        const uint32_t j = j0 + my_key;
-        bool vis = my_key < live && (t_mine < g.s.drafted || t_mine >= p.T);
-        if (vis && j >= g.s.ctx && t_mine < p.T) vis = tree_sees(p, g.b, t_mine, int(j - g.s.ctx));
-        const float x = vis ? s[0] * k_scale * p.scale_log2 : -INFINITY;
-        const unsigned seen = __ballot_sync(0xffffffffu, vis);
-        float mx = x;
-        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
-        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
-        const float m_new = fmaxf(m, mx);
-        const float ref = m_new == -INFINITY ? 0.f : m_new;
-        if (__any_sync(0xffffffffu, m_new > m)) {
-          const float alpha = exp2f(m - ref);  // 0 for the first visible key
-          l *= alpha;
+        m = m_new;
+      }
+      float w = vis ? exp2f(x - ref) : 0.f;
+      l += w;
+      w *= v_scale;
 #pragma unroll
-          for (int r = 0; r < R; ++r) {
-            const float a = __shfl_sync(0xffffffffu, alpha, kScores == 32 ? r : 2 * r);
+      for (int i = 0; i < kKeys; ++i) {
+        uint64_t v[4];
+        staged<kCache>(stage + (kKeys + i) * kRow, lane, v);
 #pragma unroll
-            for (int c = 0; c < 8; ++c) o[r][c] *= a;
-          }
-          m = m_new;
-        }
-        float w = vis ? exp2f(x - ref) : 0.f;
-        l += w;
-        w *= v_scale;
-        if (seen == 0xffffffffu) {
-#pragma unroll
-          for (int i = 0; i < kKeys; ++i)
-#pragma unroll
-            for (int r = 0; r < R; ++r) {
-              const float a = __shfl_sync(0xffffffffu, w, kScores == 32 ? i * R + r : 2 * (i * R + r));
-#pragma unroll
-              for (int c = 0; c < 8; ++c) o[r][c] = fmaf(a, v[i][c], o[r][c]);
-            }
-        } else {
+        for (int r = 0; r < R; ++r) {
+          const int src = kScores == 32 ? i * R + r : 2 * (i * R + r);
+          const float a = __shfl_sync(0xffffffffu, w, src);
+          const uint64_t a2 = pack2(a, a);
           // A hidden value takes no part at all: 0 times an infinity would be NaN.
+          if (seen == 0xffffffffu || ((seen >> src) & 1u)) {
 #pragma unroll
-          for (int i = 0; i < kKeys; ++i)
-#pragma unroll
-            for (int r = 0; r < R; ++r) {
-              const int src = kScores == 32 ? i * R + r : 2 * (i * R + r);
-              const float a = __shfl_sync(0xffffffffu, w, src);
-              if ((seen >> src) & 1u) {
-#pragma unroll
-                for (int c = 0; c < 8; ++c) o[r][c] = fmaf(a, v[i][c], o[r][c]);
-              }
-            }
+            for (int c = 0; c < 4; ++c) ffma2(o[r][c], a2, v[c]);
+          }
         }
       }
     }
+    asm volatile("cp.async.wait_all;" ::: "memory");
+    __syncthreads();  // every warp is done with its ring
     // The warps' results: maxima and sums per row, outputs, then one sum over the warps.
+    float* outs = reinterpret_cast<float*>(smem);
     l += __shfl_xor_sync(0xffffffffu, l, 8);
     l += __shfl_xor_sync(0xffffffffu, l, 16);
     if (my_key == 0 && (kScores == 32 || (lane & 1) == 0)) sh_m[warp * R + my_row] = m, sh_l[warp * R + my_row] = l;
 #pragma unroll
-    for (int r = 0; r < R; ++r) store8(smem + (warp * R + r) * kHeadDim + 8 * lane, o[r]);
+    for (int r = 0; r < R; ++r)
+#pragma unroll
+      for (int f = 0; f < 2; ++f) {
+        const float2 a = unpack2(o[r][2 * f]), b = unpack2(o[r][2 * f + 1]);
+        const float y[4] = {a.x, a.y, b.x, b.y};
+        store4(outs + (warp * R + r) * kHeadDim + column<kCache>(lane, f), y);
+      }
     __syncthreads();
     const int slot = g.slot();
     const bool whole = g.whole();
@@ -191,7 +292,7 @@ __global__ void __launch_bounds__(kThreads, R == 4 ? 2 : 1) tree_ffma_kernel(con
         if (a == 0.f && lw == lw) continue;  // a warp that saw none of the row's keys (NaN scores go on)
         sum = fmaf(a, lw, sum);
         float y[8];
-        load8(smem + (w * R + r) * kHeadDim + 8 * lane, y);
+        load8(outs + (w * R + r) * kHeadDim + 8 * lane, y);
 #pragma unroll
         for (int c = 0; c < 8; ++c) acc[c] = fmaf(a, y[c], acc[c]);
       }
@@ -215,14 +316,24 @@ __global__ void __launch_bounds__(kThreads, R == 4 ? 2 : 1) tree_ffma_kernel(con
   }
 }
 
-// One warp per output row: heads that one worker holds whole are written already; others
-// are merged from their workers' partial results in worker order, and rows of sequences
-// without tiles are cleared.
+// kPerRow warps per output row: heads that one worker holds whole are written already; others
+// are merged from their workers' partial results, and rows of sequences without tiles are
+// cleared.  With kPerRow = 8 (few rows, and then many partial results to each) warp i takes
+// every eighth of them and the warps' sums are added in their order, so the order of the
+// additions is fixed.  The kernel may start while the one before it still runs
+// (programmatic launch) and waits for it before it reads what that wrote.
+template <int kPerRow>
 __global__ void __launch_bounds__(256) tree_merge_kernel(const __grid_constant__ TreeParams p, int rows_per_tile) {
+  __shared__ float sh_sum[8], sh_max[8];
+  __shared__ float sh_acc[kPerRow == 8 ? 8 : 1][kHeadDim];
   const int64_t rows_per_seq = int64_t(p.c.Hkv) * p.G * p.T;
-  const int64_t row = int64_t(blockIdx.x) * 8 + (threadIdx.x >> 5);
-  if (row >= rows_per_seq * p.B) return;
-  const int lane = threadIdx.x & 31;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int64_t row = kPerRow == 8 ? int64_t(blockIdx.x) : int64_t(blockIdx.x) * 8 + warp;
+  if (row >= rows_per_seq * p.B) {
+    wait_for_grid();
+    return;
+  }
+  const int first = kPerRow == 8 ? warp : 0;  // this warp's first partial result
   const int b = int(row / rows_per_seq);
   const int64_t in_seq = row - b * rows_per_seq;
   const int hq = int(in_seq / p.T), t = int(in_seq - int64_t(hq) * p.T);
@@ -230,39 +341,57 @@ __global__ void __launch_bounds__(256) tree_merge_kernel(const __grid_constant__
   int64_t before;
   const int64_t W = tree_total(p, b, &before) * p.c.Hkv;
   const int64_t tiles = tree_seq(p, b).tiles;
+  const int64_t workers = tree_workers(p, W);
+  const int64_t s0 = before * p.c.Hkv + h * tiles, e0 = s0 + tiles;
+  const int64_t w0 = tiles > 0 ? ((s0 + 1) * workers - 1) / W : 0, w1 = tiles > 0 ? (e0 * workers - 1) / W : -1;
+  wait_for_grid();
+  if (tiles > 0 && w0 == w1) return;
+  const int rt = n / rows_per_tile, r = n % rows_per_tile;
+  auto at = [&](int64_t w) {
+    return ((w * 2 + (w == w0 ? 1 : 0)) * p.row_tiles + rt) * rows_per_tile + r;
+  };
+  // Lane i takes the log-sum-exp of this warp's partial result i of each 32: their weights
+  // first, then the outputs, four loads in flight.
   float acc[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
   float mx = -INFINITY, sum = 0.f;
-  if (tiles > 0) {
-    const int64_t workers = tree_workers(p, W);
-    const int64_t s0 = before * p.c.Hkv + h * tiles, e0 = s0 + tiles;
-    const int64_t w0 = ((s0 + 1) * workers - 1) / W, w1 = (e0 * workers - 1) / W;
-    if (w0 == w1) return;
-    const int rt = n / rows_per_tile, r = n % rows_per_tile;
-    auto at = [&](int64_t w) {
-      return ((w * 2 + (w == w0 ? 1 : 0)) * p.row_tiles + rt) * rows_per_tile + r;
-    };
-    // Lane i takes the log-sum-exp of partial result i of each 32: their weights first, then
-    // the outputs, eight loads in flight.
-    for (int64_t w = w0 + lane; w <= w1; w += 32) mx = fmaxf(mx, p.lse_part[at(w)]);
+  for (int64_t w = w0 + first + lane * kPerRow; w <= w1; w += 32 * kPerRow) mx = fmaxf(mx, p.lse_part[at(w)]);
 #pragma unroll
-    for (int s = 16; s >= 1; s >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, s));
-    const float ref = mx == -INFINITY ? 0.f : mx;
-    for (int64_t wb = w0; wb <= w1; wb += 32) {
-      const float mine = wb + lane <= w1 ? expf(p.lse_part[at(wb + lane)] - ref) : 0.f;
-      const int n = int(min(int64_t(32), w1 - wb + 1));
-      for (int i = 0; i < n; i += 4) {
-        float y[4][8];
+  for (int s = 16; s >= 1; s >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, s));
+  if constexpr (kPerRow == 8) {
+    if (lane == 0) sh_max[warp] = mx;
+    __syncthreads();
+    for (int w = 0; w < 8; ++w) mx = fmaxf(mx, sh_max[w]);
+  }
+  const float ref = mx == -INFINITY ? 0.f : mx;
+  for (int64_t wb = w0 + first; wb <= w1; wb += 32 * kPerRow) {
+    const float mine = wb + lane * kPerRow <= w1 ? expf(p.lse_part[at(wb + lane * kPerRow)] - ref) : 0.f;
+    const int count = int(min(int64_t(32), (w1 - wb) / kPerRow + 1));
+    for (int i = 0; i < count; i += 4) {
+      float y[4][8];
 #pragma unroll
-        for (int k = 0; k < 4; ++k) load8(p.o_part + at(min(wb + i + k, w1)) * kHeadDim + 8 * lane, y[k]);
+      for (int k = 0; k < 4; ++k)
+        load8(p.o_part + at(wb + min(i + k, count - 1) * kPerRow) * kHeadDim + 8 * lane, y[k]);
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          const float a = __shfl_sync(0xffffffffu, mine, (i + k) & 31);
-          if (i + k >= n || a == 0.f) continue;  // a partial result without a visible key is not used
-          sum += a;
+      for (int k = 0; k < 4; ++k) {
+        const float a = __shfl_sync(0xffffffffu, mine, (i + k) & 31);
+        if (i + k >= count || a == 0.f) continue;  // a partial result without a visible key is not used
+        sum += a;
 #pragma unroll
-          for (int c = 0; c < 8; ++c) acc[c] = fmaf(a, y[k][c], acc[c]);
-        }
+        for (int c = 0; c < 8; ++c) acc[c] = fmaf(a, y[k][c], acc[c]);
       }
+    }
+  }
+  if constexpr (kPerRow == 8) {
+    store8(&sh_acc[warp][8 * lane], acc);
+    if (lane == 0) sh_sum[warp] = sum;
+    __syncthreads();
+    if (warp != 0) return;
+    for (int w = 1; w < 8; ++w) {
+      float y[8];
+      load8(&sh_acc[w][8 * lane], y);
+      sum += sh_sum[w];
+#pragma unroll
+      for (int c = 0; c < 8; ++c) acc[c] += y[c];
     }
   }
   const float inv = sum == 0.f ? 0.f : 1.f / sum;
@@ -277,10 +406,9 @@ __global__ void __launch_bounds__(256) tree_merge_kernel(const __grid_constant__
 
 template <int R, int kCache, typename QT>
 int launch_one(const TreeParams& p, cudaStream_t stream) {
-  constexpr int smem = (kWarps * R * kHeadDim + 2 * kWarps * R) * 4;
-  if (cudaFuncSetAttribute(tree_ffma_kernel<R, kCache, QT>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) !=
-      cudaSuccess)
-    return GQA_ERR_LAUNCH;
+  constexpr int ring = kWarps * kStages * 2 * kKeys * RowBytes<kCache>::value, outs = kWarps * R * kHeadDim * 4;
+  constexpr int smem = ring > outs ? ring : outs;
+  if (!allow_smem<tree_ffma_kernel<R, kCache, QT>>(smem)) return GQA_ERR_LAUNCH;
   tree_ffma_kernel<R, kCache, QT><<<unsigned(p.workers) * unsigned(p.row_tiles), kThreads, smem, stream>>>(p);
   return cudaGetLastError() == cudaSuccess ? GQA_OK : GQA_ERR_LAUNCH;
 }
@@ -304,7 +432,7 @@ TreeShape tree_shape(int B, int Hkv, int G, int64_t T, int64_t max_pages, int pa
   else
     s.rows = rows <= 4 ? 4 : 8;
   s.row_tiles = int((rows + s.rows - 1) / s.rows);
-  const int slots = kB200Sms * (s.rows == 4 ? 2 : 1);
+  const int slots = kB200Sms;
   s.workers = slots / s.row_tiles > 1 ? slots / s.row_tiles : 1;
   // No more workers than tiles that the page tables could hold.
   const int64_t tiles = (max_pages * page_size + kTreeTile - 1) / kTreeTile * B * Hkv;
@@ -318,10 +446,21 @@ int launch_tree_ffma(const TreeParams& p, bool q_bf16, int rows, cudaStream_t st
 
 int launch_tree_merge(const TreeParams& p, int rows_per_tile, cudaStream_t stream) {
   const int64_t rows = int64_t(p.B) * p.c.Hkv * p.G * p.T;
-  const int64_t blocks = (rows + 7) / 8;
+  const bool few = rows <= 2 * kB200Sms;  // a CTA per row then fills the SMs about once
+  const int64_t blocks = few ? rows : (rows + 7) / 8;
   if (blocks > 0x7fffffff) return GQA_ERR_UNSUPPORTED;
-  tree_merge_kernel<<<unsigned(blocks), 256, 0, stream>>>(p, rows_per_tile);
-  return cudaGetLastError() == cudaSuccess ? GQA_OK : GQA_ERR_LAUNCH;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(unsigned(blocks));
+  cfg.blockDim = dim3(256);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  const cudaError_t e = few ? cudaLaunchKernelEx(&cfg, tree_merge_kernel<8>, p, rows_per_tile)
+                            : cudaLaunchKernelEx(&cfg, tree_merge_kernel<1>, p, rows_per_tile);
+  return e == cudaSuccess ? GQA_OK : GQA_ERR_LAUNCH;
 }
 
 }  // namespace gqa

@@ -12,6 +12,8 @@
 // tiles side by side, so a tile comes from HBM once and from L2 for the others.
 #pragma once
 
+#include <atomic>
+
 #include "decode.cuh"
 
 namespace gqa {
@@ -153,12 +155,30 @@ __device__ __forceinline__ bool tree_next(const TreeParams& p, TreeCursor& c, Tr
   return true;
 }
 
+// Programmatic launch: the kernel behind may start, and wait for the one before to end.
+__device__ __forceinline__ void launch_dependents() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+__device__ __forceinline__ void wait_for_grid() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
 // Whether drafted token t sees drafted token u (both below s.drafted).
 __device__ __forceinline__ bool tree_sees(const TreeParams& p, int b, int t, int u) {
   return p.mask ? p.mask[b * p.mask_sb + int64_t(t) * p.T + u] != 0 : u <= t;
 }
 
 #endif  // __CUDACC__
+
+// Lets a kernel use `bytes` of dynamic shared memory on the current device; asked of the driver
+// once per kernel and device (about 1 us of a decoding step's 20 on the host).
+template <auto kKernel>
+bool allow_smem(int bytes) {
+  static std::atomic<uint64_t> done{0};
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return false;
+  const uint64_t bit = dev < 64 ? uint64_t(1) << dev : 0;
+  if (done.load(std::memory_order_relaxed) & bit) return true;
+  if (cudaFuncSetAttribute(kKernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) != cudaSuccess) return false;
+  done.fetch_or(bit, std::memory_order_relaxed);
+  return true;
+}
 
 // FP32 pipe: q of either type, any pages but bf16 q over bf16 or e4m3 ones; rows 4 or 8.
 int launch_tree_ffma(const TreeParams& p, bool q_bf16, int rows, cudaStream_t stream);

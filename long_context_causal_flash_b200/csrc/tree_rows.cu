@@ -111,6 +111,7 @@ __global__ void __launch_bounds__(RowsCfg<kFp8>::kThreads, 1) tree_rows_kernel(c
   __syncthreads();
   umma::fence_after_sync();
   const uint32_t tmem = tmem_slot;
+  launch_dependents();
   TreeCursor cur = start;
   TreeSegment g;
 
@@ -559,8 +560,7 @@ int launch(const TreeParams& p, cudaStream_t stream) {
   using F = RowsCfg<kFp8>;
   CUtensorMap mk, mv;
   if (!encode_pages(&mk, p.c, false) || !encode_pages(&mv, p.c, true)) return GQA_ERR_LAUNCH;
-  if (cudaFuncSetAttribute(tree_rows_kernel<kFp8>, cudaFuncAttributeMaxDynamicSharedMemorySize, F::kSmem) != cudaSuccess)
-    return GQA_ERR_LAUNCH;
+  if (!allow_smem<tree_rows_kernel<kFp8>>(F::kSmem)) return GQA_ERR_LAUNCH;
   tree_rows_kernel<kFp8><<<unsigned(p.workers) * unsigned(p.row_tiles), F::kThreads, F::kSmem, stream>>>(mk, mv, p);
   return cudaGetLastError() == cudaSuccess ? GQA_OK : GQA_ERR_LAUNCH;
 }

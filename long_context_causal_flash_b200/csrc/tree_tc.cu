@@ -150,6 +150,7 @@ __global__ void __launch_bounds__(Cfg<kN, kFp8>::kThreads, 1) tree_tc_kernel(con
   __syncthreads();
   umma::fence_after_sync();
   const uint32_t tmem = tmem_slot;
+  launch_dependents();
   TreeCursor cur = start;
   TreeSegment g;
 
@@ -612,9 +613,7 @@ __global__ void __launch_bounds__(Cfg<kN, kFp8>::kThreads, 1) tree_tc_kernel(con
 template <int kN, bool kFp8>
 int launch_n(const TreeParams& p, const CUtensorMap& mk, const CUtensorMap& mv, cudaStream_t stream) {
   using F = Cfg<kN, kFp8>;
-  if (cudaFuncSetAttribute(tree_tc_kernel<kN, kFp8>, cudaFuncAttributeMaxDynamicSharedMemorySize, F::kSmem) !=
-      cudaSuccess)
-    return GQA_ERR_LAUNCH;
+  if (!allow_smem<tree_tc_kernel<kN, kFp8>>(F::kSmem)) return GQA_ERR_LAUNCH;
   tree_tc_kernel<kN, kFp8><<<unsigned(p.workers) * unsigned(p.row_tiles), F::kThreads, F::kSmem, stream>>>(mk, mv, p);
   return cudaGetLastError() == cudaSuccess ? GQA_OK : GQA_ERR_LAUNCH;
 }
