@@ -3,8 +3,8 @@
 //
 // A CTA holds R query rows (R / G tokens of the G heads of one key/value head) and
 // streams its worker's tiles; 8 warps take 16 of a tile's 128 keys each, four keys at a
-// time, through a ring of three groups of its own in shared memory (cp.async), so that no
-// warp waits for another and two groups per warp are under way.  A lane owns eight columns
+// time, through a ring of three groups of its own in shared memory (a bulk copy per row), so
+// that no warp waits for another and two groups per warp are under way.  A lane owns eight columns
 // of q, k, v and of the output.  The 4 R partial dot products of a lane (packed FMAs, two
 // columns each) are summed over the lanes by halving exchanges (a lane sends the half it
 // does not keep), which leaves one score per lane, or per pair of lanes at R = 4, where the
@@ -12,6 +12,8 @@
 // scores, and the output is rescaled only when some row's maximum rose.  With R = 8 a group
 // is 256 packed FMAs, 512 cycles of the FMA pipe, and about as many issue slots; with 4 rows
 // fp32 pages are bound by memory, with 8 and more by the FMA pipe.
+#include <type_traits>
+
 #include "internal.h"
 #include "tree.cuh"
 
@@ -98,10 +100,15 @@ __global__ void __launch_bounds__(kThreads, 1) tree_ffma_kernel(const __grid_con
   extern __shared__ __align__(16) char smem[];
   __shared__ TreeCursor start;
   __shared__ float sh_m[kWarps * R], sh_l[kWarps * R];
+  __shared__ __align__(16) float sh_w[kWarps][R * kKeys];        // a group's weights
+  __shared__ __align__(8) uint64_t sh_bar[kWarps * kStages];  // a ring's slots: their copies are complete
   constexpr int kRow = RowBytes<kCache>::value, kStage = 2 * kKeys * kRow;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int worker = blockIdx.x / p.row_tiles, rt = blockIdx.x % p.row_tiles;
   char* ring = smem + warp * kStages * kStage;
+  const uint32_t bars = smem_u32(sh_bar) + uint32_t(warp * kStages) * 8u;
+  if (lane < kStages) mbar_init(bars + 8u * lane, 1);
+  fence_barrier_init();
   if (warp == 0) {
     const TreeCursor c = tree_start(p, worker);
     if (lane == 0) start = c;
@@ -109,6 +116,8 @@ __global__ void __launch_bounds__(kThreads, 1) tree_ffma_kernel(const __grid_con
   __syncthreads();
   launch_dependents();
   TreeCursor cur = start;
+  uint32_t used = 0;  // groups whose copies this warp has asked for
+  bool ok = true;
 
   constexpr int kScores = R * kKeys;  // 32 or 16
   const int idx = kScores == 32 ? lane : lane >> 1;
@@ -118,7 +127,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_ffma_kernel(const __grid_con
   constexpr int kEs = kRow / kHeadDim;
 
   TreeSegment g;
-  while (tree_next(p, cur, &g)) {
+  while (ok && tree_next(p, cur, &g)) {
     const int32_t* table = p.table + int64_t(g.b) * p.max_pages;
     uint64_t q[R][4], o[R][4];
 #pragma unroll
@@ -140,48 +149,54 @@ __global__ void __launch_bounds__(kThreads, 1) tree_ffma_kernel(const __grid_con
     auto first_key = [&](int n) {
       return uint32_t(g.t0 + n / kGroups) * kTreeTile + uint32_t(warp * kKeysPerWarp + n % kGroups * kKeys);
     };
-    // Its copies, by all lanes; rows that are not there are zeros.  Returns how many keys are.
+    // The page table's entry of a group, loaded a group ahead of its use.
+    auto entry_at = [&](int n) {
+      return n < groups && first_key(n) < g.s.keys ? page_entry(p.c, table, p.max_pages, first_key(n)) : -1;
+    };
+    int entry = entry_at(0);
+    // The next group's copies: lanes 0 .. 3 the rows of k, 4 .. 7 those of v.  Rows that are not
+    // there are left as they were, and hidden below.  Returns how many keys are.
     auto fetch = [&](int n) {
+      const uint32_t stage = used % kStages;
       int live = 0;
       if (n < groups) {
         const uint32_t j0 = first_key(n);
-        const int page = j0 < g.s.keys ? page_of(p.c, table, p.max_pages, j0) : -1;
+        const int page = j0 < g.s.keys ? page_checked(p.c, entry) : -1;
+        entry = entry_at(n + 1);
         live = page < 0 ? 0 : int(min(uint32_t(kKeys), g.s.keys - j0));
-        const int64_t at = (int64_t(max(page, 0)) * p.c.sp + g.h * p.c.sh + (j0 & slot_mask) * p.c.st) * kEs;
-        const uint32_t dst = smem_u32(ring + n % kStages * kStage);
-        constexpr int kUnits = kRow / 16;  // 16-byte units of a row
-        constexpr int kRowsAtOnce = kUnits >= 32 ? 1 : 32 / kUnits;
-#pragma unroll
-        for (int kv = 0; kv < 2; ++kv)
-#pragma unroll
-          for (int i = 0; i < kKeys; i += kRowsAtOnce)
-#pragma unroll
-            for (int u0 = 0; u0 < kUnits; u0 += 32) {
-              const int row = i + (kUnits >= 32 ? 0 : lane / kUnits), unit = u0 + lane % (kUnits >= 32 ? 32 : kUnits);
-              const char* src = (kv ? p.c.v : p.c.k) + at + row * p.c.st * kEs + unit * 16;
-              asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(
-                               dst + uint32_t((kv * kKeys + row) * kRow + unit * 16)),
-                           "l"(row < live ? src : p.c.k), "r"(row < live ? 16 : 0)
-                           : "memory");
-            }
+        if (lane == 0) mbar_arrive_expect_tx(bars + 8u * stage, uint32_t(2 * live * kRow));
+        __syncwarp();
+        const int row = lane & (kKeys - 1);
+        if (lane < 2 * kKeys && row < live) {
+          const int64_t at = (int64_t(page) * p.c.sp + g.h * p.c.sh + ((j0 & slot_mask) + row) * p.c.st) * kEs;
+          asm volatile(
+              "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
+                  smem_u32(ring) + stage * uint32_t(kStage) + uint32_t(lane * kRow)),
+              "l"((lane < kKeys ? p.c.k : p.c.v) + at), "r"(uint32_t(kRow)), "r"(bars + 8u * stage)
+              : "memory");
+        }
+        ++used;
       }
-      asm volatile("cp.async.commit_group;" ::: "memory");
       return live;
     };
-    int live_at[kStages];  // of the groups in the ring, the next one first
+    const uint32_t base = used;  // the segment's first group in the ring
+    int live_at[kStages];        // of the groups in the ring, the next one first
 #pragma unroll
     for (int i = 0; i < kStages - 1; ++i) live_at[i] = fetch(i);
     for (int n = 0; n < groups; ++n) {
       __syncwarp();  // the stage to be filled has been read by all lanes
       live_at[kStages - 1] = fetch(n + kStages - 1);
-      asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 1) : "memory");
-      __syncwarp();
+      const uint32_t turn = base + uint32_t(n);
+      if (!__all_sync(0xffffffffu, mbar_wait_inline(bars + 8u * (turn % kStages), (turn / kStages) & 1u, p.wait_budget_ns,
+                                                    p.c.status)))
+        ok = false;
+      if (!ok) break;
       const int live = live_at[0];
 #pragma unroll
       for (int i = 0; i + 1 < kStages; ++i) live_at[i] = live_at[i + 1];
       if (live == 0) continue;
       const uint32_t j0 = first_key(n);
-      const char* stage = ring + n % kStages * kStage;
+      const char* stage = ring + turn % kStages * kStage;
       float k_scale = 1.f, v_scale = 1.f;
       if constexpr (kCache == GQA_E4M3) {
         const int page = page_of(p.c, table, p.max_pages, j0);
@@ -240,26 +255,42 @@ __global__ void __launch_bounds__(kThreads, 1) tree_ffma_kernel(const __grid_con
       }
       float w = vis ? exp2f(x - ref) : 0.f;
       l += w;
-      w *= v_scale;
+      sh_w[warp][idx] = w * v_scale;
+      __syncwarp();
+      // A hidden value takes no part at all: 0 times an infinity would be NaN.
+      auto add_values = [&](auto all) {
 #pragma unroll
-      for (int i = 0; i < kKeys; ++i) {
-        uint64_t v[4];
-        staged<kCache>(stage + (kKeys + i) * kRow, lane, v);
+        for (int i = 0; i < kKeys; ++i) {
+          uint64_t v[4];
+          staged<kCache>(stage + (kKeys + i) * kRow, lane, v);
 #pragma unroll
-        for (int r = 0; r < R; ++r) {
-          const int src = kScores == 32 ? i * R + r : 2 * (i * R + r);
-          const float a = __shfl_sync(0xffffffffu, w, src);
-          const uint64_t a2 = pack2(a, a);
-          // A hidden value takes no part at all: 0 times an infinity would be NaN.
-          if (seen == 0xffffffffu || ((seen >> src) & 1u)) {
+          for (int r = 0; r < R; r += 4) {
+            const float4 a = *reinterpret_cast<const float4*>(&sh_w[warp][i * R + r]);
+            const float a4[4] = {a.x, a.y, a.z, a.w};
 #pragma unroll
-            for (int c = 0; c < 4; ++c) ffma2(o[r][c], a2, v[c]);
+            for (int k = 0; k < 4; ++k) {
+              const int src = kScores == 32 ? i * R + r + k : 2 * (i * R + r + k);
+              if (decltype(all)::value || ((seen >> src) & 1u)) {
+                const uint64_t a2 = pack2(a4[k], a4[k]);
+#pragma unroll
+                for (int c = 0; c < 4; ++c) ffma2(o[r + k][c], a2, v[c]);
+              }
+            }
           }
         }
-      }
+      };
+      if (seen == 0xffffffffu)
+        add_values(std::true_type{});
+      else
+        add_values(std::false_type{});
     }
-    asm volatile("cp.async.wait_all;" ::: "memory");
-    __syncthreads();  // every warp is done with its ring
+    // Every warp is done with its ring.  After a wait that ran out the others are given one more
+    // chance each, so that no copy is left under way, and the call ends.
+    if (!__syncthreads_and(ok)) {
+      for (uint32_t i = used > kStages ? used - kStages : 0; i < used; ++i)
+        mbar_wait_inline(bars + 8u * (i % kStages), (i / kStages) & 1u, p.wait_budget_ns, p.c.status);
+      break;
+    }
     // The warps' results: maxima and sums per row, outputs, then one sum over the warps.
     float* outs = reinterpret_cast<float*>(smem);
     l += __shfl_xor_sync(0xffffffffu, l, 8);
@@ -312,6 +343,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_ffma_kernel(const __grid_con
         if (lane == 0) p.lse_part[part * R + r] = lse;
       }
     }
+    fence_proxy_async_smem();  // the next segment's copies take the outputs' place
     __syncthreads();
   }
 }
