@@ -39,9 +39,14 @@ struct RopeView {
 // A row of 256 columns is the work of 16 threads, `unit` 0 .. 15, each with 16 columns.
 // A rotated unit (unit < rot / 16) holds pairs 8 unit .. 8 unit + 7: with the half layout
 // columns 8 unit + (0..7) and rot / 2 + 8 unit + (0..7), else columns 16 unit + (0..15).
-// c0 / c1 are the first columns of its two groups of eight.
+// Rows that are not rotated at all (rot = 0) go like those of rot = 256 in the half layout,
+// whose loads and stores are contiguous over the threads.  c0 / c1 are the first columns of
+// the unit's two groups of eight.
 __device__ __forceinline__ void unit_columns(int unit, int rot, int interleaved, int* c0, int* c1) {
-  if (!interleaved && unit < rot / 16) {
+  if (rot == 0) {
+    *c0 = 8 * unit;
+    *c1 = 128 + 8 * unit;
+  } else if (!interleaved && unit < rot / 16) {
     *c0 = 8 * unit;
     *c1 = rot / 2 + 8 * unit;
   } else {
@@ -65,6 +70,35 @@ __device__ __forceinline__ void unpack8(uint4 u, float* x) {
 __device__ __forceinline__ void load8(const __nv_bfloat16* p, float* x) {
   unpack8(*reinterpret_cast<const uint4*>(p), x);
 }
+// Sixteen columns as they were loaded: bf16 in half the registers of their values, so that more
+// loads are in flight at the same occupancy.
+template <typename T>
+struct Raw16;
+template <>
+struct Raw16<__nv_bfloat16> {
+  uint4 a, b;
+  __device__ __forceinline__ void load(const __nv_bfloat16* p, const __nv_bfloat16* q) {
+    a = *reinterpret_cast<const uint4*>(p);
+    b = *reinterpret_cast<const uint4*>(q);
+  }
+  __device__ __forceinline__ void values(float* x) const {
+    unpack8(a, x);
+    unpack8(b, x + 8);
+  }
+};
+template <>
+struct Raw16<float> {
+  float x[16];
+  __device__ __forceinline__ void load(const float* p, const float* q) {
+    load8(p, x);
+    load8(q, x + 8);
+  }
+  __device__ __forceinline__ void values(float* y) const {
+#pragma unroll
+    for (int i = 0; i < 16; ++i) y[i] = x[i];
+  }
+};
+
 __device__ __forceinline__ void store8(float* p, const float* x) {
   *reinterpret_cast<float4*>(p) = make_float4(x[0], x[1], x[2], x[3]);
   *reinterpret_cast<float4*>(p + 4) = make_float4(x[4], x[5], x[6], x[7]);
@@ -123,19 +157,37 @@ __device__ __forceinline__ int page_of(const CacheView& c, const int32_t* table,
   return page_checked(c, page_entry(c, table, max_pages, j));
 }
 
-// cos and sin of the eight pairs of a rotated unit at position p, times m.  p * turns
-// modulo 2^64 is the angle as a fraction of a turn, exact; its upper 32 bits, as a signed
-// number of 2^-32 turns in [-1/2, 1/2), go to fp32 and sincospi.
+// cos and sin of a fraction of a turn, `frac` 2^-64 turns, times m.  The angle is taken to the
+// nearest quarter turn and an eighth around it, |a| <= pi / 4, in whole numbers; there the
+// Taylor series of sine and cosine to a^9 and a^10 leave less than 2e-9, so the results are
+// off by the fp32 roundings of a (half a step) and of the sums.
+__device__ __forceinline__ void turn_angle(uint64_t frac, float m, float* co, float* si) {
+  const uint32_t top = uint32_t(frac >> 32);                   // 2^-32 turns
+  const uint32_t quarter = (top + 0x20000000u) >> 30;          // nearest quarter turn
+  const float a = float(int32_t(top - (quarter << 30))) * 1.4629180792671596e-9f;  // 2 pi 2^-32
+  const float z = a * a;
+  float s = fmaf(z, 2.7557319224e-6f, -1.9841269841e-4f);  // 1 / 9!, -1 / 7!
+  s = fmaf(s, z, 8.3333333333e-3f);
+  s = fmaf(s, z, -1.6666666667e-1f);
+  s = fmaf(s * z, a, a);
+  float c = fmaf(z, -2.7557319224e-7f, 2.4801587302e-5f);  // -1 / 10!, 1 / 8!
+  c = fmaf(c, z, -1.3888888889e-3f);
+  c = fmaf(c, z, 4.1666666667e-2f);
+  c = fmaf(c, z, -0.5f);
+  c = fmaf(c, z, 1.f);
+  const float x = quarter & 1u ? s : c, y = quarter & 1u ? c : s;
+  *co = (((quarter + 1u) & 2u) ? -x : x) * m;
+  *si = ((quarter & 2u) ? -y : y) * m;
+}
+
+// cos and sin of the eight pairs of a rotated unit at position p, times m: p * turns modulo
+// 2^64 is the angle as a fraction of a turn, exact.
 __device__ __forceinline__ void unit_angles(const uint64_t* turns, int unit, int64_t p, float m, float sign, float* co,
                                             float* si) {
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
-    const uint64_t frac = uint64_t(p) * __ldg(reinterpret_cast<const unsigned long long*>(turns) + 8 * unit + i);
-    const float half_turns = float(int32_t(uint32_t(frac >> 32))) * 4.656612873077393e-10f;  // 2^-31
-    float s, c;
-    sincospif(half_turns, &s, &c);
-    co[i] = c * m;
-    si[i] = s * m * sign;
+    turn_angle(uint64_t(p) * __ldg(reinterpret_cast<const unsigned long long*>(turns) + 8 * unit + i), m, &co[i], &si[i]);
+    si[i] *= sign;
   }
 }
 

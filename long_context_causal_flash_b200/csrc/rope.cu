@@ -19,7 +19,7 @@ constexpr int kTokens = kThreads / 16;  // tokens per CTA
 constexpr int kBatch = 4;               // heads whose loads are in flight together
 
 template <typename T>
-__global__ void __launch_bounds__(kThreads) rope_kernel(RowsView x, RowsView y, RowsView x2, RowsView y2, int64_t tokens,
+__global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 3 : 2) rope_kernel(RowsView x, RowsView y, RowsView x2, RowsView y2, int64_t tokens,
                                                         int64_t L, RopeView r, float sign, int heads_per_thread) {
   const int unit = threadIdx.x & 15;
   const int64_t token = int64_t(blockIdx.x) * kTokens + (threadIdx.x >> 4);
@@ -36,25 +36,26 @@ __global__ void __launch_bounds__(kThreads) rope_kernel(RowsView x, RowsView y, 
   const int H = x.H + x2.H;
   const int h_end = min(H, (int(blockIdx.y) + 1) * heads_per_thread);
   for (int h0 = int(blockIdx.y) * heads_per_thread; h0 < h_end; h0 += kBatch) {
-    float v[kBatch][16];
+    Raw16<T> raw[kBatch];
 #pragma unroll
     for (int i = 0; i < kBatch; ++i) {
       const int h = h0 + i;
       if (h >= h_end) break;
       const RowsView& s = h < x.H ? x : x2;
       const T* src = reinterpret_cast<const T*>(s.p) + b * s.sb + int64_t(h < x.H ? h : h - x.H) * s.sh + l * s.sl;
-      load8(src + c0, v[i]);
-      load8(src + c1, v[i] + 8);
+      raw[i].load(src + c0, src + c1);
     }
 #pragma unroll
     for (int i = 0; i < kBatch; ++i) {
       const int h = h0 + i;
       if (h >= h_end) break;
-      if (turned) turn_unit(v[i], r.interleaved, co, si);
+      float v[16];
+      raw[i].values(v);
+      if (turned) turn_unit(v, r.interleaved, co, si);
       const RowsView& d = h < x.H ? y : y2;
       T* dst = reinterpret_cast<T*>(d.p) + b * d.sb + int64_t(h < x.H ? h : h - x.H) * d.sh + l * d.sl;
-      store8(dst + c0, v[i]);
-      store8(dst + c1, v[i] + 8);
+      store8(dst + c0, v);
+      store8(dst + c1, v + 8);
     }
   }
 }
@@ -67,8 +68,14 @@ int launch_rope(const RowsView& x, const RowsView& y, const RowsView& x2, const 
   if (tokens == 0) return GQA_OK;
   const int64_t blocks = (tokens + kTokens - 1) / kTokens;
   const int H = x.H + x2.H;
-  const int hpt = kBatch;
-  const int64_t groups = (H + hpt - 1) / hpt;
+  // Heads of a token per thread.  Its sines and cosines cost about as much as turning four heads,
+  // so all heads share them where the tokens alone fill the GPU twice (8 CTAs to an SM), and
+  // few tokens are spread over more threads, down to one batch of heads each.
+  const int batches = (H + kBatch - 1) / kBatch;
+  int64_t groups = (8 * 148 + blocks - 1) / blocks;
+  groups = groups < batches ? groups : batches;
+  const int hpt = int((batches + groups - 1) / groups) * kBatch;
+  groups = (H + hpt - 1) / hpt;
   if (blocks > 0x7fffffff || groups > 65535) return GQA_ERR_UNSUPPORTED;
   const dim3 grid(static_cast<unsigned>(blocks), static_cast<unsigned>(groups));
   const float sign = inverse ? -1.f : 1.f;
