@@ -186,13 +186,14 @@ int gqa_attn_fwd_tree(const gqa_rows_t* q, const gqa_cache_t* cache, const int32
   p.B = B;
   p.T = int(T);
   p.G = G;
+  p.tile_shift = s.tile_shift;
   p.workers = s.workers;
   p.row_tiles = s.row_tiles;
   p.out_bf16 = dtype == GQA_BF16;
   p.scale_log2 = float(1.0 / std::sqrt(double(d)) * 1.4426950408889634);
   p.wait_budget_ns = wait_budget_ns();
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-  rc = s.tensor ? launch_tree_tc(p, s.rows, st) : launch_tree_ffma(p, dtype == GQA_BF16, s.rows, st);
+  rc = s.tensor ? launch_tree_tc(p, s.rows, st) : launch_tree_f32(p, s.rows, dtype == GQA_BF16, st);
   return rc != GQA_OK ? rc : launch_tree_merge(p, s.rows, st);
 }
 

@@ -18,7 +18,8 @@
 
 namespace gqa {
 
-constexpr int kTreeTile = 128;
+constexpr int kTreeTileShift = 7, kTreeTile = 1 << kTreeTileShift;
+constexpr int kTreeTileShiftF32 = 5;  // its kernel's step: a worker then has a chunk more than another, not four
 
 struct TreeParams {
   RowsView q;
@@ -33,6 +34,7 @@ struct TreeParams {
   float* o_part;    // [workers][2][row tiles][rows of a tile][256]
   float* lse_part;  // [workers][2][row tiles][rows of a tile]
   int B, T, G, workers, row_tiles;
+  int tile_shift;  // log2 of a tile's keys
   bool out_bf16;
   float scale_log2;
   int64_t wait_budget_ns;
@@ -54,7 +56,7 @@ __device__ __forceinline__ TreeSeq tree_seq(const TreeParams& p, int b) {
   s.ctx = uint32_t(max(ctx, 0));
   if (ctx < 0 || int64_t(s.ctx) + s.drafted > cap) set_status(p.c.status, GQA_ERR_DEVICE_BOUNDS);
   s.keys = uint32_t(min(int64_t(s.ctx) + s.drafted, cap));
-  s.tiles = s.drafted > 0 ? int((s.keys + kTreeTile - 1) / kTreeTile) : 0;
+  s.tiles = s.drafted > 0 ? int((s.keys + (1u << p.tile_shift) - 1) >> p.tile_shift) : 0;
   return s;
 }
 
@@ -180,8 +182,9 @@ bool allow_smem(int bytes) {
   return true;
 }
 
-// FP32 pipe: q of either type, any pages but bf16 q over bf16 or e4m3 ones; rows 4 or 8.
-int launch_tree_ffma(const TreeParams& p, bool q_bf16, int rows, cudaStream_t stream);
+// fp32 accuracy: q of either type, any pages but bf16 q over bf16 or e4m3 ones; rows 8, 16
+// or 24.
+int launch_tree_f32(const TreeParams& p, int rows, bool q_bf16, cudaStream_t stream);
 // Tensor cores: bf16 q over bf16 or e4m3 pages; rows 16, 32, 64 (the keys as M) or 128.
 int launch_tree_tc(const TreeParams& p, int rows, cudaStream_t stream);
 int launch_tree_rows(const TreeParams& p, cudaStream_t stream);
@@ -190,6 +193,7 @@ int launch_tree_merge(const TreeParams& p, int rows_per_tile, cudaStream_t strea
 // Rows per CTA and worker count of a call, by types and shape (host).
 struct TreeShape {
   int rows, row_tiles, workers;
+  int tile_shift;
   bool tensor;
 };
 TreeShape tree_shape(int B, int Hkv, int G, int64_t T, int64_t max_pages, int page_size, bool q_bf16, int cache_dtype);

@@ -286,24 +286,29 @@ __device__ __forceinline__ void produce(const TreeParams& p, A& a, B& b) {
   b.drain(p);
 }
 
-// The tensor map of a pool's keys or values: (64 or 128 columns of a 128-byte block, token of
-// the page, block, head, page); boxes as Feed takes them.
-inline bool encode_pages(CUtensorMap* m, const CacheView& c, bool values) {
+// The tensor map of a pool's keys or values: (columns of a 128-byte block, token of the page,
+// block, head, page); boxes of `keys` tokens or a page of fewer, of one column block or all.
+inline bool encode_tokens(CUtensorMap* m, const CacheView& c, const void* data, int keys, bool all_blocks) {
   EncodeTiledFn enc = encode_tiled_fn();
   if (!enc) return false;
-  const bool fp8 = c.dtype == GQA_E4M3;
-  const cuuint64_t es = fp8 ? 1 : 2;
-  const int most = !values ? 7 : fp8 ? 6 : 5, shift = c.page_shift < most ? c.page_shift : most;
-  const cuuint64_t dims[5] = {128 / es, cuuint64_t(1) << c.page_shift, 2 * es, cuuint64_t(c.Hkv), cuuint64_t(c.n_pages)};
+  const cuuint64_t es = c.dtype == GQA_F32 ? 4 : c.dtype == GQA_BF16 ? 2 : 1, page = cuuint64_t(1) << c.page_shift;
+  const cuuint64_t dims[5] = {128 / es, page, 2 * es, cuuint64_t(c.Hkv), cuuint64_t(c.n_pages)};
   // A dimension of one has no stride of its own (views may carry any number there).
   const cuuint64_t strides[4] = {cuuint64_t(c.st) * es, 128, c.Hkv > 1 ? cuuint64_t(c.sh) * es : 16,
                                  c.n_pages > 1 ? cuuint64_t(c.sp) * es : 16};
-  const cuuint32_t box[5] = {cuuint32_t(128 / es), cuuint32_t(1) << shift,
-                             cuuint32_t(values && shift == most ? 2 * es : 1), 1, 1},
+  const cuuint32_t box[5] = {cuuint32_t(128 / es), cuuint32_t(page < cuuint64_t(keys) ? page : keys),
+                             cuuint32_t(all_blocks ? 2 * es : 1), 1, 1},
                    estr[5] = {1, 1, 1, 1, 1};
-  return enc(m, fp8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 5, values ? c.v : c.k, dims,
-             strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+  return enc(m, es == 4 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : es == 2 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
+                                                                   : CU_TENSOR_MAP_DATA_TYPE_UINT8,
+             5, const_cast<void*>(data), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+             CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+// The same as Feed takes them.
+inline bool encode_pages(CUtensorMap* m, const CacheView& c, bool values) {
+  const int most = !values ? 7 : c.dtype == GQA_E4M3 ? 6 : 5;
+  return encode_tokens(m, c, values ? c.v : c.k, 1 << most, values && c.page_shift >= most);
 }
 
 // One 16-byte unit of a value in shared memory: cleared whole, or its elements that are not

@@ -401,3 +401,28 @@ def test_a_decoder_with_the_operators_together(cuda_device, dtype, kind):
     tol = 4e-5 if dtype == F32 else 2e-2
     assert (out2[:, :, 2] - out[:, :, 4]).abs().max() <= tol and (lse2[:, :, 2] - lse[:, :, 4]).abs().max() <= 4e-4
     assert cache.status(pool) == 0
+
+
+@pytest.mark.parametrize("dtype,kind", PAIRS, ids=IDS)
+@pytest.mark.parametrize("bits", [0x7fc00000, -1, 0x7f800001])
+def test_a_visible_nan_reaches_its_rows(cuda_device, dtype, kind, bits):
+    """A NaN of any payload in a key makes the rows that see it NaN and no other; in a value, their column."""
+    p = Problem(cuda_device, 1, 4, 2, 3, [40], 16, dtype, kind, seed=31)
+    clean, _ = p.attend()
+    nan = torch.tensor([bits], dtype=torch.int32).view(F32)
+    for pool, column in ((p.pool.k, None), (p.pool.v, 77)):
+        at = pool[p.table[0, 2], 0, 9]  # token 41, drafted token 1, of key/value head 0
+        kept = at.clone()
+        if kind == F32:
+            at[77] = nan.to(cuda_device)[0]
+        elif kind == BF16:
+            at.view(torch.int16)[77] = {0x7fc00000: 0x7fc0, -1: -1, 0x7f800001: 0x7f81}[bits]
+        else:
+            at.view(torch.int8)[77] = {0x7fc00000: 0x7f, -1: -1, 0x7f800001: 0x7f}[bits]
+        out, _ = p.attend()
+        nans = torch.zeros_like(out, dtype=torch.bool)
+        nans[0, :2, 1:, slice(None) if column is None else column] = True
+        assert torch.equal(out.isnan(), nans)
+        same = ~nans if column is not None else ~nans.any(-1, keepdim=True).expand_as(nans)
+        assert torch.equal(out[same], clean[same])
+        at.copy_(kept)
