@@ -241,20 +241,26 @@ __global__ void __launch_bounds__(RowsCfg<kFp8>::kThreads, 1) tree_rows_kernel(c
         ++segs;
         for (int tile = g.t0; ok && tile < g.t1; ++tile, ++tt) {
           const uint32_t b = tt & 1u, ph = (tt >> 1) & 1u;
-          // O += P(t - 2) V has read what S(t) overwrites; P(t) is there.
-          if (is_s)
-            ok = tt < 2 || mbar_wait_inline(bar(kRBarPV + int(b)), ph ^ 1u, budget, status);
-          else
-            ok = mbar_wait_inline(bar(kRBarP + int(b)), ph, budget, status);
           const uint32_t slots = is_s ? F::kKSlots : F::kVSlots;
           const uint32_t full = bar(is_s ? kRBarKFull : kRBarVFull), empty = bar(is_s ? kRBarKEmpty : kRBarVEmpty);
           const uint32_t sbuf = tmem + 256u + b * 128u;
+          // What has been loaded is waited for first: P, or the last reader of S, comes after it, and
+          // from then on only the products stand between it and the next one.
+#pragma unroll 1
+          for (uint32_t i = 0; ok && i < I::kTile; ++i) {
+            const uint32_t item = I::kTile * tt + i;
+            ok = mbar_wait_inline(full + 8u * (item % slots), (item / slots) & 1u, budget, status);
+          }
+          // O += P(t - 2) V has read what S(t) overwrites; P(t) is there.
+          if (is_s)
+            ok = ok && (tt < 2 || mbar_wait_inline(bar(kRBarPV + int(b)), ph ^ 1u, budget, status));
+          else
+            ok = ok && mbar_wait_inline(bar(kRBarP + int(b)), ph, budget, status);
+          if (!ok) break;
+          umma::fence_after_sync();
 #pragma unroll 1
           for (uint32_t i = 0; i < I::kTile; ++i) {
             const uint32_t item = I::kTile * tt + i, slot = item % slots;
-            ok = ok && mbar_wait_inline(full + 8u * slot, (item / slots) & 1u, budget, status);
-            if (!ok) break;
-            umma::fence_after_sync();
             const uint32_t base = (is_s ? sK : sV) + slot * uint32_t(kSlotBytes);
             if (is_s) {
               // column block i of Q against that of the keys: four steps of 32 bytes
@@ -277,7 +283,7 @@ __global__ void __launch_bounds__(RowsCfg<kFp8>::kThreads, 1) tree_rows_kernel(c
             }
             umma::commit(empty + 8u * slot);
           }
-          if (ok) umma::commit(bar((is_s ? kRBarS : kRBarPV) + int(b)));
+          umma::commit(bar((is_s ? kRBarS : kRBarPV) + int(b)));
         }
       }
       // Every product complete before TMEM is released.

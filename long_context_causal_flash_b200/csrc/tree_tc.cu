@@ -181,19 +181,25 @@ __global__ void __launch_bounds__(Cfg<kN, kFp8>::kThreads, 1) tree_tc_kernel(con
         ++segs;
         for (int tile = g.t0; ok && tile < g.t1; ++tile, ++tt) {
           const uint32_t b = tt & 1u, ph = (tt >> 1) & 1u;
-          // The softmax has read S(t - 2), or written P(t).
-          if (is_s)
-            ok = tt < 2 || mbar_wait_inline(bar(kBarSFree + int(b)), ph ^ 1u, budget, status);
-          else
-            ok = mbar_wait_inline(bar(kBarP + int(b)), ph, budget, status);
           const uint32_t slots = is_s ? F::kKSlots : F::kVSlots;
           const uint32_t full = bar(is_s ? kBarKFull : kBarVFull), empty = bar(is_s ? kBarKEmpty : kBarVEmpty);
+          // What has been loaded is waited for first: P, or the last reader of S, comes after it, and
+          // from then on only the products stand between it and the next one.
+#pragma unroll 1
+          for (uint32_t i = 0; ok && i < I::kTile; ++i) {
+            const uint32_t item = I::kTile * tt + i;
+            ok = mbar_wait_inline(full + 8u * (item % slots), (item / slots) & 1u, budget, status);
+          }
+          // The softmax has read S(t - 2), or written P(t).
+          if (is_s)
+            ok = ok && (tt < 2 || mbar_wait_inline(bar(kBarSFree + int(b)), ph ^ 1u, budget, status));
+          else
+            ok = ok && mbar_wait_inline(bar(kBarP + int(b)), ph, budget, status);
+          if (!ok) break;
+          umma::fence_after_sync();
 #pragma unroll 1
           for (uint32_t i = 0; i < I::kTile; ++i) {
             const uint32_t item = I::kTile * tt + i, slot = item % slots;
-            ok = ok && mbar_wait_inline(full + 8u * slot, (item / slots) & 1u, budget, status);
-            if (!ok) break;
-            umma::fence_after_sync();
             const uint32_t base = (is_s ? sK : sV) + slot * uint32_t(kSlotBytes);
             if (is_s) {
               // column block i of the keys against that of Q: four steps of 32 bytes
@@ -215,7 +221,7 @@ __global__ void __launch_bounds__(Cfg<kN, kFp8>::kThreads, 1) tree_tc_kernel(con
             }
             umma::commit(empty + 8u * slot);
           }
-          if (ok) umma::commit(bar((is_s ? kBarS : kBarPV) + int(b)));
+          umma::commit(bar((is_s ? kBarS : kBarPV) + int(b)));
         }
       }
       // Every product complete before TMEM is released.
