@@ -230,14 +230,15 @@ __global__ void __launch_bounds__(RowsCfg<kFp8>::kThreads, 1) tree_rows_kernel(c
     }
   } else if (warp >= F::kIssuer) {
     // ---------------------------------------------------------------- MMA issuers
-    if (lane == 0) {
+    {
       const bool is_s = warp == F::kIssuer;
       constexpr uint32_t id_s = idesc<kFp8>(128, 0, 0), id_o = idesc<kFp8>(256, 0, 1);
       const uint64_t dq = umma::smem_desc(sQ, 16, 1024);
+      const uint32_t high = uint32_t(dq >> 32);
       uint32_t tt = 0, segs = 0;  // tiles issued
       bool ok = true;
       while (ok && tree_next(p, cur, &g)) {
-        if (is_s && !(ok = mbar_wait_inline(bar(kRBarQ), segs & 1u, budget, status))) break;
+        if (is_s && !(ok = warp_wait(bar(kRBarQ), segs & 1u, budget, status))) break;
         ++segs;
         for (int tile = g.t0; ok && tile < g.t1; ++tile, ++tt) {
           const uint32_t b = tt & 1u, ph = (tt >> 1) & 1u;
@@ -249,49 +250,55 @@ __global__ void __launch_bounds__(RowsCfg<kFp8>::kThreads, 1) tree_rows_kernel(c
 #pragma unroll 1
           for (uint32_t i = 0; ok && i < I::kTile; ++i) {
             const uint32_t item = I::kTile * tt + i;
-            ok = mbar_wait_inline(full + 8u * (item % slots), (item / slots) & 1u, budget, status);
+            ok = warp_wait(full + 8u * (item % slots), (item / slots) & 1u, budget, status);
           }
           // O += P(t - 2) V has read what S(t) overwrites; P(t) is there.
           if (is_s)
-            ok = ok && (tt < 2 || mbar_wait_inline(bar(kRBarPV + int(b)), ph ^ 1u, budget, status));
+            ok = ok && (tt < 2 || warp_wait(bar(kRBarPV + int(b)), ph ^ 1u, budget, status));
           else
-            ok = ok && mbar_wait_inline(bar(kRBarP + int(b)), ph, budget, status);
+            ok = ok && warp_wait(bar(kRBarP + int(b)), ph, budget, status);
           if (!ok) break;
           umma::fence_after_sync();
-#pragma unroll 1
-          for (uint32_t i = 0; i < I::kTile; ++i) {
-            const uint32_t item = I::kTile * tt + i, slot = item % slots;
-            const uint32_t base = (is_s ? sK : sV) + slot * uint32_t(kSlotBytes);
-            if (is_s) {
-              // column block i of Q against that of the keys: four steps of 32 bytes
-              const uint64_t dk = umma::smem_desc(base, 16, 1024);
+          if (elect_lane()) {
 #pragma unroll
-              for (uint32_t k = 0; k < 4; ++k)
+            for (uint32_t i = 0; i < I::kTile; ++i) {
+              const uint32_t item = I::kTile * tt + i, slot = item % slots;
+              const uint32_t base = (is_s ? sK : sV) + slot * uint32_t(kSlotBytes);
+              if (is_s) {
+                // column block i of Q against that of the keys: four steps of 32 bytes
+                const uint64_t dk = umma::smem_desc(base, 16, 1024);
 #pragma unroll
-                for (uint32_t piece = 0; piece < (kFp8 ? 2 : 1); ++piece)
-                  mma<kFp8>(sbuf, umma::desc_add(dq, (i + 2 * piece) * (kRows * 128u) + k * 32u),
-                            umma::desc_add(dk, k * 32u), id_s, (i | k | piece) != 0);
-            } else {
-              // the slot's keys in two steps, all columns of the values
-              const uint64_t dv = umma::smem_desc(base, I::kVBlock, 1024);
+                for (uint32_t k = 0; k < 4; ++k)
 #pragma unroll
-              for (uint32_t k = 0; k < 2; ++k)
+                  for (uint32_t piece = 0; piece < (kFp8 ? 2 : 1); ++piece)
+                    mma<kFp8>(sbuf, desc_low(dq, (i + 2 * piece) * (kRows * 128u) + k * 32u), desc_low(dk, k * 32u), high,
+                              id_s, (i | k | piece) != 0);
+              } else {
+                // the slot's keys in two steps, all columns of the values
+                const uint64_t dv = umma::smem_desc(base, I::kVBlock, 1024);
 #pragma unroll
-                for (uint32_t piece = 0; piece < (kFp8 ? 2 : 1); ++piece)
-                  mma_ts<kFp8>(tmem, sbuf + 32u * piece + 8u * (2 * i + k), umma::desc_add(dv, k * I::kStep), id_o,
-                               tile > g.t0 || (i | k | piece) != 0);
+                for (uint32_t k = 0; k < 2; ++k)
+#pragma unroll
+                  for (uint32_t piece = 0; piece < (kFp8 ? 2 : 1); ++piece)
+                    mma_ts<kFp8>(tmem, sbuf + 32u * piece + 8u * (2 * i + k), desc_low(dv, k * I::kStep), high, id_o,
+                                 tile > g.t0 || (i | k | piece) != 0);
+              }
+              umma::commit(empty + 8u * slot);
             }
-            umma::commit(empty + 8u * slot);
+            umma::commit(bar((is_s ? kRBarS : kRBarPV) + int(b)));
           }
-          umma::commit(bar((is_s ? kRBarS : kRBarPV) + int(b)));
+          __syncwarp();
         }
       }
       // Every product complete before TMEM is released.
-      if (tt > 0)
-        umma::commit(bar(kRBarDrain));
-      else
-        mbar_arrive(bar(kRBarDrain));
-      mbar_wait_inline(bar(kRBarDrain), 0, budget, status);
+      if (elect_lane()) {
+        if (tt > 0)
+          umma::commit(bar(kRBarDrain));
+        else
+          mbar_arrive(bar(kRBarDrain));
+      }
+      __syncwarp();
+      warp_wait(bar(kRBarDrain), 0, budget, status);
     }
     __syncwarp();
   } else {

@@ -170,14 +170,15 @@ __global__ void __launch_bounds__(Cfg<kN, kFp8>::kThreads, 1) tree_tc_kernel(con
     // ---------------------------------------------------------------- MMA issuers
     // One thread issues every S^T = K Q^T, another every O^T += V^T P^T, so that neither
     // waits for the other's tiles to arrive.
-    if (lane == 0) {
+    {
       const bool is_s = warp == F::kIssuer;
       constexpr uint32_t id_s = idesc<kFp8>(F::kNN, 0, 0), id_o = idesc<kFp8>(F::kNN, 1, 1);
       const uint64_t dq = umma::smem_desc(sQ, 16, 1024), dp = umma::smem_desc(sP, 16384, 1024);
+      const uint32_t high = uint32_t(dq >> 32);
       uint32_t tt = 0, segs = 0;  // tiles issued
       bool ok = true;
       while (ok && tree_next(p, cur, &g)) {
-        if (is_s && !(ok = mbar_wait_inline(bar(kBarQ), segs & 1u, budget, status))) break;
+        if (is_s && !(ok = warp_wait(bar(kBarQ), segs & 1u, budget, status))) break;
         ++segs;
         for (int tile = g.t0; ok && tile < g.t1; ++tile, ++tt) {
           const uint32_t b = tt & 1u, ph = (tt >> 1) & 1u;
@@ -188,48 +189,54 @@ __global__ void __launch_bounds__(Cfg<kN, kFp8>::kThreads, 1) tree_tc_kernel(con
 #pragma unroll 1
           for (uint32_t i = 0; ok && i < I::kTile; ++i) {
             const uint32_t item = I::kTile * tt + i;
-            ok = mbar_wait_inline(full + 8u * (item % slots), (item / slots) & 1u, budget, status);
+            ok = warp_wait(full + 8u * (item % slots), (item / slots) & 1u, budget, status);
           }
           // The softmax has read S(t - 2), or written P(t).
           if (is_s)
-            ok = ok && (tt < 2 || mbar_wait_inline(bar(kBarSFree + int(b)), ph ^ 1u, budget, status));
+            ok = ok && (tt < 2 || warp_wait(bar(kBarSFree + int(b)), ph ^ 1u, budget, status));
           else
-            ok = ok && mbar_wait_inline(bar(kBarP + int(b)), ph, budget, status);
+            ok = ok && warp_wait(bar(kBarP + int(b)), ph, budget, status);
           if (!ok) break;
           umma::fence_after_sync();
-#pragma unroll 1
-          for (uint32_t i = 0; i < I::kTile; ++i) {
-            const uint32_t item = I::kTile * tt + i, slot = item % slots;
-            const uint32_t base = (is_s ? sK : sV) + slot * uint32_t(kSlotBytes);
-            if (is_s) {
-              // column block i of the keys against that of Q: four steps of 32 bytes
-              const uint64_t dk = umma::smem_desc(base, 16, 1024);
+          if (elect_lane()) {
 #pragma unroll
-              for (uint32_t k = 0; k < 4; ++k)
-                mma<kFp8>(tmem + b * F::kNN, umma::desc_add(dk, k * 32u), umma::desc_add(dq, i * (F::kNN * 128u) + k * 32u),
-                          id_s, (i | k) != 0);
-            } else {
-              // the slot's keys, in two steps, for both halves of the values' columns
+            for (uint32_t i = 0; i < I::kTile; ++i) {
+              const uint32_t item = I::kTile * tt + i, slot = item % slots;
+              const uint32_t base = (is_s ? sK : sV) + slot * uint32_t(kSlotBytes);
+              if (is_s) {
+                // column block i of the keys against that of Q: four steps of 32 bytes
+                const uint64_t dk = umma::smem_desc(base, 16, 1024);
 #pragma unroll
-              for (uint32_t half = 0; half < 2; ++half) {
-                const uint64_t dv = umma::smem_desc(base + half * (kSlotBytes / 2), I::kVBlock, 1024);
+                for (uint32_t k = 0; k < 4; ++k)
+                  mma<kFp8>(tmem + b * F::kNN, desc_low(dk, k * 32u), desc_low(dq, i * (F::kNN * 128u) + k * 32u), high, id_s,
+                            (i | k) != 0);
+              } else {
+                // the slot's keys, in two steps, for both halves of the values' columns
 #pragma unroll
-                for (uint32_t k = 0; k < 2; ++k)
-                  mma<kFp8>(tmem + (2 + half) * F::kNN, umma::desc_add(dv, k * I::kStep),
-                            umma::desc_add(dp, (2 * i + k) * I::kStep), id_o, tile > g.t0 || (i | k) != 0);
+                for (uint32_t half = 0; half < 2; ++half) {
+                  const uint64_t dv = umma::smem_desc(base + half * (kSlotBytes / 2), I::kVBlock, 1024);
+#pragma unroll
+                  for (uint32_t k = 0; k < 2; ++k)
+                    mma<kFp8>(tmem + (2 + half) * F::kNN, desc_low(dv, k * I::kStep), desc_low(dp, (2 * i + k) * I::kStep),
+                              high, id_o, tile > g.t0 || (i | k) != 0);
+                }
               }
+              umma::commit(empty + 8u * slot);
             }
-            umma::commit(empty + 8u * slot);
+            umma::commit(bar((is_s ? kBarS : kBarPV) + int(b)));
           }
-          umma::commit(bar((is_s ? kBarS : kBarPV) + int(b)));
+          __syncwarp();
         }
       }
       // Every product complete before TMEM is released.
-      if (tt > 0)
-        umma::commit(bar(kBarDrain));
-      else
-        mbar_arrive(bar(kBarDrain));
-      mbar_wait_inline(bar(kBarDrain), 0, budget, status);
+      if (elect_lane()) {
+        if (tt > 0)
+          umma::commit(bar(kBarDrain));
+        else
+          mbar_arrive(bar(kBarDrain));
+      }
+      __syncwarp();
+      warp_wait(bar(kBarDrain), 0, budget, status);
     }
     __syncwarp();
   } else {

@@ -66,30 +66,52 @@ __device__ __forceinline__ uint4 lds16(uint32_t a) {
   return v;
 }
 
+// One lane of a whole warp, always the same.  The products are issued under this predicate: the
+// compiler then keeps their operands in uniform registers, where under `lane == 0` it moves
+// every word of them there first.  With softmax warps that fill the scheduler an issue takes 75
+// cycles, under `lane == 0` 230 (and the product itself 65 - 130).
+__device__ __forceinline__ bool elect_lane() {
+  uint32_t ok;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(ok));
+  return ok != 0;
+}
+
+// Shared-memory descriptors by their low words: the high words, of strides and layout, are the
+// same for all operands of a kernel but for the stride between column blocks in the low ones.
+__device__ __forceinline__ uint32_t desc_low(uint64_t d, uint32_t bytes) { return uint32_t(d) + (bytes >> 4); }
+
 // D[tmem] (+)= A[smem] B[smem]^T in the type of the pages.
 template <bool kFp8>
-__device__ __forceinline__ void mma(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool add) {
+__device__ __forceinline__ void mma(uint32_t d, uint32_t a, uint32_t b, uint32_t high, uint32_t idesc, bool add) {
   if constexpr (kFp8)
     asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "setp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}\n" ::"r"(d),
-        "l"(a), "l"(b), "r"(idesc), "r"(uint32_t(add)));
+        "{\n\t.reg .pred p;\n\t.reg .b64 a, b;\n\tmov.b64 a, {%1, %3};\n\tmov.b64 b, {%2, %3};\n\t"
+        "setp.ne.b32 p, %5, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], a, b, %4, p;\n\t}\n" ::"r"(d),
+        "r"(a), "r"(b), "r"(high), "r"(idesc), "r"(uint32_t(add)));
   else
-    umma::mma_ss(d, a, b, idesc, add);
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t.reg .b64 a, b;\n\tmov.b64 a, {%1, %3};\n\tmov.b64 b, {%2, %3};\n\t"
+        "setp.ne.b32 p, %5, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %4, p;\n\t}\n" ::"r"(d),
+        "r"(a), "r"(b), "r"(high), "r"(idesc), "r"(uint32_t(add)));
 }
 
 // The same with A in TMEM: row m in lane m, a step's 32 bytes in eight columns.
 template <bool kFp8>
-__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, bool add) {
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint32_t b, uint32_t high, uint32_t idesc, bool add) {
   if constexpr (kFp8)
     asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "setp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], [%1], %2, %3, p;\n\t}\n" ::"r"(d),
-        "r"(a), "l"(b), "r"(idesc), "r"(uint32_t(add)));
+        "{\n\t.reg .pred p;\n\t.reg .b64 b;\n\tmov.b64 b, {%2, %3};\n\t"
+        "setp.ne.b32 p, %5, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], [%1], b, %4, p;\n\t}\n" ::"r"(d),
+        "r"(a), "r"(b), "r"(high), "r"(idesc), "r"(uint32_t(add)));
   else
-    umma::mma_ts(d, a, b, idesc, add);
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t.reg .b64 b;\n\tmov.b64 b, {%2, %3};\n\t"
+        "setp.ne.b32 p, %5, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], b, %4, p;\n\t}\n" ::"r"(d),
+        "r"(a), "r"(b), "r"(high), "r"(idesc), "r"(uint32_t(add)));
 }
 
 // Instruction descriptor: fp32 accumulator, M = 128; e4m3 is format 0 of kind::f8f6f4, bf16
