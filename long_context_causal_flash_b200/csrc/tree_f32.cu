@@ -562,7 +562,8 @@ int launch_one(const TreeParams& p, cudaStream_t stream) {
   constexpr int smem = F32Cfg<NT, kCache, QT>::kSmem;
   if (!allow_smem<tree_f32_kernel<NT, kCache, QT>>(smem)) return GQA_ERR_LAUNCH;
   CUtensorMap map_k, map_v;
-  if (!encode_tokens(&map_k, p.c, p.c.k, kChunk, true) || !encode_tokens(&map_v, p.c, p.c.v, kChunk, true))
+  constexpr int blocks = 2 * F32Cfg<NT, kCache, QT>::kEs;
+  if (!encode_tokens(&map_k, p.c, p.c.k, kChunk, blocks, blocks) || !encode_tokens(&map_v, p.c, p.c.v, kChunk, blocks, blocks))
     return GQA_ERR_LAUNCH;
   tree_f32_kernel<NT, kCache, QT><<<unsigned(p.workers) * unsigned(p.row_tiles), kThreads, smem, stream>>>(p, map_k,
                                                                                                          map_v);

@@ -30,7 +30,7 @@ struct RowsCfg {
   static constexpr int kOffK = kRows * 512;
   static constexpr int kOffV = kOffK + kKSlots * kSlotBytes;
   static constexpr int kOffBar = kOffV + kVSlots * kSlotBytes;
-  static constexpr int kOffStart = kOffBar + 8 * 32;  // the worker's cursor, the TMEM address
+  static constexpr int kOffStart = kOffBar + 8 * 34;  // the worker's cursor, the TMEM address
   static constexpr int kOffBad = kOffStart + 48;      // 32 words: drafted tokens with a value that is not finite
   static constexpr int kOffThere = kOffBad + 128;     // [2][4] words: which keys of the tile are there
   static constexpr int kOffRed = kOffThere + 32;      // [4 parts][128 rows] exchange
@@ -52,7 +52,8 @@ enum {
   kRBarKFull = 10,
   kRBarKEmpty = 15,
   kRBarVFull = 20,
-  kRBarVEmpty = 25
+  kRBarVEmpty = 25,
+  kRBarRelay = 30  // to the odd CTA of a pair, per part: its values are there
 };
 
 // Eight consecutive 32-bit columns of raw words into this thread's TMEM lane.
@@ -62,7 +63,30 @@ __device__ __forceinline__ void tmem_st8u(uint32_t taddr, const uint32_t (&r)[8]
                : "memory");
 }
 
-template <bool kFp8>
+// The pair's products, issued by the even CTA: A's rows 0 .. 127 are its own, 128 .. 255 the odd
+// one's; B's N lies half in one, half in the other.
+__device__ __forceinline__ void mma_pair(uint32_t d, uint32_t a, uint32_t b, uint32_t high, uint32_t idesc, bool add) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t.reg .b64 a, b;\n\tmov.b64 a, {%1, %3};\n\tmov.b64 b, {%2, %3};\n\t"
+      "setp.ne.b32 p, %5, 0;\n\t"
+      "tcgen05.mma.cta_group::2.kind::f16 [%0], a, b, %4, p;\n\t}\n" ::"r"(d),
+      "r"(a), "r"(b), "r"(high), "r"(idesc), "r"(uint32_t(add)));
+}
+__device__ __forceinline__ void mma_ts_pair(uint32_t d, uint32_t a, uint32_t b, uint32_t high, uint32_t idesc, bool add) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t.reg .b64 b;\n\tmov.b64 b, {%2, %3};\n\t"
+      "setp.ne.b32 p, %5, 0;\n\t"
+      "tcgen05.mma.cta_group::2.kind::f16 [%0], [%1], b, %4, p;\n\t}\n" ::"r"(d),
+      "r"(a), "r"(b), "r"(high), "r"(idesc), "r"(uint32_t(add)));
+}
+
+// An arrival in the other CTA (or this one) that publishes shared memory, not only tensor memory.
+__device__ __forceinline__ void arrive_release_cluster(uint32_t cluster_addr) {
+  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
+}
+__device__ __forceinline__ void fence_cluster() { asm volatile("fence.acq_rel.cluster;" ::: "memory"); }
+
+template <bool kFp8, bool kPair>
 __global__ void __launch_bounds__(RowsCfg<kFp8>::kThreads, 1) tree_rows_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v,
                  const __grid_constant__ TreeParams p) {
   using F = RowsCfg<kFp8>;
@@ -80,20 +104,29 @@ __global__ void __launch_bounds__(RowsCfg<kFp8>::kThreads, 1) tree_rows_kernel(c
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int worker = blockIdx.x / p.row_tiles, rt = blockIdx.x % p.row_tiles;
   const int64_t budget = p.wait_budget_ns;
+  static_assert(!kPair || !kFp8);
+  constexpr int kTile = kPair ? 2 : I::kTile;      // items of a tile's keys, and of its values
+  constexpr int kVKeys = 128 / kTile;              // keys of a value item
+  constexpr uint32_t kVBlock = kVKeys * 128u;      // bytes from one of its column blocks to the next
+  constexpr int kUnits = kFp8 || kPair ? 16 : 32;  // 16-byte units of a key's values here
+  const uint32_t rank = kPair ? cluster_ctarank() : 0;  // 0: the even CTA, which issues the products
+  const uint32_t lead_bar = kPair ? mapa_shared(sbase + F::kOffBar, 0) : 0;
+  auto lead = [&](int i) { return lead_bar + 8u * uint32_t(i); };
   int32_t* status = p.c.status;
 
   if (warp == 0) {
     const TreeCursor c = tree_start(p, worker);
     if (lane == 0) {
       start = c;
-      mbar_init(bar(kRBarQ), kSoftWarps);
+      mbar_init(bar(kRBarQ), kPair ? 2 * kSoftWarps : kSoftWarps);
       for (int i = 0; i < 2; ++i) {
         mbar_init(bar(kRBarS + i), 1);
-        mbar_init(bar(kRBarP + i), kSoftWarps);
+        mbar_init(bar(kRBarP + i), kPair ? 2 * kSoftWarps : kSoftWarps);
         mbar_init(bar(kRBarPV + i), 1);
         mbar_init(bar(kRBarKeys + i), 1);
       }
       mbar_init(bar(kRBarDrain), 2);
+      for (int i = 0; i < 4; ++i) mbar_init(bar(kRBarRelay + i), 1);
       for (int i = 0; i < F::kKSlots; ++i) {
         mbar_init(bar(kRBarKFull + i), 1);
         mbar_init(bar(kRBarKEmpty + i), 1);
@@ -106,9 +139,17 @@ __global__ void __launch_bounds__(RowsCfg<kFp8>::kThreads, 1) tree_rows_kernel(c
       if (misaligned) set_status(status, GQA_ERR_LAUNCH);
     }
   }
-  if (warp == F::kIssuer) umma::tmem_alloc(sbase + F::kOffStart + 40, 512);
+  if (warp == F::kIssuer) {
+    if constexpr (kPair)
+      umma::tmem_alloc_2sm(sbase + F::kOffStart + 40, 512);
+    else
+      umma::tmem_alloc(sbase + F::kOffStart + 40, 512);
+  }
   umma::fence_before_sync();
-  __syncthreads();
+  if constexpr (kPair)
+    cluster_sync();
+  else
+    __syncthreads();
   umma::fence_after_sync();
   const uint32_t tmem = tmem_slot;
   launch_dependents();
@@ -118,7 +159,8 @@ __global__ void __launch_bounds__(RowsCfg<kFp8>::kThreads, 1) tree_rows_kernel(c
   if (misaligned) {
     // no role
   } else if (warp == kSoftWarps) {
-    Feed<kFp8, false, F::kKSlots> k;
+    Feed<kFp8, false, F::kKSlots, kPair> k;
+    k.rank = int(rank);
     k.begin(p, cur, &map_k, sK, bar(kRBarKFull), bar(kRBarKEmpty));
     if constexpr (kFp8) {
       Feed<kFp8, true, F::kVSlots> v;
@@ -130,8 +172,9 @@ __global__ void __launch_bounds__(RowsCfg<kFp8>::kThreads, 1) tree_rows_kernel(c
       produce(p, k, none);
     }
   } else if (!kFp8 && warp == kSoftWarps + 1) {
-    Feed<kFp8, true, F::kVSlots> v;
+    Feed<kFp8, true, F::kVSlots, kPair> v;
     NoFeed none;
+    v.rank = int(rank);
     v.begin(p, cur, &map_v, sV, bar(kRBarVFull), bar(kRBarVEmpty));
     produce(p, v, none);
   } else if (warp == kSoftWarps + 1) {
@@ -230,15 +273,18 @@ __global__ void __launch_bounds__(RowsCfg<kFp8>::kThreads, 1) tree_rows_kernel(c
     }
   } else if (warp >= F::kIssuer) {
     // ---------------------------------------------------------------- MMA issuers
-    {
+    // (of a pair, the even CTA's)
+    if (!kPair || rank == 0) {
       const bool is_s = warp == F::kIssuer;
-      constexpr uint32_t id_s = idesc<kFp8>(128, 0, 0), id_o = idesc<kFp8>(256, 0, 1);
+      constexpr uint32_t kM = kPair ? 8u << 24 : 0;  // M = 256 instead of 128
+      constexpr uint32_t id_s = idesc<kFp8>(128, 0, 0) + kM, id_o = idesc<kFp8>(256, 0, 1) + kM;
       const uint64_t dq = umma::smem_desc(sQ, 16, 1024);
       const uint32_t high = uint32_t(dq >> 32);
       uint32_t tt = 0, segs = 0;  // tiles issued
       bool ok = true;
       while (ok && tree_next(p, cur, &g)) {
         if (is_s && !(ok = warp_wait(bar(kRBarQ), segs & 1u, budget, status))) break;
+        if constexpr (kPair) fence_cluster();  // the odd CTA's Q is behind that word
         ++segs;
         for (int tile = g.t0; ok && tile < g.t1; ++tile, ++tt) {
           const uint32_t b = tt & 1u, ph = (tt >> 1) & 1u;
@@ -248,8 +294,8 @@ __global__ void __launch_bounds__(RowsCfg<kFp8>::kThreads, 1) tree_rows_kernel(c
           // What has been loaded is waited for first: P, or the last reader of S, comes after it, and
           // from then on only the products stand between it and the next one.
 #pragma unroll 1
-          for (uint32_t i = 0; ok && i < I::kTile; ++i) {
-            const uint32_t item = I::kTile * tt + i;
+          for (uint32_t i = 0; ok && i < kTile; ++i) {
+            const uint32_t item = kTile * tt + i;
             ok = warp_wait(full + 8u * (item % slots), (item / slots) & 1u, budget, status);
           }
           // O += P(t - 2) V has read what S(t) overwrites; P(t) is there.
@@ -261,9 +307,27 @@ __global__ void __launch_bounds__(RowsCfg<kFp8>::kThreads, 1) tree_rows_kernel(c
           umma::fence_after_sync();
           if (elect_lane()) {
 #pragma unroll
-            for (uint32_t i = 0; i < I::kTile; ++i) {
-              const uint32_t item = I::kTile * tt + i, slot = item % slots;
+            for (uint32_t i = 0; i < kTile; ++i) {
+              const uint32_t item = kTile * tt + i, slot = item % slots;
               const uint32_t base = (is_s ? sK : sV) + slot * uint32_t(kSlotBytes);
+              if constexpr (kPair) {
+                // two column blocks of Q against those of the keys, or four steps of 16 values
+                if (is_s) {
+                  const uint64_t dk = umma::smem_desc(base, 16, 1024);
+#pragma unroll
+                  for (uint32_t k = 0; k < 8; ++k)
+                    mma_pair(sbuf, desc_low(dq, (2 * i + k / 4) * (kRows * 128u) + k % 4 * 32u),
+                             desc_low(dk, k / 4 * 8192u + k % 4 * 32u), high, id_s, (i | k) != 0);
+                } else {
+                  const uint64_t dv = umma::smem_desc(base, kVBlock, 1024);
+#pragma unroll
+                  for (uint32_t k = 0; k < 4; ++k)
+                    mma_ts_pair(tmem, sbuf + 8u * (4 * i + k), desc_low(dv, k * I::kStep), high, id_o,
+                                tile > g.t0 || (i | k) != 0);
+                }
+                umma::commit_2sm_mc(empty + 8u * slot, 3);
+                continue;
+              }
               if (is_s) {
                 // column block i of Q against that of the keys: four steps of 32 bytes
                 const uint64_t dk = umma::smem_desc(base, 16, 1024);
@@ -275,7 +339,7 @@ __global__ void __launch_bounds__(RowsCfg<kFp8>::kThreads, 1) tree_rows_kernel(c
                               id_s, (i | k | piece) != 0);
               } else {
                 // the slot's keys in two steps, all columns of the values
-                const uint64_t dv = umma::smem_desc(base, I::kVBlock, 1024);
+                const uint64_t dv = umma::smem_desc(base, kVBlock, 1024);
 #pragma unroll
                 for (uint32_t k = 0; k < 2; ++k)
 #pragma unroll
@@ -285,17 +349,23 @@ __global__ void __launch_bounds__(RowsCfg<kFp8>::kThreads, 1) tree_rows_kernel(c
               }
               umma::commit(empty + 8u * slot);
             }
-            umma::commit(bar((is_s ? kRBarS : kRBarPV) + int(b)));
+            const uint32_t done = bar((is_s ? kRBarS : kRBarPV) + int(b));
+            if constexpr (kPair)
+              umma::commit_2sm_mc(done, 3);
+            else
+              umma::commit(done);
           }
           __syncwarp();
         }
       }
       // Every product complete before TMEM is released.
       if (elect_lane()) {
-        if (tt > 0)
-          umma::commit(bar(kRBarDrain));
-        else
+        if (tt == 0)
           mbar_arrive(bar(kRBarDrain));
+        else if constexpr (kPair)
+          umma::commit_2sm(bar(kRBarDrain));
+        else
+          umma::commit(bar(kRBarDrain));
       }
       __syncwarp();
       warp_wait(bar(kRBarDrain), 0, budget, status);
@@ -316,7 +386,8 @@ __global__ void __launch_bounds__(RowsCfg<kFp8>::kThreads, 1) tree_rows_kernel(c
     // One value per part and row.
     float* sh_red = reinterpret_cast<float*>(smem_raw + F::kOffRed);
     auto red = [&](int q) -> float& { return sh_red[q * kRows + r]; };
-    uint32_t tt = 0;
+    uint32_t tt = 0, relays = 0;  // tiles so far; values told of by the even CTA
+    (void)relays;
     bool ok = true;
 
     while (ok && tree_next(p, cur, &g)) {
@@ -347,7 +418,12 @@ __global__ void __launch_bounds__(RowsCfg<kFp8>::kThreads, 1) tree_rows_kernel(c
       if (warp == 0) sh_bad[lane] = 0;
       fence_proxy_async_smem();
       __syncwarp();
-      if (lane == 0) mbar_arrive(bar(kRBarQ));
+      if (lane == 0) {
+        if constexpr (kPair)
+          arrive_release_cluster(lead(kRBarQ));
+        else
+          mbar_arrive(bar(kRBarQ));
+      }
       sync_threads(15, kAll);  // sh_f and sh_bad are other warps' too
       const float factor = kFp8 ? sh_f[r] : p.scale_log2;
       const bool live = t < g.s.drafted;
@@ -366,19 +442,36 @@ __global__ void __launch_bounds__(RowsCfg<kFp8>::kThreads, 1) tree_rows_kernel(c
         bool fine = ok;
         // The values of keys 32 part .. + 31 are in their slot.  The product of the tile before is over
         // first, so that the barrier stands at no earlier use of the slot.
-        const uint32_t v_item = I::kTile * tt + uint32_t(part * 32 / I::kVKeys);
+        const uint32_t v_item = kTile * tt + uint32_t(part * 32 / kVKeys);
         auto values_there = [&]() {
           if (tt > 0 && !warp_wait(bar(kRBarPV + int((tt - 1) & 1u)), ((tt - 1) >> 1) & 1u, budget, status)) return false;
-          return warp_wait(bar(kRBarVFull + int(v_item % F::kVSlots)), (v_item / F::kVSlots) & 1u, budget, status);
+          if (!kPair || rank == 0) {
+            if (!warp_wait(bar(kRBarVFull + int(v_item % F::kVSlots)), (v_item / F::kVSlots) & 1u, budget, status)) return false;
+            // The odd CTA's values are counted here too: its warp of the same part waits for the word.
+            if (kPair && lane == 0) arrive_release_cluster(mapa_shared(bar(kRBarRelay + part), 1));
+            return true;
+          }
+          const bool there = warp_wait(bar(kRBarRelay + part), relays & 1u, budget, status);
+          fence_cluster();
+          ++relays;
+          return there;
         };
         auto value_unit = [&](int c) {  // 16-byte unit c of this thread's key's values, in any order
-          return sV + (v_item % F::kVSlots) * uint32_t(kSlotBytes) + uint32_t(c >> 3) * I::kVBlock +
-                 uint32_t(key % I::kVKeys) * 128u + uint32_t(((c ^ key) & 7) << 4);
+          return sV + (v_item % F::kVSlots) * uint32_t(kSlotBytes) + uint32_t(c >> 3) * kVBlock +
+                 uint32_t(key % kVKeys) * 128u + uint32_t(((c ^ key) & 7) << 4);
+        };
+        auto give_p = [&](bool cleared) {  // one lane
+          if constexpr (!kPair)
+            mbar_arrive(bar(kRBarP + int(sb)));
+          else if (cleared)
+            arrive_release_cluster(lead(kRBarP + int(sb)));
+          else
+            mbar_arrive_remote(lead(kRBarP + int(sb)));
         };
         if (idle) {  // its rows of S and O are nobody's; the tiles are counted
           ok = warp_wait(bar(kRBarS + int(sb)), ph, budget, status);
           if (!ok) break;
-          if (lane == 0) mbar_arrive(bar(kRBarP + int(sb)));
+          if (lane == 0) give_p(false);
           continue;
         }
         // Which of the 32 keys are there, and which this row sees.
@@ -400,22 +493,30 @@ __global__ void __launch_bounds__(RowsCfg<kFp8>::kThreads, 1) tree_rows_kernel(c
             if (j0 + i >= g.s.ctx && ((vis >> i) & 1u) && !tree_sees(p, g.b, t, int(j0 + i - g.s.ctx))) vis &= ~(1u << i);
         }
         const bool masked = __any_sync(0xffffffffu, vis != 0xffffffffu);
+        fine = warp_wait(bar(kRBarS + int(sb)), ph, budget, status) && fine;
+        umma::fence_after_sync();
         // Values that take no part, as in tree_tc.cu.  Quarter 0's warps look after the 128 keys.
+        // (After S: both CTAs of a pair have then begun this segment.)
         const bool gone = !((there >> lane) & 1u), drafted = !gone && p.T > 1 && j0 + lane >= g.s.ctx;
-        if (quarter == 0 && __any_sync(0xffffffffu, gone || drafted)) {
+        const bool cleared = quarter == 0 && __any_sync(0xffffffffu, gone || drafted);
+        if (cleared) {
           fine = values_there() && fine;
           if (fine && (gone || drafted)) {
             uint32_t bad = 0;
 #pragma unroll 1
-            for (int c = 0; c < (kFp8 ? 16 : 32); ++c) bad |= mend_unit<kFp8>(value_unit(c), gone);
+            for (int c = 0; c < kUnits; ++c) bad |= mend_unit<kFp8>(value_unit(c), gone);
             const int u = int(j0 + lane - g.s.ctx);
-            if (bad) atomicOr(&sh_bad[u >> 5], 1u << (u & 31));
+            if (bad) {
+              atomicOr(&sh_bad[u >> 5], 1u << (u & 31));
+              if constexpr (kPair) {  // each has half of the columns
+                const uint32_t to = mapa_shared(smem_u32(&sh_bad[u >> 5]), rank ^ 1u);
+                asm volatile("red.relaxed.cluster.shared::cluster.or.b32 [%0], %1;" ::"r"(to), "r"(1u << (u & 31)) : "memory");
+              }
+            }
           }
           fence_proxy_async_smem();
           __syncwarp();
         }
-        fine = warp_wait(bar(kRBarS + int(sb)), ph, budget, status) && fine;
-        umma::fence_after_sync();
         float x[32];
         umma::tmem_ld32(lane_addr + 256u + sb * 128u + uint32_t(part * 32), x);
         umma::tmem_wait_ld();
@@ -509,7 +610,7 @@ __global__ void __launch_bounds__(RowsCfg<kFp8>::kThreads, 1) tree_rows_kernel(c
         umma::tmem_wait_st();
         umma::fence_before_sync();
         __syncwarp();
-        if (lane == 0 && ok) mbar_arrive(bar(kRBarP + int(sb)));
+        if (lane == 0 && ok) give_p(cleared);
       }
       // ------------------------------------------------------------ the segment's result
       const uint32_t last = tt - 1;
@@ -561,27 +662,48 @@ __global__ void __launch_bounds__(RowsCfg<kFp8>::kThreads, 1) tree_rows_kernel(c
     }
   }
   umma::fence_before_sync();
-  __syncthreads();
+  if constexpr (kPair)  // neither leaves while products or copies may touch its memory
+    cluster_sync();
+  else
+    __syncthreads();
   if (warp == F::kIssuer) {
     umma::fence_after_sync();
-    umma::tmem_dealloc(tmem, 512);
+    if constexpr (kPair)
+      umma::tmem_dealloc_2sm(tmem, 512);
+    else
+      umma::tmem_dealloc(tmem, 512);
   }
 }
 
-template <bool kFp8>
-int launch(const TreeParams& p, cudaStream_t stream) {
+template <bool kFp8, bool kPair>
+int launch(const TreeParams& p, const CUtensorMap& mk, const CUtensorMap& mv, cudaStream_t stream) {
   using F = RowsCfg<kFp8>;
-  CUtensorMap mk, mv;
-  if (!encode_pages(&mk, p.c, false) || !encode_pages(&mv, p.c, true)) return GQA_ERR_LAUNCH;
-  if (!allow_smem<tree_rows_kernel<kFp8>>(F::kSmem)) return GQA_ERR_LAUNCH;
-  tree_rows_kernel<kFp8><<<unsigned(p.workers) * unsigned(p.row_tiles), F::kThreads, F::kSmem, stream>>>(mk, mv, p);
-  return cudaGetLastError() == cudaSuccess ? GQA_OK : GQA_ERR_LAUNCH;
+  if (!allow_smem<tree_rows_kernel<kFp8, kPair>>(F::kSmem)) return GQA_ERR_LAUNCH;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(unsigned(p.workers) * unsigned(p.row_tiles));
+  cfg.blockDim = dim3(F::kThreads);
+  cfg.dynamicSmemBytes = F::kSmem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = 2;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = kPair ? 1 : 0;
+  return cudaLaunchKernelEx(&cfg, tree_rows_kernel<kFp8, kPair>, mk, mv, p) == cudaSuccess ? GQA_OK : GQA_ERR_LAUNCH;
 }
 
 }  // namespace
 
 int launch_tree_rows(const TreeParams& p, cudaStream_t stream) {
-  return p.c.dtype == GQA_E4M3 ? launch<true>(p, stream) : launch<false>(p, stream);
+  CUtensorMap mk, mv;
+  if (p.c.dtype == GQA_BF16 && p.row_tiles % 2 == 0) {
+    if (!encode_tokens(&mk, p.c, p.c.k, 64, 2, 1) || !encode_tokens(&mv, p.c, p.c.v, 64, 2, 1)) return GQA_ERR_LAUNCH;
+    return launch<false, true>(p, mk, mv, stream);
+  }
+  if (!encode_pages(&mk, p.c, false) || !encode_pages(&mv, p.c, true)) return GQA_ERR_LAUNCH;
+  return p.c.dtype == GQA_E4M3 ? launch<true, false>(p, mk, mv, stream) : launch<false, false>(p, mk, mv, stream);
 }
 
 }  // namespace gqa

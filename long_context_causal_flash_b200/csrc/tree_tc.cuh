@@ -152,6 +152,16 @@ __device__ __forceinline__ void tma_load_5d(uint32_t dst, const CUtensorMap* map
       : "memory");
 }
 
+// The same, counted on a barrier of either CTA of the pair (a shared::cluster address).
+__device__ __forceinline__ void tma_load_5d_pair(uint32_t dst, const CUtensorMap* map, uint32_t bar, int c0, int c1,
+                                                 int c2, int c3, int c4) {
+  asm volatile(
+      "cp.async.bulk.tensor.5d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%3, %4, %5, %6, %7}], [%2];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(c0), "r"(c1), "r"(c2), "r"(c3), "r"(c4)
+      : "memory");
+}
+
 // mbarrier phase `parity` is over; does not wait.
 __device__ __forceinline__ bool mbar_test(uint32_t bar, uint32_t parity) {
   uint32_t ok;
@@ -177,15 +187,21 @@ __device__ __forceinline__ bool mbar_test(uint32_t bar, uint32_t parity) {
 // Whole boxes are loaded: rows of a page past the last key hold what the page holds, pages
 // that are not there leave the slot as it was.  The softmax warps hide those keys' scores
 // and clear their values.
-template <bool kFp8, bool kIsV, int kSlots>
+// A CTA of a pair loads its half of a tile, 64 keys or half of the values' columns, in items
+// of 64 keys and two column blocks; the even CTA's barriers count both halves' bytes.
+template <bool kFp8, bool kIsV, int kSlots, bool kPair = false>
 struct Feed {
   using I = Items<kFp8>;
-  static constexpr int kKeys = kIsV ? I::kVKeys : 128, kBlocks = kIsV ? (kFp8 ? 2 : 4) : 1;
-  static constexpr int kMostShift = kIsV ? (kFp8 ? 6 : 5) : 7;  // log2 kKeys
+  static constexpr int kKeys = kPair ? 64 : kIsV ? I::kVKeys : 128;
+  static constexpr int kBlocks = kPair ? 2 : kIsV ? (kFp8 ? 2 : 4) : 1;
+  static constexpr int kMostShift = kPair ? 6 : kIsV ? (kFp8 ? 6 : 5) : 7;  // log2 kKeys
+  static constexpr int kTile = kPair ? 2 : I::kTile;                       // items of a tile
+  static_assert(!kPair || !kFp8);
   const CUtensorMap* map;
   uint32_t ring, bar_full, bar_empty;
   TreeCursor cur;
   TreeSegment g;
+  int rank = 0;                   // in the pair
   uint32_t slot = 0, parity = 1;  // of the next item; parity: of the wait for the slot to be empty
   int issued = 0;                 // items so far, kSlots at most
   int tile = 0, index = 0, page = -1, page_next = -1;
@@ -238,22 +254,33 @@ struct Feed {
   __device__ __forceinline__ void issue(const TreeParams& p) {
     const int lane = threadIdx.x & 31;
     const uint32_t full = bar_full + 8u * slot;
-    const int at = (kIsV ? index * kKeys : 0) + k;  // key of the tile
+    const int at = (kIsV ? index * kKeys : kPair ? rank * kKeys : 0) + k;  // key of the tile
     const int pg = __shfl_sync(0xffffffffu, page, (at >> 3) & 15);
     const bool send = mine && pg >= 0;
-    uint32_t total = kSlotBytes;
-    if (!whole) total = bytes * uint32_t(__popc(__ballot_sync(0xffffffffu, send)));
-    if (lane == 0) mbar_arrive_expect_tx(full, total);
+    uint32_t total = kPair ? 2 * kSlotBytes : kSlotBytes;
+    if (!whole) {
+      uint32_t boxes = __popc(__ballot_sync(0xffffffffu, send));
+      if constexpr (kPair) {  // and the other CTA's, whose keys are others
+        const int other = kIsV ? at : at ^ kKeys;
+        const int its = __shfl_sync(0xffffffffu, page, (other >> 3) & 15);  // by all lanes
+        boxes += __popc(__ballot_sync(0xffffffffu, mine && its >= 0));
+      }
+      total = bytes * boxes;
+    }
+    if (lane == 0 && (!kPair || rank == 0)) mbar_arrive_expect_tx(full, total);
     __syncwarp();
     if (send) {
-      const uint32_t j = uint32_t(tile) * kTreeTile + uint32_t(at);
-      tma_load_5d(ring + slot * uint32_t(kSlotBytes) + offset, map, full, 0, int(j & ((1u << p.c.page_shift) - 1)),
-                  kIsV ? block : index, g.h, pg);
+      const uint32_t j = uint32_t(tile) * kTreeTile + uint32_t(at), dst = ring + slot * uint32_t(kSlotBytes) + offset;
+      const int in_page = int(j & ((1u << p.c.page_shift) - 1));
+      if constexpr (kPair)
+        tma_load_5d_pair(dst, map, mapa_shared(full, 0), 0, in_page, (kIsV ? rank * kBlocks : index * kBlocks) + block, g.h, pg);
+      else
+        tma_load_5d(dst, map, full, 0, in_page, kIsV ? block : index, g.h, pg);
     }
     __syncwarp();
     if (issued < kSlots) ++issued;
     if (++slot == kSlots) slot = 0, parity ^= 1u;
-    if (++index == I::kTile) {
+    if (++index == kTile) {
       index = 0;
       if (++tile < g.t1) {
         check(p, page_next);
@@ -265,6 +292,7 @@ struct Feed {
   }
   // No copy may be in flight when the CTA ends: the last use of each slot is complete.
   __device__ __forceinline__ void drain(const TreeParams& p) const {
+    if (kPair && rank != 0) return;  // the even CTA's barriers count this one's too; it is waited for at the end
     for (int i = 0; i < issued; ++i) {
       const uint32_t s = slot + kSlots - 1 - i, at = s % kSlots;
       // slots below `slot` have been used in this round (parity ^ 1 of the wait before), others in the last
@@ -309,8 +337,9 @@ __device__ __forceinline__ void produce(const TreeParams& p, A& a, B& b) {
 }
 
 // The tensor map of a pool's keys or values: (columns of a 128-byte block, token of the page,
-// block, head, page); boxes of `keys` tokens or a page of fewer, of one column block or all.
-inline bool encode_tokens(CUtensorMap* m, const CacheView& c, const void* data, int keys, bool all_blocks) {
+// block, head, page); boxes of `keys` tokens and `blocks` column blocks, or
+// of a page of fewer and `fewer` blocks.
+inline bool encode_tokens(CUtensorMap* m, const CacheView& c, const void* data, int keys, int blocks, int fewer) {
   EncodeTiledFn enc = encode_tiled_fn();
   if (!enc) return false;
   const cuuint64_t es = c.dtype == GQA_F32 ? 4 : c.dtype == GQA_BF16 ? 2 : 1, page = cuuint64_t(1) << c.page_shift;
@@ -319,7 +348,7 @@ inline bool encode_tokens(CUtensorMap* m, const CacheView& c, const void* data, 
   const cuuint64_t strides[4] = {cuuint64_t(c.st) * es, 128, c.Hkv > 1 ? cuuint64_t(c.sh) * es : 16,
                                  c.n_pages > 1 ? cuuint64_t(c.sp) * es : 16};
   const cuuint32_t box[5] = {cuuint32_t(128 / es), cuuint32_t(page < cuuint64_t(keys) ? page : keys),
-                             cuuint32_t(all_blocks ? 2 * es : 1), 1, 1},
+                             cuuint32_t(page < cuuint64_t(keys) ? fewer : blocks), 1, 1},
                    estr[5] = {1, 1, 1, 1, 1};
   return enc(m, es == 4 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : es == 2 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
                                                                    : CU_TENSOR_MAP_DATA_TYPE_UINT8,
@@ -329,8 +358,8 @@ inline bool encode_tokens(CUtensorMap* m, const CacheView& c, const void* data, 
 }
 // The same as Feed takes them.
 inline bool encode_pages(CUtensorMap* m, const CacheView& c, bool values) {
-  const int most = !values ? 7 : c.dtype == GQA_E4M3 ? 6 : 5;
-  return encode_tokens(m, c, values ? c.v : c.k, 1 << most, values && c.page_shift >= most);
+  const bool fp8 = c.dtype == GQA_E4M3;
+  return values ? encode_tokens(m, c, c.v, fp8 ? 64 : 32, fp8 ? 2 : 4, 1) : encode_tokens(m, c, c.k, 128, 1, 1);
 }
 
 // One 16-byte unit of a value in shared memory: cleared whole, or its elements that are not

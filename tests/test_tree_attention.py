@@ -8,6 +8,12 @@ largest element times sum |k| / 16, below 2e-4 for these inputs, which bounds th
 Each probability is rounded to at least 8 bits, off by at most 2^-8 of itself, and so is the output: out is
 off by at most 2^-8 (|out| + sum p |v| / sum p) plus the scores' share, 2 x 2e-4 of
 that sum.
+Over e4m3 values, that holds for probabilities down to 2^-6 of the largest p s (s: the
+value's scale).  16 p s / m is stored, m at most that largest, in two e4m3 pieces whose
+smallest step is 2^-9: a smaller p is off by at most 2^-10 / 16 = 2^-14 of max(p s) / s, and
+out by 2^-14 max(p) / sum p x (sum of the |v| a row sees) x (largest s / smallest s), which is
+2 for rows of 256 normal numbers, whose largest lies in (1.75, 7].  Where a row sees few keys
+of very different weights (``small``) this is added.
 """
 
 import numpy as np
@@ -68,7 +74,19 @@ class Problem:
         return cache.attend(self.q.to(self.dev), self.pool, self.table, self.ctx_dev, tree_mask=mask,
                             tree_lens=self.drafted_dev, **kw)
 
-    def check(self, out, lse, mask=None, rows=None):
+    def small(self, b, mask):
+        """What e4m3 probabilities below 2^-6 of the largest lose: see the tolerances above."""
+        n, T, G = self.ctx[b] + self.drafted[b], self.q.shape[2], self.q.shape[1] // self.k.shape[1]
+        sees = np.zeros((T, n), dtype=bool)
+        d = self.drafted[b]
+        sees[:d, : self.ctx[b]] = True
+        sees[:d, self.ctx[b]:] = np.tril(np.ones((d, d), dtype=bool)) if mask is None else np.asarray(mask)[:d, :d]
+        k, v = (x[b, :, :n].double().numpy().repeat(G, 0) for x in (self.k, self.v))
+        x = np.where(sees, self.q[b].double().numpy() @ k.transpose(0, 2, 1) / 16.0, -np.inf)
+        w = np.exp(x - np.max(x, -1, keepdims=True, initial=-1e300))
+        return 2.0 ** -13 / np.maximum(w.sum(-1, keepdims=True), 1.0) * (sees @ np.abs(v))
+
+    def check(self, out, lse, mask=None, rows=None, small=False):
         exact = self.q.dtype == F32
         out, lse = out.double().cpu().numpy(), lse.double().cpu().numpy()
         for b in range(len(self.ctx)) if rows is None else rows:
@@ -84,6 +102,8 @@ class Problem:
                 tol_o, tol_l = 2e-5 * max(1.0, float(np.abs(o).max())), 1e-5
             else:
                 tol_o, tol_l = 2.0 ** -8 * (np.abs(o) + spread) + 4e-4 * spread, 2e-4
+            if small:
+                tol_o = tol_o + self.small(b, m)
             d_l = np.abs(lse[b][fin] - l[fin]).max()
             d_o = np.abs(out[b] - o)
             assert d_l <= tol_l, f"sequence {b}: LSE off by {d_l:.2e}"
@@ -426,3 +446,52 @@ def test_a_visible_nan_reaches_its_rows(cuda_device, dtype, kind, bits):
         same = ~nans if column is not None else ~nans.any(-1, keepdim=True).expand_as(nans)
         assert torch.equal(out[same], clean[same])
         at.copy_(kept)
+
+
+@pytest.mark.parametrize("dtype,kind", [(BF16, BF16), (BF16, E4M3)], ids=["bf16", "bf16_e4m3"])
+@pytest.mark.parametrize("T,Hq,page", [(40, 16, 8), (64, 16, 16), (33, 32, 64), (128, 16, 128), (96, 16, 32)])
+def test_many_rows(cuda_device, dtype, kind, T, Hq, page):
+    """Two to four tiles of 128 rows to a head, ragged contexts and trees, padding rows."""
+    ctx = [0, 130, 700, 63]
+    p = Problem(cuda_device, 4, Hq, 4, T, ctx, page, dtype, kind, seed=T, drafted=[T, T - 3, 1, 0])
+    p.check(*p.attend(), small=kind == E4M3)
+    mask = np.stack([_tree(T, 60 + b) for b in range(4)])
+    mask[0, 5] = False  # a row that sees nothing where there is no context
+    p.check(*p.attend(mask), mask=mask, small=kind == E4M3)
+    assert cache.status(p.pool) == 0
+
+
+@pytest.mark.parametrize("column", [3, 127, 128, 250])
+@pytest.mark.parametrize("bad", [float("nan"), float("inf"), -float("inf")], ids=["nan", "inf", "-inf"])
+def test_hidden_values_of_many_rows(cuda_device, bad, column):
+    """Two tiles of rows: a bad value in any column reaches the rows that see it, in that column."""
+    T = 48
+    p = Problem(cuda_device, 1, 16, 4, T, [100], 32, BF16, BF16, seed=9)
+    mask = _tree(T, 4)
+    clean, clean_lse = p.attend(mask)
+    at = p.pool.v[p.table[0, (100 + 7) // 32].item(), 2, (100 + 7) % 32]
+    at[column] = bad
+    out, lse = p.attend(mask)
+    sees = torch.zeros((1, 16, T, 256), dtype=torch.bool)
+    sees[0, 8:12, torch.as_tensor(mask[:, 7]), column] = True
+    assert torch.equal(lse, clean_lse)
+    assert torch.equal(out[~sees.to(out.device)], clean[~sees.to(out.device)])
+    got = out[sees.to(out.device)].float()
+    assert got.numel() and bool((got.isnan() if bad != bad else got == bad).all())
+
+
+@pytest.mark.parametrize("kind", [BF16, E4M3], ids=["bf16", "e4m3"])
+def test_many_rows_over_long_contexts(cuda_device, kind):
+    """Rings go round many times, workers cross heads; equal calls give equal bits, also replayed."""
+    p = Problem(cuda_device, 2, 16, 4, 40, [9000, 4100], 16, BF16, kind, seed=41)
+    first, lse = p.attend()
+    p.check(first, lse)
+    for _ in range(20):
+        out, l2 = p.attend()
+        assert torch.equal(out, first) and torch.equal(l2, lse)
+    q, graph = p.q.to(cuda_device), torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out, l2 = cache.attend(q, p.pool, p.table, p.ctx_dev)
+    for _ in range(3):
+        graph.replay()
+    assert torch.equal(out, first) and torch.equal(l2, lse)
