@@ -17,6 +17,7 @@ template <int kPerRow>
 __global__ void __launch_bounds__(256) tree_merge_kernel(const __grid_constant__ TreeParams p, int rows_per_tile) {
   __shared__ float sh_sum[8], sh_max[8];
   __shared__ float sh_acc[kPerRow == 8 ? 8 : 1][kHeadDim];
+  launch_dependents();
   const int64_t rows_per_seq = int64_t(p.c.Hkv) * p.G * p.T;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int64_t row = kPerRow == 8 ? int64_t(blockIdx.x) : int64_t(blockIdx.x) * 8 + warp;
@@ -123,18 +124,8 @@ int launch_tree_merge(const TreeParams& p, int rows_per_tile, cudaStream_t strea
   const bool few = rows <= 2 * kB200Sms;  // a CTA per row then fills the SMs about once
   const int64_t blocks = few ? rows : (rows + 7) / 8;
   if (blocks > 0x7fffffff) return GQA_ERR_UNSUPPORTED;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(unsigned(blocks));
-  cfg.blockDim = dim3(256);
-  cfg.stream = stream;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  const cudaError_t e = few ? cudaLaunchKernelEx(&cfg, tree_merge_kernel<8>, p, rows_per_tile)
-                            : cudaLaunchKernelEx(&cfg, tree_merge_kernel<1>, p, rows_per_tile);
-  return e == cudaSuccess ? GQA_OK : GQA_ERR_LAUNCH;
+  return few ? launch_programmatic(tree_merge_kernel<8>, unsigned(blocks), 256, 0, stream, p, rows_per_tile)
+             : launch_programmatic(tree_merge_kernel<1>, unsigned(blocks), 256, 0, stream, p, rows_per_tile);
 }
 
 }  // namespace gqa

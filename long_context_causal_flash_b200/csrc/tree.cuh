@@ -182,6 +182,24 @@ bool allow_smem(int bytes) {
   return true;
 }
 
+// Launches a kernel that may start while the one before it in the stream still runs, and
+// itself waits for that one's end (wait_for_grid).
+template <typename... Params, typename... Args>
+int launch_programmatic(void (*kernel)(Params...), unsigned blocks, int threads, int smem, cudaStream_t stream,
+                        const Args&... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(blocks);
+  cfg.blockDim = dim3(unsigned(threads));
+  cfg.dynamicSmemBytes = size_t(smem);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, args...) == cudaSuccess ? GQA_OK : GQA_ERR_LAUNCH;
+}
+
 // fp32 accuracy: q of either type, any pages but bf16 q over bf16 or e4m3 ones; rows 8, 16
 // or 24.
 int launch_tree_f32(const TreeParams& p, int rows, bool q_bf16, cudaStream_t stream);

@@ -205,6 +205,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_f32_kernel(const __grid_cons
     for (int i = 0; i < F::kSlotsV; ++i) mbar_init(full_v + 8u * i, 1);
     fence_barrier_init();
   }
+  wait_for_grid();  // what comes before in the stream may still have been running
   if (warp == 0) {
     const TreeCursor c = tree_start(p, worker);
     if (lane == 0) start = c;
@@ -565,9 +566,8 @@ int launch_one(const TreeParams& p, cudaStream_t stream) {
   constexpr int blocks = 2 * F32Cfg<NT, kCache, QT>::kEs;
   if (!encode_tokens(&map_k, p.c, p.c.k, kChunk, blocks, blocks) || !encode_tokens(&map_v, p.c, p.c.v, kChunk, blocks, blocks))
     return GQA_ERR_LAUNCH;
-  tree_f32_kernel<NT, kCache, QT><<<unsigned(p.workers) * unsigned(p.row_tiles), kThreads, smem, stream>>>(p, map_k,
-                                                                                                         map_v);
-  return cudaGetLastError() == cudaSuccess ? GQA_OK : GQA_ERR_LAUNCH;
+  return launch_programmatic(tree_f32_kernel<NT, kCache, QT>, unsigned(p.workers) * unsigned(p.row_tiles), kThreads, smem,
+                             stream, p, map_k, map_v);
 }
 
 template <int NT>

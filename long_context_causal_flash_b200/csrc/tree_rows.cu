@@ -114,6 +114,7 @@ __global__ void __launch_bounds__(RowsCfg<kFp8>::kThreads, 1) tree_rows_kernel(c
   auto lead = [&](int i) { return lead_bar + 8u * uint32_t(i); };
   int32_t* status = p.c.status;
 
+  wait_for_grid();  // what comes before in the stream may still have been running
   if (warp == 0) {
     const TreeCursor c = tree_start(p, worker);
     if (lane == 0) {
@@ -392,28 +393,27 @@ __global__ void __launch_bounds__(RowsCfg<kFp8>::kThreads, 1) tree_rows_kernel(c
 
     while (ok && tree_next(p, cur, &g)) {
       const int32_t* table = p.table + int64_t(g.b) * p.max_pages;
-      // Q of this head, eight rows per warp, four loads in flight.
+      // Q of this head, eight rows per warp, four loads in flight (and the code of one row: it is
+      // run from a cold instruction cache).
+      auto q_row = [&](int i) {
+        const int n = rt * kRows + warp + i * kSoftWarps, tq = n >> g_shift;
+        uint4 u = make_uint4(0, 0, 0, 0);
+        if (i < kRows / kSoftWarps && tq < g.s.drafted)
+          u = *reinterpret_cast<const uint4*>(reinterpret_cast<const __nv_bfloat16*>(p.q.p) + g.b * p.q.sb +
+                                              int64_t(g.h * p.G + (n & (p.G - 1))) * p.q.sh + tq * p.q.sl + 8 * lane);
+        return u;
+      };
+      uint4 u[4] = {q_row(0), q_row(1), q_row(2), q_row(3)};
 #pragma unroll 1
-      for (int r0 = warp; r0 < kRows; r0 += 4 * kSoftWarps) {
-        uint4 u[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int n = rt * kRows + r0 + i * kSoftWarps, tq = n >> g_shift;
-          u[i] = make_uint4(0, 0, 0, 0);
-          if (tq < g.s.drafted)
-            u[i] = *reinterpret_cast<const uint4*>(reinterpret_cast<const __nv_bfloat16*>(p.q.p) + g.b * p.q.sb +
-                                                   int64_t(g.h * p.G + (n & (p.G - 1))) * p.q.sh + tq * p.q.sl + 8 * lane);
+      for (int i = 0; i < kRows / kSoftWarps; ++i) {
+        const int rq = warp + i * kSoftWarps;
+        if constexpr (!kFp8) {
+          sts16(sQ + uint32_t(lane >> 3) * (kRows * 128u) + uint32_t(rq) * 128u + uint32_t(((lane & 7) ^ (rq & 7)) << 4), u[0]);
+        } else {
+          const float f = put_query<kRows, false>(u[0], sQ, rq);
+          if (lane == 0) sh_f[rq] = f * p.scale_log2;
         }
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int rq = r0 + i * kSoftWarps;
-          if constexpr (!kFp8) {
-            sts16(sQ + uint32_t(lane >> 3) * (kRows * 128u) + uint32_t(rq) * 128u + uint32_t(((lane & 7) ^ (rq & 7)) << 4), u[i]);
-          } else {
-            const float f = put_query<kRows, false>(u[i], sQ, rq);
-            if (lane == 0) sh_f[rq] = f * p.scale_log2;
-          }
-        }
+        u[0] = u[1], u[1] = u[2], u[2] = u[3], u[3] = q_row(i + 4);
       }
       if (warp == 0) sh_bad[lane] = 0;
       fence_proxy_async_smem();
@@ -488,9 +488,9 @@ __global__ void __launch_bounds__(RowsCfg<kFp8>::kThreads, 1) tree_rows_kernel(c
         uint32_t vis = there;
         const bool drafted_tile = j0 + 32 > g.s.ctx && vis != 0;
         if (drafted_tile && live) {
-#pragma unroll 8
+#pragma unroll 16
           for (int i = 0; i < 32; ++i)
-            if (j0 + i >= g.s.ctx && ((vis >> i) & 1u) && !tree_sees(p, g.b, t, int(j0 + i - g.s.ctx))) vis &= ~(1u << i);
+            if (j0 + i >= g.s.ctx && ((there >> i) & 1u) && !tree_sees(p, g.b, t, int(j0 + i - g.s.ctx))) vis &= ~(1u << i);
         }
         const bool masked = __any_sync(0xffffffffu, vis != 0xffffffffu);
         fine = warp_wait(bar(kRBarS + int(sb)), ph, budget, status) && fine;
@@ -625,35 +625,49 @@ __global__ void __launch_bounds__(RowsCfg<kFp8>::kThreads, 1) tree_rows_kernel(c
         const float inv = none ? 0.f : (kFp8 ? 1.f / kPScale : 1.f) / sum;
         const float lse = none ? -INFINITY : (m + log2f(sum)) * kLn2;
         const bool whole = g.whole();
-        const int64_t part_row = ((int64_t(worker) * 2 + g.slot()) * p.row_tiles + rt) * kRows + r;
-        const int64_t out_row =
-            ((int64_t(g.b) * p.c.Hkv + g.h) * p.G + (row & (p.G - 1))) * int64_t(p.T) + t;
+        const int64_t part_row = ((int64_t(worker) * 2 + g.slot()) * p.row_tiles + rt) * kRows;
+        const int64_t head = (int64_t(g.b) * p.c.Hkv + g.h) * p.G;
         if (mine && part == 0) {
           if (whole)
-            p.lse[out_row] = lse;
+            p.lse[(head + (row & (p.G - 1))) * p.T + t] = lse;
           else
-            p.lse_part[part_row] = lse;
+            p.lse_part[part_row + r] = lse;
         }
         const bool bad = __any_sync(0xffffffffu, sh_bad[lane] != 0);
+        // 32 rows x 32 columns at a time through Q's place, so that eight lanes write 128 (64)
+        // bytes of a row; a lane that writes its own row takes 8 us for a tile of 128.
+        const uint32_t stage = sQ + uint32_t(warp) * 4096u;
 #pragma unroll 1
-        for (int c0 = part * 64; c0 < part * 64 + 64; c0 += 16) {
-          float o[16];
-          umma::tmem_ld16(lane_addr + uint32_t(c0), o);
+        for (int c0 = part * 64; c0 < part * 64 + 64; c0 += 32) {
+          float o[32];
+          umma::tmem_ld32(lane_addr + uint32_t(c0), o);
           umma::tmem_wait_ld();
 #pragma unroll
-          for (int i = 0; i < 16; ++i) {
-            o[i] = none ? 0.f : o[i] * inv;
-            if (bad && !none) o[i] += hidden_values<kFp8>(p, g, table, sh_bad, t, c0 + i);
+          for (int i = 0; i < 32; ++i) o[i] = none ? 0.f : o[i] * inv;
+          if (bad && !none)
+#pragma unroll
+            for (int i = 0; i < 32; ++i) o[i] += hidden_values<kFp8>(p, g, table, sh_bad, t, c0 + i);
+#pragma unroll
+          for (int i = 0; i < 8; ++i)
+            sts16(stage + uint32_t(lane) * 128u + uint32_t((i ^ (lane & 7)) << 4),
+                  make_uint4(__float_as_uint(o[4 * i]), __float_as_uint(o[4 * i + 1]), __float_as_uint(o[4 * i + 2]),
+                             __float_as_uint(o[4 * i + 3])));
+          __syncwarp();
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            const int rr = 4 * i + (lane >> 3), n = rt * kRows + quarter * 32 + rr;
+            const uint4 y = lds16(stage + uint32_t(rr) * 128u + uint32_t(((lane ^ rr) & 7) << 4));
+            if (n >= p.T * p.G) continue;
+            const int col = c0 + 4 * (lane & 7);
+            if (whole)
+              *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(p.out) +
+                                        ((head + (n & (p.G - 1))) * p.T + (n >> g_shift)) * kHeadDim + col) =
+                  make_uint2(pack_bf16x2(__uint_as_float(y.x), __uint_as_float(y.y)),
+                             pack_bf16x2(__uint_as_float(y.z), __uint_as_float(y.w)));
+            else
+              *reinterpret_cast<uint4*>(p.o_part + (part_row + quarter * 32 + rr) * kHeadDim + col) = y;
           }
-          if (mine && whole) {
-            __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(p.out) + out_row * kHeadDim + c0;
-            store8(dst, o);
-            store8(dst + 8, o + 8);
-          } else if (mine) {
-            float* dst = p.o_part + part_row * kHeadDim + c0;
-            store8(dst, o);
-            store8(dst + 8, o + 8);
-          }
+          __syncwarp();
         }
         umma::fence_before_sync();
       }
@@ -684,13 +698,15 @@ int launch(const TreeParams& p, const CUtensorMap& mk, const CUtensorMap& mv, cu
   cfg.blockDim = dim3(F::kThreads);
   cfg.dynamicSmemBytes = F::kSmem;
   cfg.stream = stream;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = 2;
-  attr[0].val.clusterDim.y = 1;
-  attr[0].val.clusterDim.z = 1;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = 2;
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = kPair ? 1 : 0;
+  cfg.numAttrs = kPair ? 2 : 1;
   return cudaLaunchKernelEx(&cfg, tree_rows_kernel<kFp8, kPair>, mk, mv, p) == cudaSuccess ? GQA_OK : GQA_ERR_LAUNCH;
 }
 

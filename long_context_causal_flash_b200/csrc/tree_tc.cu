@@ -121,6 +121,7 @@ __global__ void __launch_bounds__(Cfg<kN, kFp8>::kThreads, 1) tree_tc_kernel(con
   const int64_t budget = p.wait_budget_ns;
   int32_t* status = p.c.status;
 
+  wait_for_grid();  // what comes before in the stream may still have been running
   if (warp == 0) {
     const TreeCursor c = tree_start(p, worker);
     if (lane == 0) {
@@ -269,31 +270,32 @@ __global__ void __launch_bounds__(Cfg<kN, kFp8>::kThreads, 1) tree_tc_kernel(con
     uint32_t tt = 0;  // tiles so far
     bool ok = true;
 
-    while (ok && tree_next(p, cur, &g)) {
+    // Q's rows of this warp, loaded ahead of their segment.
+    constexpr int kQRows = kN / F::kSoftWarps;
+    uint4 u[kQRows];
+    auto load_q = [&]() {
+#pragma unroll
+      for (int i = 0; i < kQRows; ++i) {
+        const int n = row0 + warp + i * F::kSoftWarps, t = n >> g_shift;
+        u[i] = make_uint4(0, 0, 0, 0);
+        if (t < g.s.drafted)
+          u[i] = *reinterpret_cast<const uint4*>(reinterpret_cast<const __nv_bfloat16*>(p.q.p) + g.b * p.q.sb +
+                                                 int64_t(g.h * p.G + (n & (p.G - 1))) * p.q.sh + t * p.q.sl + 8 * lane);
+      }
+    };
+    bool more = tree_next(p, cur, &g);
+    if (more) load_q();
+
+    while (ok && more) {
       const int32_t* table = p.table + int64_t(g.b) * p.max_pages;
-      // Q of this head: all softmax warps, a row each time; every reader of the last one is done.
-      constexpr int kQRows = kN / F::kSoftWarps < 4 ? kN / F::kSoftWarps : 4;  // loads in flight
-#pragma unroll 1
-      for (int r0 = warp; r0 < kN; r0 += kQRows * F::kSoftWarps) {
-        uint4 u[kQRows];
 #pragma unroll
-        for (int i = 0; i < kQRows; ++i) {
-          const int n = row0 + r0 + i * F::kSoftWarps, t = n >> g_shift;
-          u[i] = make_uint4(0, 0, 0, 0);
-          if (t < g.s.drafted)
-            u[i] = *reinterpret_cast<const uint4*>(reinterpret_cast<const __nv_bfloat16*>(p.q.p) + g.b * p.q.sb +
-                                                   int64_t(g.h * p.G + (n & (p.G - 1))) * p.q.sh + t * p.q.sl + 8 * lane);
-        }
-#pragma unroll
-        for (int i = 0; i < kQRows; ++i) {
-          const int r = r0 + i * F::kSoftWarps;
-          if constexpr (!kFp8) {
-            sts16(sQ + uint32_t(lane >> 3) * (kN * 128u) + uint32_t(r) * 128u + uint32_t(((lane & 7) ^ (r & 7)) << 4),
-                  u[i]);
-          } else {
-            const float f = put_query<kN, true>(u[i], sQ, r);
-            if (lane == 0) sh_f[r] = f * p.scale_log2;
-          }
+      for (int i = 0; i < kQRows; ++i) {
+        const int r = warp + i * F::kSoftWarps;
+        if constexpr (!kFp8) {
+          sts16(sQ + uint32_t(lane >> 3) * (kN * 128u) + uint32_t(r) * 128u + uint32_t(((lane & 7) ^ (r & 7)) << 4), u[i]);
+        } else {
+          const float f = put_query<kN, true>(u[i], sQ, r);
+          if (lane == 0) sh_f[r] = f * p.scale_log2;
         }
       }
       if (quarter == 0 && lane < C) sh_m[n0 + lane] = 0.f;
@@ -541,6 +543,9 @@ __global__ void __launch_bounds__(Cfg<kN, kFp8>::kThreads, 1) tree_tc_kernel(con
       }
       // ------------------------------------------------------------ the segment's result
       const uint32_t last = tt - 1;
+      const TreeSegment d = g;  // the one that is done; the next one's Q is loaded meanwhile
+      more = tree_next(p, cur, &g);
+      if (more) load_q();
       if (ok) ok = warp_wait(bar(kBarPV + int(last & 1u)), (last >> 1) & 1u, budget, status);
       umma::fence_after_sync();
       ok = !any_thread(15, kAll, !ok);
@@ -555,9 +560,9 @@ __global__ void __launch_bounds__(Cfg<kN, kFp8>::kThreads, 1) tree_tc_kernel(con
           if (lane < 16) put(c0, v);
         }
         sync_threads(part_bar, 128);
-        const bool whole = g.whole();
-        const int64_t part_at = ((int64_t(worker) * 2 + g.slot()) * p.row_tiles + rt) * kN;
-        const int64_t head_row = (int64_t(g.b) * p.c.Hkv + g.h) * p.G;
+        const bool whole = d.whole();
+        const int64_t part_at = ((int64_t(worker) * 2 + d.slot()) * p.row_tiles + rt) * kN;
+        const int64_t head_row = (int64_t(d.b) * p.c.Hkv + d.h) * p.G;
         const bool bad = __any_sync(0xffffffffu, sh_bad[lane] != 0);
         // Lane n of every warp: row n's factor.
         const int my_row = row0 + n0 + lane, my_t = my_row >> g_shift;
@@ -565,7 +570,7 @@ __global__ void __launch_bounds__(Cfg<kN, kFp8>::kThreads, 1) tree_tc_kernel(con
         if (lane < C && my_row < rows_all) {
           const int c0 = lane & 16, n = lane & 15;
           const float sum = (get(c0, 0, n) + get(c0, 1, n)) + (get(c0, 2, n) + get(c0, 3, n));
-          const bool none = my_t >= g.s.drafted || sum == 0.f;
+          const bool none = my_t >= d.s.drafted || sum == 0.f;
           inv = none ? 0.f : (kFp8 ? 1.f / kPScale : 1.f) / sum;
           if (quarter == 0) {
             const float lse = none ? -INFINITY : (sh_m[n0 + lane] + log2f(sum)) * kLn2;
@@ -600,7 +605,7 @@ __global__ void __launch_bounds__(Cfg<kN, kFp8>::kThreads, 1) tree_tc_kernel(con
 #pragma unroll
             for (int half = 0; half < 2; ++half) {
               float v = f == 0.f ? 0.f : o[half][i] * f;
-              if (bad && f != 0.f) v += hidden_values<kFp8>(p, g, table, sh_bad, t, half * 128 + key);
+              if (bad && f != 0.f) v += hidden_values<kFp8>(p, d, table, sh_bad, t, half * 128 + key);
               if (row >= rows_all) continue;
               if (whole)
                 static_cast<__nv_bfloat16*>(p.out)[at + half * 128] = __float2bfloat16_rn(v);
@@ -627,8 +632,8 @@ template <int kN, bool kFp8>
 int launch_n(const TreeParams& p, const CUtensorMap& mk, const CUtensorMap& mv, cudaStream_t stream) {
   using F = Cfg<kN, kFp8>;
   if (!allow_smem<tree_tc_kernel<kN, kFp8>>(F::kSmem)) return GQA_ERR_LAUNCH;
-  tree_tc_kernel<kN, kFp8><<<unsigned(p.workers) * unsigned(p.row_tiles), F::kThreads, F::kSmem, stream>>>(mk, mv, p);
-  return cudaGetLastError() == cudaSuccess ? GQA_OK : GQA_ERR_LAUNCH;
+  return launch_programmatic(tree_tc_kernel<kN, kFp8>, unsigned(p.workers) * unsigned(p.row_tiles), F::kThreads, F::kSmem,
+                             stream, mk, mv, p);
 }
 
 template <bool kFp8>
