@@ -393,27 +393,26 @@ __global__ void __launch_bounds__(RowsCfg<kFp8>::kThreads, 1) tree_rows_kernel(c
 
     while (ok && tree_next(p, cur, &g)) {
       const int32_t* table = p.table + int64_t(g.b) * p.max_pages;
-      // Q of this head, eight rows per warp, four loads in flight (and the code of one row: it is
-      // run from a cold instruction cache).
-      auto q_row = [&](int i) {
+      // Q of this head, eight rows per warp, all loads in flight.
+      constexpr int kQRows = kRows / kSoftWarps;
+      uint4 u[kQRows];
+#pragma unroll
+      for (int i = 0; i < kQRows; ++i) {
         const int n = rt * kRows + warp + i * kSoftWarps, tq = n >> g_shift;
-        uint4 u = make_uint4(0, 0, 0, 0);
-        if (i < kRows / kSoftWarps && tq < g.s.drafted)
-          u = *reinterpret_cast<const uint4*>(reinterpret_cast<const __nv_bfloat16*>(p.q.p) + g.b * p.q.sb +
-                                              int64_t(g.h * p.G + (n & (p.G - 1))) * p.q.sh + tq * p.q.sl + 8 * lane);
-        return u;
-      };
-      uint4 u[4] = {q_row(0), q_row(1), q_row(2), q_row(3)};
-#pragma unroll 1
-      for (int i = 0; i < kRows / kSoftWarps; ++i) {
+        u[i] = make_uint4(0, 0, 0, 0);
+        if (tq < g.s.drafted)
+          u[i] = *reinterpret_cast<const uint4*>(reinterpret_cast<const __nv_bfloat16*>(p.q.p) + g.b * p.q.sb +
+                                                 int64_t(g.h * p.G + (n & (p.G - 1))) * p.q.sh + tq * p.q.sl + 8 * lane);
+      }
+#pragma unroll
+      for (int i = 0; i < kQRows; ++i) {
         const int rq = warp + i * kSoftWarps;
         if constexpr (!kFp8) {
-          sts16(sQ + uint32_t(lane >> 3) * (kRows * 128u) + uint32_t(rq) * 128u + uint32_t(((lane & 7) ^ (rq & 7)) << 4), u[0]);
+          sts16(sQ + uint32_t(lane >> 3) * (kRows * 128u) + uint32_t(rq) * 128u + uint32_t(((lane & 7) ^ (rq & 7)) << 4), u[i]);
         } else {
-          const float f = put_query<kRows, false>(u[0], sQ, rq);
+          const float f = put_query<kRows, false>(u[i], sQ, rq);
           if (lane == 0) sh_f[rq] = f * p.scale_log2;
         }
-        u[0] = u[1], u[1] = u[2], u[2] = u[3], u[3] = q_row(i + 4);
       }
       if (warp == 0) sh_bad[lane] = 0;
       fence_proxy_async_smem();
@@ -487,10 +486,18 @@ __global__ void __launch_bounds__(RowsCfg<kFp8>::kThreads, 1) tree_rows_kernel(c
         const float* scale = sh_scale + sb * 384 + part * 32;
         uint32_t vis = there;
         const bool drafted_tile = j0 + 32 > g.s.ctx && vis != 0;
-        if (drafted_tile && live) {
-#pragma unroll 16
-          for (int i = 0; i < 32; ++i)
-            if (j0 + i >= g.s.ctx && ((there >> i) & 1u) && !tree_sees(p, g.b, t, int(j0 + i - g.s.ctx))) vis &= ~(1u << i);
+        if (drafted_tile) {
+          // A lane looks at one key for each token of the quarter's rows in turn: loads of whole
+          // lines, eight in flight.
+          const int u = int(j0 + lane - g.s.ctx), t0 = (rt * kRows + quarter * 32) >> g_shift;
+          uint32_t mine_sees = 0;
+#pragma unroll 8
+          for (int i = 0; i < 32 >> g_shift; ++i) {
+            const bool sees = u < 0 || (u < g.s.drafted && t0 + i < g.s.drafted && tree_sees(p, g.b, t0 + i, u));
+            const uint32_t word = __ballot_sync(0xffffffffu, sees);
+            if (t == t0 + i) mine_sees = word;
+          }
+          if (live) vis &= mine_sees;
         }
         const bool masked = __any_sync(0xffffffffu, vis != 0xffffffffu);
         fine = warp_wait(bar(kRBarS + int(sb)), ph, budget, status) && fine;
@@ -644,14 +651,20 @@ __global__ void __launch_bounds__(RowsCfg<kFp8>::kThreads, 1) tree_rows_kernel(c
           umma::tmem_wait_ld();
 #pragma unroll
           for (int i = 0; i < 32; ++i) o[i] = none ? 0.f : o[i] * inv;
-          if (bad && !none)
-#pragma unroll
-            for (int i = 0; i < 32; ++i) o[i] += hidden_values<kFp8>(p, g, table, sh_bad, t, c0 + i);
 #pragma unroll
           for (int i = 0; i < 8; ++i)
             sts16(stage + uint32_t(lane) * 128u + uint32_t((i ^ (lane & 7)) << 4),
                   make_uint4(__float_as_uint(o[4 * i]), __float_as_uint(o[4 * i + 1]), __float_as_uint(o[4 * i + 2]),
                              __float_as_uint(o[4 * i + 3])));
+          if (bad && !none)
+#pragma unroll 1
+            for (int i = 0; i < 32; ++i) {
+              const uint32_t a = stage + uint32_t(lane) * 128u + uint32_t((((i >> 2) ^ lane) & 7) << 4) + uint32_t(i & 3) * 4u;
+              float y;
+              asm volatile("ld.shared.f32 %0, [%1];" : "=f"(y) : "r"(a) : "memory");
+              y += hidden_values<kFp8>(p, g, table, sh_bad, t, c0 + i);
+              asm volatile("st.shared.f32 [%0], %1;" ::"r"(a), "f"(y) : "memory");
+            }
           __syncwarp();
 #pragma unroll
           for (int i = 0; i < 8; ++i) {
