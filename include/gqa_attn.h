@@ -566,9 +566,11 @@ int gqa_attn_cache_read(const gqa_cache_t *cache, const int32_t *page_table, int
  *                 overwritten; calls that share one must be ordered on one stream.
  * What a row's mask hides does not reach the row, NaN and infinities among it.  Work is cut
  * evenly over the SMs whatever the lengths; partial results are merged in a fixed order, so
- * equal calls give equal bits.  GQA_BF16 queries over GQA_BF16 or GQA_E4M3 pages run on the
- * tensor cores, the other pairs of types on the FP32 pipe.  Errors: as gqa_attn_cache_write, GQA_ERR_UNSUPPORTED
- * (d, Hq / Hkv, T > 1024), GQA_ERR_WORKSPACE.
+ * equal calls give equal bits.  GQA_BF16 queries over GQA_BF16 or GQA_E4M3 pages are
+ * multiplied as they are, the other pairs of types to fp32 accuracy (two tf32 pieces of each
+ * fp32 number): there an infinite key makes the rows that see it NaN, and an infinite value
+ * their column.  Errors: as gqa_attn_cache_write, GQA_ERR_UNSUPPORTED (d, Hq / Hkv, T > 1024,
+ * B Hq above 2^31 - 1), GQA_ERR_WORKSPACE.
  * gqa_attn_tree_workspace_bytes returns 0 for a shape that the call rejects.  Host-only.
  */
 size_t gqa_attn_tree_workspace_bytes(int B, int Hq, int Hkv, int64_t T, int64_t max_pages, int page_size, int d,

@@ -14,6 +14,9 @@ kernels.  PyTorch provides device memory and streams.
     dq, dk, dv = bwd(q, k, v, out, lse, dout)                # gradients from the saved LSE
     out = attention(q, k, v)                                 # differentiable (autograd: fwd + bwd)
 
+Decoding (modules ``rotary`` and ``cache``): rotary positions, a paged key/value cache in
+fp32, bf16 or e4m3, written and read back, and attention of one or more drafted tokens over it.
+
 q: [B, Hq, Lq, 256], k/v: [B, Hkv, Lk, 256], fp32 or bf16, contiguous CUDA
 tensors; Lk = q_pos_offset + Lq.  Returns out (dtype of q) and lse (fp32).
 """

@@ -77,7 +77,7 @@ int check_tree(int B, int Hq, int Hkv, int64_t T, int64_t max_pages, int page_si
     return GQA_ERR_INVALID_ARG;
   if (!page_size_ok(page_size) || !float_dtype(dtype)) return GQA_ERR_INVALID_ARG;
   if (cache_dtype != GQA_F32 && cache_dtype != GQA_BF16 && cache_dtype != GQA_E4M3) return GQA_ERR_INVALID_ARG;
-  if (d != kHeadDim || T > 1024) return GQA_ERR_UNSUPPORTED;
+  if (d != kHeadDim || T > 1024 || int64_t(B) * Hq > 0x7fffffff) return GQA_ERR_UNSUPPORTED;
   const int G = Hq / Hkv;
   if (G != 1 && G != 2 && G != 4 && G != 8 && G != 16) return GQA_ERR_UNSUPPORTED;
   return GQA_OK;

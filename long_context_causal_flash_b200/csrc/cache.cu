@@ -5,6 +5,11 @@
 // largest |x| first, which those threads find by four shuffles; the row never leaves the
 // registers between the read, the rotation and the store of its codes, so both kernels
 // move each byte once and are bound by memory (for a few tokens, by the launch).
+// 30,468 tokens of 4 heads written as e4m3, keys rotated (187 MB): 45 us, 29 for the bytes; a
+// row's conversions and shuffles keep the writer's warps busier than the reader's, for which
+// 45,000 tokens read back to bf16 (254 MB) take 44 us, 39 for the bytes.  Loads stay raw until
+// they are used, so that four rows of a half-warp are in flight in 80 registers (55 and 49 us
+// with one row).
 #include <type_traits>
 
 #include "decode.cuh"

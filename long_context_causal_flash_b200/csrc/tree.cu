@@ -114,8 +114,8 @@ TreeShape tree_shape(int B, int Hkv, int G, int64_t T, int64_t max_pages, int pa
   const int slots = kB200Sms;
   s.workers = slots / s.row_tiles > 1 ? slots / s.row_tiles : 1;
   // No more workers than tiles that the page tables could hold.
-  const int64_t tiles = ((max_pages * page_size - 1 >> s.tile_shift) + 1) * B * Hkv;
-  if (tiles < s.workers) s.workers = int(tiles);
+  const int64_t per_head = ((max_pages * page_size - 1) >> s.tile_shift) + 1, heads = int64_t(B) * Hkv;
+  if (per_head < s.workers && heads * per_head < s.workers) s.workers = int(heads * per_head);
   return s;
 }
 

@@ -1,8 +1,8 @@
 // The work split of the drafted-token attention: which tiles of which sequence and
 // key/value head a worker takes, and where its partial results go.
 //
-// Lengths are known to the device only, and differ between sequences.  All tiles of 128
-// keys are therefore put into one list, ordered by (sequence, key/value head, tile), and
+// Lengths are known to the device only, and differ between sequences.  All tiles of 128 (for
+// fp32 accuracy 32) keys are therefore put into one list, ordered by (sequence, key/value head, tile), and
 // worker w of n takes the items [w W / n, (w + 1) W / n): every worker streams the same
 // number of keys, to one tile.  A worker's range falls into segments, one per (sequence,
 // head) it touches.  A segment that holds all of a head's tiles writes the output; any

@@ -21,7 +21,7 @@
 // filled by two warps that have no rows of the softmax, a box per page: a copy of 1 KiB per
 // row costs its warp 95 cycles, 3,000 a step.
 //
-// 5 tokens of 4 heads to a key/value head, 2 x 15,231 fp32 keys, 249 MB: 112 us, of which
+// 5 tokens of 4 heads to a key/value head, 2 x 15,231 fp32 keys, 249 MB: 111 us, of which
 // memory alone takes 38.  A step of 24 rows takes 6,300 cycles, 2,300 of them the tensor
 // cores' (8 cycles of a scheduler per instruction, 288 of them): S 1,650, softmax 900 and O
 // 1,950 come one after another, barriers and waits 900.  Tried: the O before the softmax in

@@ -13,6 +13,18 @@
 //
 // Warps: 16 for the softmax (lane quarter x 32 keys), two producers (bf16: keys and values; e4m3,
 // with half the bytes: one for both, and one that fetches the keys' scales), two issuers.
+//
+// Pairs (bf16 pages, an even number of row tiles): the CTAs of two row tiles, which sweep the
+// same keys, issue products of M = 256 together (cta_group::2), and each loads 64 of a tile's keys
+// and half of its values' columns.  A CTA by itself has room for 1.25 tiles of keys and of
+// values, and a tile comes 3,500 cycles after its slot is free, so it takes 3,800 cycles a tile;
+// the pair takes 2,850.  64 tokens of 4 heads, 4 sequences of
+// 30,468 bf16 keys (500 MB, 128 GFLOP): 132 us in short runs, 155 - 160 in long ones, whose
+// clock falls (unpaired: 176); 77 for the bytes, as much for the flops.  e4m3 stays
+// single: there the softmax is the bound, 3,700 cycles a tile (128 x 128 exponentials
+// and their conversions to two pieces), not the loads.  24 tokens of 4 heads over 8 e4m3 sequences of up
+// to 15,231 keys (159 MB): 76 us against 24.5; 11 pass before the first softmax, 5 per head begun
+// and 4.5 per head written (128 rows of fp32 from every SM at once), 10 in the merge.
 #include "tree_tc.cuh"
 
 namespace gqa {

@@ -23,8 +23,12 @@
 // to 2^-8 of the first maximum, and is off by at most 2^-14 of it below.
 //
 // Warps: 4 softmax warps per 32 (or 16) rows, a producer each for keys and values (TMA,
-// through the page table, into rings of 16 KiB slots), and two warps whose first lanes issue
-// the products.
+// through the page table, into rings of 16 KiB slots), and two warps that issue the products.
+//
+// One token of 4 heads, 60,926 bf16 keys (249 MB): 48 us, 38 for the bytes alone; the kernel
+// itself 47 of which 4.5 pass before the first scores and 3.5 behind the last.  32 sequences of up
+// to 8,192 e4m3 keys (313 MB): 70 us against 48; a tile takes 2,100 cycles where memory allows it
+// (the softmax's 128 threads), and each head begun costs 4 us (Q, an empty pipeline, the output).
 #include "tree_tc.cuh"
 
 namespace gqa {
@@ -169,7 +173,7 @@ __global__ void __launch_bounds__(Cfg<kN, kFp8>::kThreads, 1) tree_tc_kernel(con
     produce(p, feed, none);
   } else if (warp >= F::kIssuer) {
     // ---------------------------------------------------------------- MMA issuers
-    // One thread issues every S^T = K Q^T, another every O^T += V^T P^T, so that neither
+    // One warp issues every S^T = K Q^T, another every O^T += V^T P^T, so that neither
     // waits for the other's tiles to arrive.
     {
       const bool is_s = warp == F::kIssuer;

@@ -208,3 +208,14 @@ def test_host_tensors_are_refused():
     with pytest.raises(ValueError):
         cache.PagedCache(torch.zeros(2, 4, 16, 256, dtype=torch.float16), torch.zeros(2, 4, 16, 256,
                                                                                       dtype=torch.float16))
+
+
+def test_workspace_of_the_largest_shapes(lib):
+    """Sizes that pass 32 bits on the way: counted, or refused."""
+    size = lib.gqa_attn_tree_workspace_bytes
+    for code in (_lib.GQA_F32, _lib.GQA_BF16):
+        assert 0 < size(1, 16, 4, 1, 0x7fffffff, 1024, 256, code, code) < 1 << 26
+        assert 0 < size(1 << 20, 1 << 10, 1 << 6, 1024, 0x7fffffff, 1024, 256, code, code) < 1 << 28
+        assert size(1 << 24, 1 << 8, 1 << 4, 1, 10, 64, 256, code, code) == 0
+        # a page table of one page: no more workers than tiles
+        assert size(1, 4, 4, 1, 1, 8, 256, code, code) <= 4 * 2 * 16 * (1024 + 4) + 256

@@ -1,11 +1,11 @@
 """Rotary positions on the GPU against the float64 definition.
 
 Tolerances, in units of e = 2^-24 (half a step of fp32) times m (|x1| + |x2|), the size of
-the terms: the angle as an fp32 number of half turns in [-1, 1] is off by at most e / 2, so
-by pi e / 2 < 1.6 e in radians, plus 2^-31 pi < 0.03 e for the bits cut off; sincospi is
-within 2 e of its exact value (two steps below 1); the product with m, the product with x
-and the sum round once each, 1 e apiece.  7 e in all, 8 e taken.  bf16 outputs add half
-a step, 2^-8 of the value.
+the terms: the angle within a quarter turn, at most pi / 4, is rounded to fp32 and multiplied by
+a rounded constant, off by at most 3 pi e / 4 < 2.4 e, plus 2^-31 pi < 0.03 e for the bits cut
+off; the series leave out less than 0.03 e and round by half a step of their result, 0.5 e, and
+less than 0.5 e before; the product with m, the product with x and the sum round once each, 1 e
+apiece.  6.5 e in all, 8 e taken.  bf16 outputs add half a step, 2^-8 of the value.
 """
 
 import numpy as np
