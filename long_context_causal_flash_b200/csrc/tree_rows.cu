@@ -131,7 +131,7 @@ __global__ void __launch_bounds__(RowsCfg<kFp8>::kThreads, 1) tree_rows_kernel(c
     const TreeCursor c = tree_start(p, worker);
     if (lane == 0) {
       start = c;
-      mbar_init(bar(kRBarQ), kPair ? 2 * kSoftWarps : kSoftWarps);
+      mbar_init(bar(kRBarQ), kPair ? 2 : kSoftWarps);
       for (int i = 0; i < 2; ++i) {
         mbar_init(bar(kRBarS + i), 1);
         mbar_init(bar(kRBarP + i), kPair ? 2 * kSoftWarps : kSoftWarps);
@@ -272,10 +272,14 @@ __global__ void __launch_bounds__(RowsCfg<kFp8>::kThreads, 1) tree_rows_kernel(c
           float* sc = sh_scale + b * 384;
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
-            const float v = v_now[i] == 0.f ? 7.8886090522101181e-31f : v_now[i];  // 2^-100
             sc[i * 32 + lane] = k_now[i];
-            sc[128 + i * 32 + lane] = log2f(v);
-            sc[256 + i * 32 + lane] = 1.f / v;
+            sc[128 + i * 32 + lane] = v_now[i] == 0.f ? 7.8886090522101181e-31f : v_now[i];  // 2^-100
+          }
+#pragma unroll 1
+          for (int i = 128; i < 256; i += 32) {  // one key's code, as with Q
+            const float v = sc[i + lane];
+            sc[i + lane] = log2f(v);
+            sc[128 + i + lane] = 1.f / v;
           }
         }
         if (lane < 4) sh_there[b * 4 + lane] = lane == 0 ? there[0] : lane == 1 ? there[1] : lane == 2 ? there[2] : there[3];
@@ -297,7 +301,6 @@ __global__ void __launch_bounds__(RowsCfg<kFp8>::kThreads, 1) tree_rows_kernel(c
       bool ok = true;
       while (ok && tree_next(p, cur, &g)) {
         if (is_s && !(ok = warp_wait(bar(kRBarQ), segs & 1u, budget, status))) break;
-        if constexpr (kPair) fence_cluster();  // the odd CTA's Q is behind that word
         ++segs;
         for (int tile = g.t0; ok && tile < g.t1; ++tile, ++tt) {
           const uint32_t b = tt & 1u, ph = (tt >> 1) & 1u;
@@ -416,26 +419,27 @@ __global__ void __launch_bounds__(RowsCfg<kFp8>::kThreads, 1) tree_rows_kernel(c
           u[i] = *reinterpret_cast<const uint4*>(reinterpret_cast<const __nv_bfloat16*>(p.q.p) + g.b * p.q.sb +
                                                  int64_t(g.h * p.G + (n & (p.G - 1))) * p.q.sh + tq * p.q.sl + 8 * lane);
       }
-#pragma unroll
-      for (int i = 0; i < kQRows; ++i) {
-        const int rq = warp + i * kSoftWarps;
+      // (The code of one row: it is run from a cold instruction cache, eight rows' in 10,000 cycles.)
+#pragma unroll 1
+      for (int rq = warp; rq < kRows; rq += kSoftWarps) {
         if constexpr (!kFp8) {
-          sts16(sQ + uint32_t(lane >> 3) * (kRows * 128u) + uint32_t(rq) * 128u + uint32_t(((lane & 7) ^ (rq & 7)) << 4), u[i]);
+          sts16(sQ + uint32_t(lane >> 3) * (kRows * 128u) + uint32_t(rq) * 128u + uint32_t(((lane & 7) ^ (rq & 7)) << 4), u[0]);
         } else {
-          const float f = put_query<kRows, false>(u[i], sQ, rq);
+          const float f = put_query<kRows, false>(u[0], sQ, rq);
           if (lane == 0) sh_f[rq] = f * p.scale_log2;
         }
+#pragma unroll
+        for (int i = 1; i < kQRows; ++i) u[i - 1] = u[i];
       }
       if (warp == 0) sh_bad[lane] = 0;
       fence_proxy_async_smem();
       __syncwarp();
-      if (lane == 0) {
-        if constexpr (kPair)
-          arrive_release_cluster(lead(kRBarQ));
-        else
-          mbar_arrive(bar(kRBarQ));
-      }
+      if (!kPair && lane == 0) mbar_arrive(bar(kRBarQ));
       sync_threads(15, kAll);  // sh_f and sh_bad are other warps' too
+      // The odd CTA's Q is read by its own tensor core: its writes are over (the barrier) and visible
+      // there (the proxy fence of each writer).  The word to the even CTA is a plain arrival, as
+      // with P; a release at cluster scope takes 5,000 cycles.
+      if (kPair && threadIdx.x == 0) mbar_arrive_remote(lead(kRBarQ));
       const float factor = kFp8 ? sh_f[r] : p.scale_log2;
       const bool live = t < g.s.drafted;
 

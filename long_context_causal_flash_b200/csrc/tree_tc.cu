@@ -292,15 +292,17 @@ __global__ void __launch_bounds__(Cfg<kN, kFp8>::kThreads, 1) tree_tc_kernel(con
 
     while (ok && more) {
       const int32_t* table = p.table + int64_t(g.b) * p.max_pages;
-#pragma unroll
-      for (int i = 0; i < kQRows; ++i) {
-        const int r = warp + i * F::kSoftWarps;
+      // (The code of one row: it is run from a cold instruction cache.)
+#pragma unroll 1
+      for (int r = warp; r < kN; r += F::kSoftWarps) {
         if constexpr (!kFp8) {
-          sts16(sQ + uint32_t(lane >> 3) * (kN * 128u) + uint32_t(r) * 128u + uint32_t(((lane & 7) ^ (r & 7)) << 4), u[i]);
+          sts16(sQ + uint32_t(lane >> 3) * (kN * 128u) + uint32_t(r) * 128u + uint32_t(((lane & 7) ^ (r & 7)) << 4), u[0]);
         } else {
-          const float f = put_query<kN, true>(u[i], sQ, r);
+          const float f = put_query<kN, true>(u[0], sQ, r);
           if (lane == 0) sh_f[r] = f * p.scale_log2;
         }
+#pragma unroll
+        for (int i = 1; i < kQRows; ++i) u[i - 1] = u[i];
       }
       if (quarter == 0 && lane < C) sh_m[n0 + lane] = 0.f;
       if (warp == 0) sh_bad[lane] = 0;
