@@ -23,7 +23,7 @@
 // clock falls (unpaired: 176); 77 for the bytes, as much for the flops.  e4m3 stays
 // single: there the softmax is the bound, 3,700 cycles a tile (128 x 128 exponentials
 // and their conversions to two pieces), not the loads.  24 tokens of 4 heads over 8 e4m3 sequences of up
-// to 15,231 keys (159 MB): 76 us against 24.5; 11 pass before the first softmax, 5 per head begun
+// to 15,231 keys (159 MB): 73 us against 24.5; 11 pass before the first softmax, 5 per head begun
 // and 4.5 per head written (128 rows of fp32 from every SM at once), 10 in the merge.
 #include "tree_tc.cuh"
 

@@ -495,3 +495,52 @@ def test_many_rows_over_long_contexts(cuda_device, kind):
     for _ in range(3):
         graph.replay()
     assert torch.equal(out, first) and torch.equal(l2, lse)
+
+
+def test_calls_of_all_kinds_in_a_row(cuda_device):
+    """Calls of every kernel behind one another on one stream, sharing a workspace (each may start
+    while the one before ends), the same on two streams at once, and captured as one graph of
+    two branches: the same bits as alone."""
+    kinds = [(F32, F32, 5), (BF16, BF16, 1), (BF16, BF16, 40), (BF16, E4M3, 40), (BF16, E4M3, 3), (F32, BF16, 1),
+             (BF16, BF16, 12), (BF16, F32, 2), (BF16, BF16, 20)]
+    problems = [Problem(cuda_device, 2, 16, 4, T, [1500, 37], 32, dtype, kind, seed=70 + i)
+                for i, (dtype, kind, T) in enumerate(kinds)]
+    qs = [p.q.to(cuda_device) for p in problems]
+    size = max(cache.workspace_bytes(2, 16, p.q.shape[2], p.pool, p.table.shape[1], p.q.dtype) for p in problems)
+
+    def call(i, ws=None, **kw):
+        p = problems[i]
+        return cache.attend(qs[i], p.pool, p.table, p.ctx_dev, workspace=ws, **kw)
+
+    want = []
+    for i in range(len(kinds)):
+        want.append(call(i))
+        torch.cuda.synchronize()
+
+    def same(got):
+        torch.cuda.synchronize()
+        for i, (out, lse) in got:
+            assert torch.equal(out, want[i][0]) and torch.equal(lse, want[i][1]), f"call {i}"
+
+    order = [i for r in range(4) for i in np.random.default_rng(r).permutation(len(kinds))]
+    ws = [torch.empty(size, dtype=torch.uint8, device=cuda_device) for _ in range(2)]
+    same([(i, call(i, ws[0])) for i in order])
+
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    for s in streams:
+        s.wait_stream(torch.cuda.current_stream())
+    same([(i, call(i, ws[k], stream=streams[k])) for i in order for k in range(2)])
+
+    graph, side = torch.cuda.CUDAGraph(), torch.cuda.Stream()
+    with torch.cuda.graph(graph):
+        fork = torch.cuda.current_stream()
+        side.wait_stream(fork)
+        got = [(i, call(i, ws[0])) for i in order[:9]]
+        with torch.cuda.stream(side):
+            got += [(i, call(i, ws[1])) for i in order[9:18]]
+        fork.wait_stream(side)
+    for _ in range(3):
+        for _, (out, _) in got:
+            out.zero_()
+        graph.replay()
+        same(got)
