@@ -9,7 +9,7 @@
 // row's conversions and shuffles keep the writer's warps busier than the reader's, for which
 // 45,000 tokens read back to bf16 (254 MB) take 44 us, 39 for the bytes.  Loads stay raw until
 // they are used, so that four rows of a half-warp are in flight in 80 registers (55 and 49 us
-// with one row).
+// with one row; 47 in 64 registers, which spill, with four CTAs on an SM instead of three).
 #include <type_traits>
 
 #include "decode.cuh"
