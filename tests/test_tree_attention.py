@@ -544,3 +544,31 @@ def test_calls_of_all_kinds_in_a_row(cuda_device):
             out.zero_()
         graph.replay()
         same(got)
+
+
+@pytest.mark.parametrize("dtype,kind,T", [(BF16, BF16, 1), (BF16, BF16, 40), (BF16, E4M3, 40), (F32, F32, 5)])
+def test_captured_behind_copies_and_joined_streams(cuda_device, dtype, kind, T):
+    """In a graph: behind a copy of the lengths, behind a cleared output, and behind two streams
+    that join; the lengths change between replays."""
+    p = Problem(cuda_device, 2, 16, 4, T, [1500, 37], 32, dtype, kind, seed=90 + T)
+    q, ctx, source = p.q.to(cuda_device), p.ctx_dev.clone(), p.ctx_dev.clone()
+    out = [torch.empty_like(q) for _ in range(3)]
+    side, graph = torch.cuda.Stream(), torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        main = torch.cuda.current_stream()
+        ctx.copy_(source)
+        cache.attend(q, p.pool, p.table, ctx, out=out[0])
+        side.wait_stream(main)
+        with torch.cuda.stream(side):
+            out[1].zero_()
+            cache.attend(q, p.pool, p.table, ctx, out=out[1])
+        out[2].zero_()
+        main.wait_stream(side)
+        cache.attend(q, p.pool, p.table, ctx, out=out[2])
+    for lens in ([1500, 37], [200, 30], [0, 1]):
+        source.copy_(torch.tensor(lens, dtype=torch.int32))
+        graph.replay()
+        want, _ = cache.attend(q, p.pool, p.table, source)
+        torch.cuda.synchronize()
+        for o in out:
+            assert torch.equal(o, want)
