@@ -244,14 +244,16 @@ __global__ void __launch_bounds__(RowsCfg<kFp8>::kThreads, 1) tree_rows_kernel(c
         checked(tile + 1, entry_next);
         scales_at(tile + 1);
         entries_at(tile + 2, entry_next);
-        // The softmax has read what the buffer held for tile t - 2.
-        if (tt >= 2) ok = warp_wait(bar(kRBarP + int(b)), ((tt - 2) >> 1) & 1u, budget, status);
+        // Product t - 2 is over, so the softmax has read what the buffer held for that tile.  This is
+        // waited for with every tile, before its scales are given: the product barrier's next phase
+        // needs them, so no phase can pass that this warp has not seen (a wait for the phase before
+        // last would last until the phase after next, which waits for this warp).  S(t) waits for the
+        // same product, so it costs the softmax nothing.
+        if (tt >= 2) ok = warp_wait(bar(kRBarPV + int(b)), ((tt - 2) >> 1) & 1u, budget, status);
         {
           // A row of zeros (written with scale 1): see tree_tc.cu.
           if (__any_sync(0xffffffffu, one)) {
-            // The product before is over first, so that the slot's barrier stands at no earlier use;
-            // and the one two before that, which the same barrier counts.
-            if (tt >= 3) ok = warp_wait(bar(kRBarPV + int((tt - 3) & 1u)), ((tt - 3) >> 1) & 1u, budget, status) && ok;
+            // The product before is over first, so that the slot's barrier stands at no earlier use.
             if (tt > 0) ok = warp_wait(bar(kRBarPV + int((tt - 1) & 1u)), ((tt - 1) >> 1) & 1u, budget, status) && ok;
 #pragma unroll
             for (int i = 0; i < 4; ++i) {

@@ -572,3 +572,20 @@ def test_captured_behind_copies_and_joined_streams(cuda_device, dtype, kind, T):
         torch.cuda.synchronize()
         for o in out:
             assert torch.equal(o, want)
+
+
+@pytest.mark.parametrize("T", [1, 12, 24, 64])
+def test_scales_of_one_throughout(cuda_device, T):
+    """A pool quantised with the scale 1 for every value: any row may then be one of zeros, so the
+    kernels look at each of them, tile after tile, over many rounds of the rings.  Equal calls
+    give equal bits and no wait runs out."""
+    p = Problem(cuda_device, 2, 16, 4, T, [9000, 4100], 32, BF16, E4M3, seed=110 + T)
+    codes = p.pool.v.float().cpu()[p.table.cpu().long()].transpose(1, 2).flatten(2, 3)  # up to 448 each
+    p.v = codes[:, :, : p.v.shape[2]].nan_to_num(0.0)  # (behind a sequence's end the pages hold NaN)
+    p.pool.v_scale.fill_(1.0)
+    first, lse = p.attend()
+    p.check(first, lse)
+    for _ in range(20):
+        out, again = p.attend()
+        assert torch.equal(out, first) and torch.equal(again, lse)
+    assert cache.status(p.pool) == 0
