@@ -566,10 +566,16 @@ int gqa_attn_cache_read(const gqa_cache_t *cache, const int32_t *page_table, int
  *                 overwritten; calls that share one must be ordered on one stream.
  * What a row's mask hides does not reach the row, NaN and infinities among it.  Work is cut
  * evenly over the SMs whatever the lengths; partial results are merged in a fixed order, so
- * equal calls give equal bits.  GQA_BF16 queries over GQA_BF16 or GQA_E4M3 pages are
- * multiplied as they are, the other pairs of types to fp32 accuracy (two tf32 pieces of each
- * fp32 number): there an infinite key makes the rows that see it NaN, and an infinite value
- * their column.  Errors: as gqa_attn_cache_write, GQA_ERR_UNSUPPORTED (d, Hq / Hkv, T > 1024,
+ * equal calls give equal bits.
+ * Accuracy.  Sums, maxima and the log-sum-exp are fp32.  GQA_BF16 queries over GQA_BF16 pages:
+ * products of the numbers as they are; a probability is rounded to bf16 (2^-9 of itself) before it
+ * is multiplied with its value, as in gqa_attn_fwd.  Over GQA_E4M3 pages: products of the codes as they
+ * are; a query is off by 2^-10 after its row is scaled to at most 448, and a probability by
+ * 2^-8.8 of itself down to 2^-20 of the largest p x scale that the row sees, and by 2^-28 of that
+ * below, so many small ones keep what they hold together (2^-10 of the output at most for 2^18 keys).
+ * The other pairs of types are multiplied to fp32 accuracy (two tf32 pieces of each fp32 number):
+ * there an infinite key makes the rows that see it NaN, and an infinite value their column.
+ * Errors: as gqa_attn_cache_write, GQA_ERR_UNSUPPORTED (d, Hq / Hkv, T > 1024,
  * B Hq above 2^31 - 1), GQA_ERR_WORKSPACE.
  * gqa_attn_tree_workspace_bytes returns 0 for a shape that the call rejects.  Host-only.
  */

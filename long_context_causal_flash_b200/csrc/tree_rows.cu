@@ -5,8 +5,8 @@
 // step measured 140 cycles against 97 for S and 136 for twice the work of O here).
 //
 // S = Q K^T (M = rows, N = 128 keys) and O += P V (P in TMEM, N = 256 columns).  TMEM: O in
-// columns 0 .. 255, two S buffers of 128; P(t) takes the place of the first 64 columns of
-// S(t): bf16 pairs, or both e4m3 pieces of 32 columns each.  Softmax: one thread per row and
+// columns 0 .. 255, two S buffers of 128; P(t) takes the place of the first columns of
+// S(t): 64 of bf16 pairs, or 32 for each of three e5m2 pieces.  Softmax: one thread per row and
 // 32 keys, so that maxima and sums are the thread's own, joined over four warps through
 // shared memory only when a maximum rises.  e4m3 pages, their scales, the pieces of queries
 // and probabilities, lazy maxima and values that a mask hides: as in tree_tc.cu.
@@ -22,7 +22,7 @@
 // 30,468 bf16 keys (500 MB, 128 GFLOP): 132 us in short runs, 155 - 160 in long ones, whose
 // clock falls (unpaired: 176); 77 for the bytes, as much for the flops.  e4m3 stays
 // single: there the softmax is the bound, 3,700 cycles a tile (128 x 128 exponentials
-// and their conversions to two pieces), not the loads.  24 tokens of 4 heads over 8 e4m3 sequences of up
+// and their conversions to pieces), not the loads.  24 tokens of 4 heads over 8 e4m3 sequences of up
 // to 15,231 keys (159 MB): 73 us against 24.5; 11 pass before the first softmax, 5 per head begun
 // and 4.5 per head written (128 rows of fp32 from every SM at once), 10 in the merge.
 #include "tree_tc.cuh"
@@ -68,10 +68,10 @@ enum {
   kRBarRelay = 30  // to the odd CTA of a pair, per part: its values are there
 };
 
-// Eight consecutive 32-bit columns of raw words into this thread's TMEM lane.
-__device__ __forceinline__ void tmem_st8u(uint32_t taddr, const uint32_t (&r)[8]) {
-  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(taddr), "r"(r[0]), "r"(r[1]),
-               "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+// Four consecutive 32-bit columns of raw words into this thread's TMEM lane.
+__device__ __forceinline__ void tmem_st4u(uint32_t taddr, const uint32_t (&r)[4]) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x4.b32 [%0], {%1,%2,%3,%4};" ::"r"(taddr), "r"(r[0]), "r"(r[1]), "r"(r[2]),
+               "r"(r[3])
                : "memory");
 }
 
@@ -296,7 +296,7 @@ __global__ void __launch_bounds__(RowsCfg<kFp8>::kThreads, 1) tree_rows_kernel(c
     if (!kPair || rank == 0) {
       const bool is_s = warp == F::kIssuer;
       constexpr uint32_t kM = kPair ? 8u << 24 : 0;  // M = 256 instead of 128
-      constexpr uint32_t id_s = idesc<kFp8>(128, 0, 0) + kM, id_o = idesc<kFp8>(256, 0, 1) + kM;
+      constexpr uint32_t id_s = idesc<kFp8>(128, 0, 0) + kM, id_o = idesc<kFp8>(256, 0, 1, kFp8) + kM;
       const uint64_t dq = umma::smem_desc(sQ, 16, 1024);
       const uint32_t high = uint32_t(dq >> 32);
       uint32_t tt = 0, segs = 0;  // tiles issued
@@ -361,7 +361,7 @@ __global__ void __launch_bounds__(RowsCfg<kFp8>::kThreads, 1) tree_rows_kernel(c
 #pragma unroll
                 for (uint32_t k = 0; k < 2; ++k)
 #pragma unroll
-                  for (uint32_t piece = 0; piece < (kFp8 ? 2 : 1); ++piece)
+                  for (uint32_t piece = 0; piece < (kFp8 ? 3 : 1); ++piece)
                     mma_ts<kFp8>(tmem, sbuf + 32u * piece + 8u * (2 * i + k), desc_low(dv, k * I::kStep), high, id_o,
                                  tile > g.t0 || (i | k | piece) != 0);
               }
@@ -601,25 +601,25 @@ __global__ void __launch_bounds__(RowsCfg<kFp8>::kThreads, 1) tree_rows_kernel(c
         }
         // P and the row's sum.
         if constexpr (kFp8) {
-          uint32_t hi[8], lo[8];
 #pragma unroll
-          for (int i = 0; i < 32; i += 4) {
-            const float4 inv = *reinterpret_cast<const float4*>(scale + 256 + i);
-            float e[4], h[4];
+          for (int i0 = 0; i0 < 32; i0 += 16) {
+            uint32_t hi[4], mid[4], lo[4];
 #pragma unroll
-            for (int k = 0; k < 4; ++k) e[k] = ex2(x[i + k] - m);
-            l = fmaf(e[0], inv.x, fmaf(e[1], inv.y, fmaf(e[2], inv.z, fmaf(e[3], inv.w, l))));
+            for (int i = i0; i < i0 + 16; i += 4) {
+              const float4 inv = *reinterpret_cast<const float4*>(scale + 256 + i);
+              float e[4];
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
-              e[k] *= kPScale;
-              h[k] = __uint_as_float(__float_as_uint(e[k]) & 0xfff00000u);  // three mantissa bits
-              e[k] -= h[k];
+              for (int k = 0; k < 4; ++k) e[k] = ex2(x[i + k] - m);
+              l = fmaf(e[0], inv.x, fmaf(e[1], inv.y, fmaf(e[2], inv.z, fmaf(e[3], inv.w, l))));
+#pragma unroll
+              for (int k = 0; k < 4; ++k) e[k] *= kPScale;
+              e5m2_pieces4(e, hi[(i - i0) / 4], mid[(i - i0) / 4], lo[(i - i0) / 4]);
             }
-            hi[i / 4] = e4m3_encode4(h);
-            lo[i / 4] = e4m3_encode4(e);
+            const uint32_t to = lane_addr + 256u + sb * 128u + uint32_t(part * 8 + i0 / 4);
+            tmem_st4u(to, hi);
+            tmem_st4u(to + 32u, mid);
+            tmem_st4u(to + 64u, lo);
           }
-          tmem_st8u(lane_addr + 256u + sb * 128u + uint32_t(part * 8), hi);
-          tmem_st8u(lane_addr + 256u + sb * 128u + 32u + uint32_t(part * 8), lo);
         } else {
           uint32_t pk[16];
           float sum[4] = {0.f, 0.f, 0.f, 0.f};

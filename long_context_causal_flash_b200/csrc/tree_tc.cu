@@ -4,23 +4,26 @@
 // Few query rows meet many keys, so the keys take the long side of every product: a tile
 // of 128 keys is the M of S^T = K Q^T (N = the query rows, 16 .. 64), and the 256 columns
 // of the values, in two halves, are the M of O^T += V^T P^T.  With the rows as M, 4 rows
-// would cost what 128 do (tree_rows.cu, for more rows).  TMEM, per CTA: two S^T buffers of N columns (lane = key) and the
-// two halves of O^T (lane = column of the output), 4 N columns in all.
+// would cost what 128 do (tree_rows.cu, for more rows).  TMEM, per CTA: two S^T buffers (lane = key) and the
+// two halves of O^T (lane = column of the output), N columns each, or as many times that as there are
+// pieces side by side.
 //
 // e4m3 pages are multiplied as they are (kind::f8f6f4, exact products in fp32): the query
 // is scaled by a power of two so that its largest element lies in (224, 448] and taken
-// apart into two e4m3 pieces, q = hi + lo, off by at most 2^-10 of that scale; so is each
-// probability.  The pieces lie side by side in N and their products are added afterwards.
+// apart into two e4m3 pieces, q = hi + lo, off by at most 2^-10 of that scale; a probability into
+// three e5m2 pieces (tree_tc.cuh), which keep the bits of a bf16 one over 20 powers of two.  The
+// pieces lie side by side in N and their products are added afterwards; of 64 rows there is room
+// for two beside one another, and the third is multiplied by itself into the first one's place.
 // The scales of a key go into its scores, those of a value into its probability, before
 // that is rounded.
 //
 // Softmax: one thread per key and up to 32 rows; the running maximum m of a row is raised
 // only when a score passes it by kSlack (in powers of two), so most tiles need no
 // reduction over the keys and no rescaling of O.  P = 2^(x - m) goes to shared memory as
-// the B operand; the row sum stays with the threads, in fp32, until the end.  For e4m3, x
+// the B operand, over bf16 pages rounded to bf16 (2^-9 of itself: the product then takes the pages as
+// they are, and one of N columns; a second piece would be as many again); the row sum stays with the threads, in fp32, until the end.  For e4m3, x
 // includes log2 of the value's scale, so that m follows the largest product p v rather
-// than the largest p, and P is stored as 16 P <= 256: a probability then keeps 8 bits down
-// to 2^-8 of the first maximum, and is off by at most 2^-14 of it below.
+// than the largest p, and P is stored as 2^11 P <= 2^15.
 //
 // Warps: 4 softmax warps per 32 (or 16) rows, a producer each for keys and values (TMA,
 // through the page table, into rings of 16 KiB slots), and two warps that issue the products.
@@ -39,10 +42,13 @@ struct Cfg {
   static constexpr int kCols = kN < 32 ? kN : 32;  // rows of a softmax thread
   static constexpr int kParts = kN / kCols;
   static constexpr int kSoftWarps = 4 * kParts;
-  static constexpr int kNN = kFp8 ? 2 * kN : kN;  // N of a product: e4m3 pieces lie side by side
-  static constexpr int kQBytes = kN * 512;        // bf16, or two e4m3 pieces
-  static constexpr int kPBytes = 16384;           // [128 keys][128 bytes]
-  static constexpr int kKSlots = kN > 32 ? 5 : 6, kVSlots = 6;  // what shared memory has room for
+  static constexpr int kNN = kFp8 ? 2 * kN : kN;  // N of S's products: the query's pieces lie side by side
+  static constexpr int kPieces = kFp8 ? 3 : 1;    // of a probability,
+  static constexpr int kSide = kFp8 && kN > 32 ? 2 : kPieces;  // of them side by side: a row of P has 128 bytes,
+  static constexpr int kNO = kSide * kN;                       // tensor memory 512 columns.  N of O's products
+  static constexpr int kQBytes = kN * 512;                     // bf16, or two e4m3 pieces
+  static constexpr int kPBytes = kSide < kPieces ? 32768 : 16384;  // [128 keys][128 bytes], a third piece behind them
+  static constexpr int kKSlots = kN > 32 ? 5 : 6, kVSlots = kSide < kPieces ? 5 : 6;  // what shared memory has room for
   static constexpr int kIssuer = kSoftWarps + 2;  // the S issuer's warp, after the producers; then the O issuer's
   static constexpr int kWarps = kIssuer + 2;
   static constexpr int kThreads = 32 * kWarps;
@@ -56,7 +62,10 @@ struct Cfg {
   static constexpr int kOffBad = kOffF + kN * 4;  // 32 words: drafted tokens with a value that is not finite
   static constexpr int kSmem = kOffBad + 128;
   static constexpr float kSlack = kFp8 ? 4.f : 8.f;
-  static constexpr uint32_t kTmem = 4 * kNN;
+  static constexpr uint32_t kOffO = 2 * kNN;  // O's columns, behind two buffers of S
+  static constexpr uint32_t kTmemCols = kOffO + 2 * kNO;
+  static constexpr uint32_t kTmem = kTmemCols <= 64 ? 64 : kTmemCols <= 128 ? 128 : kTmemCols <= 256 ? 256 : 512;
+  static_assert(kTmemCols <= 512, "tensor memory");
   static_assert(kSmem <= 232448 - 1024, "shared memory per block");
 };
 
@@ -177,7 +186,9 @@ __global__ void __launch_bounds__(Cfg<kN, kFp8>::kThreads, 1) tree_tc_kernel(con
     // waits for the other's tiles to arrive.
     {
       const bool is_s = warp == F::kIssuer;
-      constexpr uint32_t id_s = idesc<kFp8>(F::kNN, 0, 0), id_o = idesc<kFp8>(F::kNN, 1, 1);
+      constexpr uint32_t id_s = idesc<kFp8>(F::kNN, 0, 0), id_o = idesc<kFp8>(F::kNO, 1, 1, false, kFp8),
+                         id_third = idesc<kFp8>(kN, 1, 1, false, kFp8);
+      (void)id_third;
       const uint64_t dq = umma::smem_desc(sQ, 16, 1024), dp = umma::smem_desc(sP, 16384, 1024);
       const uint32_t high = uint32_t(dq >> 32);
       uint32_t tt = 0, segs = 0;  // tiles issued
@@ -221,9 +232,12 @@ __global__ void __launch_bounds__(Cfg<kN, kFp8>::kThreads, 1) tree_tc_kernel(con
                 for (uint32_t half = 0; half < 2; ++half) {
                   const uint64_t dv = umma::smem_desc(base + half * (kSlotBytes / 2), I::kVBlock, 1024);
 #pragma unroll
-                  for (uint32_t k = 0; k < 2; ++k)
-                    mma<kFp8>(tmem + (2 + half) * F::kNN, desc_low(dv, k * I::kStep), desc_low(dp, (2 * i + k) * I::kStep),
-                              high, id_o, tile > g.t0 || (i | k) != 0);
+                  for (uint32_t k = 0; k < 2; ++k) {
+                    const uint32_t o = tmem + F::kOffO + half * F::kNO, v = desc_low(dv, k * I::kStep);
+                    mma<kFp8>(o, v, desc_low(dp, (2 * i + k) * I::kStep), high, id_o, tile > g.t0 || (i | k) != 0);
+                    if constexpr (F::kSide < F::kPieces)
+                      mma<kFp8>(o, v, desc_low(dp, 16384u + (2 * i + k) * I::kStep), high, id_third, true);
+                  }
                 }
               }
               umma::commit(empty + 8u * slot);
@@ -258,8 +272,9 @@ __global__ void __launch_bounds__(Cfg<kN, kFp8>::kThreads, 1) tree_tc_kernel(con
     const uint32_t slot_mask = (1u << p.c.page_shift) - 1;
     // The 16-byte unit `i` of key k's P: eight or sixteen rows from n0 on, of a piece.
     auto p_unit = [&](int k, int i, int piece) {
-      const int un = (n0 + piece * kN) / (kFp8 ? 16 : 8) + i;
-      return sP + uint32_t(k) * 128u + uint32_t((un ^ (k & 7)) << 4);
+      const bool behind = piece >= F::kSide;
+      const int un = (n0 + (behind ? 0 : piece) * kN) / (kFp8 ? 16 : 8) + i;
+      return sP + (behind ? 16384u : 0u) + uint32_t(k) * 128u + uint32_t((un ^ (k & 7)) << 4);
     };
     // The quarters' exchange of one value for each of sixteen rows lies in the thread's own
     // columns of P, which no product reads then: row c0 + n's from quarter q is with lane n.
@@ -484,9 +499,9 @@ __global__ void __launch_bounds__(Cfg<kN, kFp8>::kThreads, 1) tree_tc_kernel(con
               }
               if (tile > g.t0) {
 #pragma unroll 1
-                for (int block = 0; block < (kFp8 ? 4 : 2); ++block) {  // halves of O, and pieces
+                for (int block = 0; block < 2 * F::kSide; ++block) {  // halves of O, and pieces
                   float o[16];
-                  const uint32_t a = lane_addr + uint32_t((2 + (block & 1)) * F::kNN + (block >> 1) * kN + c0);
+                  const uint32_t a = lane_addr + F::kOffO + uint32_t((block & 1) * F::kNO + (block >> 1) * kN + c0);
                   umma::tmem_ld16(a, o);
                   umma::tmem_wait_ld();
                   uint32_t w[16];
@@ -508,21 +523,18 @@ __global__ void __launch_bounds__(Cfg<kN, kFp8>::kThreads, 1) tree_tc_kernel(con
           }
           // The row sums, and P.  A wait that ran out here is agreed upon with the next tile.
           if (c0 == 0) ok = last_product() && ok;
-          uint32_t hi[kFp8 ? 4 : 8], lo[4];
-          (void)lo;
+          uint32_t hi[kFp8 ? 4 : 8], mid[4], lo[4];
+          (void)mid, (void)lo;
 #pragma unroll
           for (int i = 0; i < 16; i += 4) {
             if constexpr (kFp8) {
-              float e[4], h[4];
+              float e[4];
 #pragma unroll
               for (int k = 0; k < 4; ++k) {
                 l[c0 + i + k] = fmaf(x[i + k], inv_vs, l[c0 + i + k]);
                 e[k] = x[i + k] * kPScale;
-                h[k] = __uint_as_float(__float_as_uint(e[k]) & 0xfff00000u);  // three mantissa bits
-                e[k] -= h[k];
               }
-              hi[i / 4] = e4m3_encode4(h);
-              lo[i / 4] = e4m3_encode4(e);
+              e5m2_pieces4(e, hi[i / 4], mid[i / 4], lo[i / 4]);
             } else {
 #pragma unroll
               for (int k = 0; k < 4; ++k) l[c0 + i + k] += x[i + k];
@@ -532,7 +544,8 @@ __global__ void __launch_bounds__(Cfg<kN, kFp8>::kThreads, 1) tree_tc_kernel(con
           }
           if constexpr (kFp8) {
             sts16(p_unit(key, c0 / 16, 0), make_uint4(hi[0], hi[1], hi[2], hi[3]));
-            sts16(p_unit(key, c0 / 16, 1), make_uint4(lo[0], lo[1], lo[2], lo[3]));
+            sts16(p_unit(key, c0 / 16, 1), make_uint4(mid[0], mid[1], mid[2], mid[3]));
+            sts16(p_unit(key, c0 / 16, 2), make_uint4(lo[0], lo[1], lo[2], lo[3]));
           } else {
             sts16(p_unit(key, c0 / 8, 0), make_uint4(hi[0], hi[1], hi[2], hi[3]));
             sts16(p_unit(key, c0 / 8 + 1, 0), make_uint4(hi[4], hi[5], hi[6], hi[7]));
@@ -592,14 +605,16 @@ __global__ void __launch_bounds__(Cfg<kN, kFp8>::kThreads, 1) tree_tc_kernel(con
           float o[2][4];
 #pragma unroll
           for (int half = 0; half < 2; ++half) {
-            const uint32_t a = lane_addr + uint32_t((2 + half) * F::kNN + c0);
+            const uint32_t a = lane_addr + F::kOffO + uint32_t(half * F::kNO + c0);
             tmem_ld4(a, o[half]);
-            if constexpr (kFp8) {
-              float y[4];
-              tmem_ld4(a + kN, y);
+            if constexpr (kFp8) {  // the pieces worth least first
+              float y[F::kSide - 1][4];
+#pragma unroll
+              for (int piece = 1; piece < F::kSide; ++piece) tmem_ld4(a + piece * kN, y[piece - 1]);
               umma::tmem_wait_ld();
 #pragma unroll
-              for (int i = 0; i < 4; ++i) o[half][i] += y[i];
+              for (int i = 0; i < 4; ++i)
+                o[half][i] += F::kSide > 2 ? y[0][i] + y[F::kSide - 2][i] : y[0][i];
             }
           }
           umma::tmem_wait_ld();

@@ -1,6 +1,6 @@
 // What the two tensor-core kernels of the drafted-token attention share: barriers, copies,
-// products in the type of the pages, the query's two e4m3 pieces and the values that a
-// mask hides.
+// products in the type of the pages, the pieces of queries and probabilities and the values
+// that a mask hides.
 #pragma once
 
 #include "internal.h"
@@ -16,7 +16,7 @@ namespace {
 // keys were two slots of a ring that held no more, and each product waited for a load that
 // could start only when the one before it was over (128 rows, bf16: 5,900 cycles a tile).
 constexpr int kSlotBytes = 16384;
-constexpr float kPScale = 16.f;  // e4m3 probabilities are stored times this: 2^4 above the maximum is 256
+constexpr float kPScale = 2048.f;  // over e4m3 pages probabilities are stored times this: 2^4 above the maximum is 2^15
 template <bool kFp8>
 struct Items {
   static constexpr int kTile = kFp8 ? 2 : 4;              // slots of a tile's keys, and of its values
@@ -114,12 +114,34 @@ __device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint32_t b, uint3
         "r"(a), "r"(b), "r"(high), "r"(idesc), "r"(uint32_t(add)));
 }
 
-// Instruction descriptor: fp32 accumulator, M = 128; e4m3 is format 0 of kind::f8f6f4, bf16
-// format 1 of kind::f16.
+// Instruction descriptor: fp32 accumulator, M = 128; e4m3 and e5m2 are formats 0 and 1 of
+// kind::f8f6f4, whose operands may differ in theirs, bf16 is format 1 of kind::f16.
 template <bool kFp8>
-__host__ __device__ constexpr uint32_t idesc(int N, int a_mn, int b_mn) {
-  return (1u << 4) | (kFp8 ? 0u : (1u << 7) | (1u << 10)) | (uint32_t(a_mn) << 15) | (uint32_t(b_mn) << 16) |
-         (uint32_t(N >> 3) << 17) | (8u << 24);
+__host__ __device__ constexpr uint32_t idesc(int N, int a_mn, int b_mn, bool a_e5m2 = false, bool b_e5m2 = false) {
+  return (1u << 4) | (!kFp8 || a_e5m2 ? 1u << 7 : 0u) | (!kFp8 || b_e5m2 ? 1u << 10 : 0u) | (uint32_t(a_mn) << 15) |
+         (uint32_t(b_mn) << 16) | (uint32_t(N >> 3) << 17) | (8u << 24);
+}
+
+// Four probabilities (times kPScale, at most 2^15) in three e5m2 pieces each, the piece that is
+// worth most first.  The upper byte of an fp16 number is an e5m2 one: the number cut to three
+// bits.  Two cuts, whose rests are exact, and a rounding keep nine of fp16's eleven bits, off by
+// 2^-8.8 of the number at most down to 2^-9, and by 2^-17 below it: 2^-20 and 2^-28 of the
+// largest probability.  So what many small ones hold beside a large one is kept.  (Two e4m3
+// pieces have as many bits, but a smallest step of 2^-9: with room for 2^4 above the largest they
+// lost all below 2^-14 of it, a fifth of the output where one of 32,768 keys had half of the weight.)
+__device__ __forceinline__ void e5m2_pieces4(const float* e, uint32_t& hi, uint32_t& mid, uint32_t& lo) {
+  __half2 a = __floats2half2_rn(e[0], e[1]), b = __floats2half2_rn(e[2], e[3]);
+  auto cut = [&]() {  // the upper bytes, which a and b lose
+    const uint32_t u = *reinterpret_cast<uint32_t*>(&a), v = *reinterpret_cast<uint32_t*>(&b);
+    const uint32_t x = u & 0xff00ff00u, y = v & 0xff00ff00u;
+    a = __hsub2(a, *reinterpret_cast<const __half2*>(&x));
+    b = __hsub2(b, *reinterpret_cast<const __half2*>(&y));
+    return __byte_perm(u, v, 0x7531);
+  };
+  hi = cut();
+  mid = cut();
+  lo = uint32_t(__nv_cvt_halfraw2_to_fp8x2(__half2_raw(a), __NV_SATFINITE, __NV_E5M2)) |
+       uint32_t(__nv_cvt_halfraw2_to_fp8x2(__half2_raw(b), __NV_SATFINITE, __NV_E5M2)) << 16;
 }
 
 // What the cleared elements of column d (drafted values that are not finite) add to a row of

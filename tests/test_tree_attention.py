@@ -13,8 +13,12 @@ value's scale).  16 p s / m is stored, m at most that largest, in two e4m3 piece
 smallest step is 2^-9: a smaller p is off by at most 2^-10 / 16 = 2^-14 of max(p s) / s, and
 out by 2^-14 max(p) / sum p x (sum of the |v| a row sees) x (largest s / smallest s), which is
 2 for rows of 256 normal numbers, whose largest lies in (1.75, 7].  Where a row sees few keys
-of very different weights (``small``) this is added.
+of very different weights (``small``) this is added.  (Such were two e4m3 pieces.  Three e5m2 ones
+are off by 2^-8.8 of a probability down to 2^-20 of the largest, and by 2^-28 of that below: the later
+tests here take no such allowance.)
 """
+
+import functools
 
 import numpy as np
 import pytest
@@ -589,3 +593,77 @@ def test_scales_of_one_throughout(cuda_device, T):
         out, again = p.attend()
         assert torch.equal(out, first) and torch.equal(again, lse)
     assert cache.status(p.pool) == 0
+
+
+@functools.lru_cache(maxsize=2)
+def _long_pages(dev, flat, n):
+    """Pages of n + 65 tokens of four heads: unit-normal keys (all zeros with ``flat``) but for the first
+    column and the first key, values with a common mean."""
+    g = torch.Generator().manual_seed(1000 + n)
+    k, v = (torch.randn((1, 4, n + 65, 256), generator=g) for _ in range(2))
+    if flat:
+        k.zero_()
+    k[..., 0] = 0.0
+    v += 0.5
+    per = -(-(n + 65) // 128)
+    pool = cache.PagedCache.empty(per, 4, 128, E4M3, dev)
+    table = torch.arange(per, dtype=torch.int32, device=dev)[None]
+    cache.write(pool, k.to(dev), v.to(dev), table, torch.zeros(1, dtype=torch.int32, device=dev))
+    return pool, table, [torch.as_tensor(y * s[..., None]) for y, s in map(decode.quantise, (k, v))]
+
+
+class Sink:
+    """One key that holds `share` of every row's weight before `n` others, whose scores are unit
+    normals (or, `flat`, all equal); 40 sequences of four key/value heads share the pages, so that a
+    worker has a whole head's keys.  The first column of every query is 8 and that of the other
+    keys 0, so the first key's score is half of its first column."""
+
+    def __init__(self, dev, T, n, share, flat, B=40):
+        self.pool, table, (k, v) = _long_pages(dev, flat, n)
+        first = torch.zeros(1, 4, 1, 256)
+        mass = float(np.log(n)) + (0.0 if flat else 0.5)  # log of the other keys' sum
+        first[..., 0] = 2.0 * (mass + np.log(share / (1.0 - share)))
+        zero = torch.zeros(1, dtype=torch.int32, device=dev)
+        cache.write(self.pool, first.to(dev), v[:, :, :1].float().to(dev), table, zero)
+        y, s = decode.quantise(first)
+        self.k, self.v = k[0].clone(), v[0]
+        self.k[:, :1] = torch.as_tensor(y * s[..., None])[0]
+        self.table = table.expand(B, -1).contiguous()
+        q = torch.randn((B, 16, T, 256), generator=torch.Generator().manual_seed(2000 + T))
+        q[..., 0] = 8.0
+        self.q, self.ctx = q.to(BF16), n + 1
+        self.lens = torch.full((B,), n + 1, dtype=torch.int32, device=dev)
+
+    def check(self, out, lse, rows):
+        T = self.q.shape[2]
+        for b in rows:
+            for t in sorted({0, T // 2, T - 1}):  # of a chain
+                o, l, spread = decode.tree_attention(self.q[b][:, t:t + 1], self.k, self.v, self.ctx + t, 1)
+                assert np.abs(lse[b, :, t:t + 1].double().cpu().numpy() - l).max() <= 2e-4
+                tol = 2.0 ** -8 * (np.abs(o) + spread) + 4e-4 * spread
+                off = np.abs(out[b, :, t:t + 1].double().cpu().numpy() - o) / tol
+                assert off.max() <= 1.0, f"sequence {b}, token {t}: {off.max():.1f} times the tolerance"
+
+
+@pytest.mark.parametrize("share", [0.05, 0.2, 0.5, 0.95])
+@pytest.mark.parametrize("flat", [False, True], ids=["normal", "flat"])
+@pytest.mark.parametrize("T", [1, 5, 12, 24, 64])
+def test_one_key_outweighs_a_long_context(cuda_device, T, flat, share):
+    """Quantised pages keep the weight of many small probabilities beside a large one, at the
+    plain tolerance of the module's head: a probability is off by 2^-9 + 2^-11 of itself, or by 2^-28 of the
+    largest, 2^-13 of it for all 32,768 keys together.  Alone and in a batch alike."""
+    p = Sink(cuda_device, T, 32_768, share, flat)
+    q = p.q.to(cuda_device)
+    p.check(*cache.attend(q, p.pool, p.table, p.lens), rows=(0, 39))
+    p.check(*cache.attend(q[:1], p.pool, p.table[:1], p.lens[:1]), rows=(0,))
+    assert cache.status(p.pool) == 0
+
+
+@pytest.mark.parametrize("T,Hq,page", [(3, 8, 16), (40, 16, 8), (64, 16, 16), (33, 32, 64)])
+def test_few_quantised_keys_at_the_plain_tolerance(cuda_device, T, Hq, page):
+    """Rows that see few keys of very different weights: the pieces of a probability need no
+    allowance for its size."""
+    p = Problem(cuda_device, 4, Hq, 4, T, [0, 130, 700, 63], page, BF16, E4M3, seed=140 + T, drafted=[T, T - 2, 1, 0])
+    p.check(*p.attend())
+    mask = np.stack([_tree(T, 60 + b) for b in range(4)])
+    p.check(*p.attend(mask), mask=mask)
