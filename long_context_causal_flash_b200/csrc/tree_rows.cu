@@ -522,7 +522,7 @@ __global__ void __launch_bounds__(RowsCfg<kFp8>::kThreads, 1) tree_rows_kernel(c
         umma::fence_after_sync();
         // Values that take no part, as in tree_tc.cu.  Quarter 0's warps look after the 128 keys.
         // (After S: both CTAs of a pair have then begun this segment.)
-        const bool gone = !((there >> lane) & 1u), drafted = !gone && p.T > 1 && j0 + lane >= g.s.ctx;
+        const bool gone = !((there >> lane) & 1u), drafted = !gone && j0 + lane >= g.s.ctx;
         const bool cleared = quarter == 0 && __any_sync(0xffffffffu, gone || drafted);
         if (cleared) {
           fine = values_there() && fine;

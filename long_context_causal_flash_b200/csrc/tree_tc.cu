@@ -270,6 +270,7 @@ __global__ void __launch_bounds__(Cfg<kN, kFp8>::kThreads, 1) tree_tc_kernel(con
     const int rows_all = p.T * p.G;
     const int row0 = rt * kN;  // this CTA's first row among the T G of a head
     const uint32_t slot_mask = (1u << p.c.page_shift) - 1;
+    const bool hides = p.T > 1 || p.mask;  // a drafted token from some row: one token without a mask sees itself
     // The 16-byte unit `i` of key k's P: eight or sixteen rows from n0 on, of a piece.
     auto p_unit = [&](int k, int i, int piece) {
       const bool behind = piece >= F::kSide;
@@ -414,9 +415,9 @@ __global__ void __launch_bounds__(Cfg<kN, kFp8>::kThreads, 1) tree_tc_kernel(con
         // Values that take no part reach a row as 0 x what they are, NaN if that is not finite: those
         // of keys that are not there (a page's rest) are cleared in the tile, and those elements of
         // drafted tokens, which some row may not see; they are added at the end for the rows that do.
-        if (part == 0 && __any_sync(0xffffffffu, page_now < 0 || (drafted && p.T > 1))) {
+        if (part == 0 && __any_sync(0xffffffffu, page_now < 0 || (drafted && hides))) {
           fine = values_there() && fine;
-          if (fine && (page_now < 0 || (drafted && p.T > 1))) {
+          if (fine && (page_now < 0 || (drafted && hides))) {
             uint32_t bad = 0;
 #pragma unroll 1
             for (int c = 0; c < (kFp8 ? 16 : 32); ++c) bad |= mend_unit<kFp8>(value_unit(c), page_now < 0);

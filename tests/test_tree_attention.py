@@ -667,3 +667,25 @@ def test_few_quantised_keys_at_the_plain_tolerance(cuda_device, T, Hq, page):
     p.check(*p.attend())
     mask = np.stack([_tree(T, 60 + b) for b in range(4)])
     p.check(*p.attend(mask), mask=mask)
+
+
+@pytest.mark.parametrize("dtype,kind", PAIRS, ids=IDS)
+@pytest.mark.parametrize("Hq", [4, 32])
+def test_a_single_token_that_its_mask_hides(cuda_device, dtype, kind, Hq):
+    """T = 1 and a mask of 0: the row sees its context alone, whatever the token's key and value are."""
+    p = Problem(cuda_device, 2, Hq, 2, 1, [37, 128], 16, dtype, kind, seed=120)
+    mask = np.zeros((1, 1), dtype=bool)
+    good, good_lse = p.attend(mask)
+    p.check(good, good_lse, mask=mask)
+    for pages in (p.pool.v, p.pool.k):
+        for b, c in enumerate(p.ctx):
+            pages.view(torch.uint8).view(*pages.shape[:3], -1)[p.table[b, c // 16], :, c % 16] = 0xff  # NaN
+        out, lse = p.attend(mask)
+        assert torch.equal(out, good) and torch.equal(lse, good_lse)
+    if kind != E4M3:
+        for b, c in enumerate(p.ctx):
+            p.pool.v[p.table[b, c // 16], :, c % 16] = float("inf")
+        assert torch.equal(p.attend(mask)[0], good)
+    both = np.stack([mask, ~mask])  # one sequence's token hides, the other's does not
+    out, lse = p.attend(both)
+    assert torch.equal(out[0], good[0]) and out[1].isnan().all()
