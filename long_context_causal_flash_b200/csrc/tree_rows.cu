@@ -25,6 +25,8 @@
 // and their conversions to pieces), not the loads.  24 tokens of 4 heads over 8 e4m3 sequences of up
 // to 15,231 keys (159 MB): 73 us against 24.5; 11 pass before the first softmax, 5 per head begun
 // and 4.5 per head written (128 rows of fp32 from every SM at once), 10 in the merge.
+#include <cfloat>
+
 #include "tree_tc.cuh"
 
 namespace gqa {
@@ -452,7 +454,9 @@ __global__ void __launch_bounds__(RowsCfg<kFp8>::kThreads, 1) tree_rows_kernel(c
         return tile < g.t1 && j < g.s.keys ? page_entry(p.c, table, p.max_pages, j) : -1;
       };
       int entry = !kFp8 ? entry_at(g.t0) : -1;
-      float m = -1e30f, l = 0.f;  // this row's maximum (the same in all parts), this part's share of its sum
+      // This row's maximum (the same in all parts), this part's share of its sum.  It starts at the lowest
+      // number rather than -infinity, from which differences would be NaN: any score is above it.
+      float m = -FLT_MAX, l = 0.f;
       for (int tile = g.t0; tile < g.t1; ++tile, ++tt) {
         const uint32_t sb = tt & 1u, ph = (tt >> 1) & 1u;
         const uint32_t j0 = uint32_t(tile) * kTreeTile + part * 32;

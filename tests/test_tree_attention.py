@@ -689,3 +689,26 @@ def test_a_single_token_that_its_mask_hides(cuda_device, dtype, kind, Hq):
     both = np.stack([mask, ~mask])  # one sequence's token hides, the other's does not
     out, lse = p.attend(both)
     assert torch.equal(out[0], good[0]) and out[1].isnan().all()
+
+
+@pytest.mark.parametrize("dtype,kind", PAIRS, ids=IDS)
+@pytest.mark.parametrize("T", [1, 12, 24])
+def test_scores_far_below_zero(cuda_device, dtype, kind, T):
+    """Each row sees its own token only, at a score of -6.25e32: that token's value, not nothing."""
+    p = Problem(cuda_device, 1, 16, 4, T, [0], 16, dtype, kind, seed=121)
+    mask = np.eye(T, dtype=bool)
+    p.q.zero_()
+    p.q[..., 0] = 1e17
+    k = torch.zeros(1, 4, T, 256)
+    k[..., 0] = -1e17
+    k, v = k.to(BF16), torch.randn((1, 4, T, 256), generator=torch.Generator().manual_seed(122)).to(BF16)
+    cache.write(p.pool, k.to(cuda_device), v.to(cuda_device), p.table, torch.zeros_like(p.ctx_dev))
+    if kind == E4M3:
+        k, v = (torch.as_tensor(y * s[..., None]) for y, s in map(decode.quantise, (k, v)))
+    out, lse = p.attend(mask)
+    o, l, _ = decode.tree_attention(p.q[0], k[0], v[0], 0, T, mask)
+    # one product, its scale and the factors 1 / ln 2 and ln 2: each rounds by 2^-24 of the score, and the e4m3
+    # pieces of a query leave 2^-18 of it
+    assert np.all(np.abs(lse[0].double().cpu().numpy() - l) <= np.abs(l) * (8 * 2.0 ** -24 + 2.0 ** -18))
+    # weight 1: a probability's rounding (2^-8), the output's (2^-8)
+    assert np.all(np.abs(out[0].double().cpu().numpy() - o) <= 2.0 ** -7 * np.abs(o))
