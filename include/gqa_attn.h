@@ -427,7 +427,7 @@ typedef struct {
  *                     k and v, multiples of 16 bytes) allow other orders of the first
  *                     three dimensions.
  *   k_scale, v_scale  device fp32 [n_pages][Hkv][page_size], dense: the value of a
- *                     GQA_E4M3 row is code * scale.  NULL for the other dtypes.
+ *                     GQA_E4M3 row is code * scale, of any sign.  NULL for the other dtypes.
  *   status            device, one int32 word that the owner zeroes when it makes the
  *                     pool, or NULL.  The calls record the first device-side error in
  *                     it (GQA_ERR_DEVICE_BOUNDS: a page index outside 0 .. n_pages - 1
@@ -573,6 +573,9 @@ int gqa_attn_cache_read(const gqa_cache_t *cache, const int32_t *page_table, int
  * are; a query is off by 2^-10 after its row is scaled to at most 448, and a probability by
  * 2^-8.8 of itself down to 2^-20 of the largest p x scale that the row sees, and by 2^-28 of that
  * below, so many small ones keep what they hold together (2^-10 of the output at most for 2^18 keys).
+ * That holds for value scales, among the keys of a row, of 2^-100 .. 2^100 in magnitude that lie
+ * within 2^100 of one another, beside values of zeros (whose scale does not matter) of 2^-60 .. 2^60;
+ * a subnormal scale counts as zero.
  * The other pairs of types are multiplied to fp32 accuracy (two tf32 pieces of each fp32 number):
  * there an infinite key makes the rows that see it NaN, and an infinite value their column.
  * Errors: as gqa_attn_cache_write, GQA_ERR_UNSUPPORTED (d, Hq / Hkv, T > 1024,

@@ -49,8 +49,8 @@ struct RowsCfg {
   static constexpr int kOffThere = kOffBad + 128;     // [2][4] words: which keys of the tile are there
   static constexpr int kOffRed = kOffThere + 32;      // [4 parts][128 rows] exchange
   static constexpr int kOffF = kOffRed + 4 * kRows * 4;       // [128] factors of the rows' scores (e4m3)
-  static constexpr int kOffScale = kOffF + (kFp8 ? 512 : 0);  // [2][3][128]: ks, log2 vs, 1 / vs (e4m3)
-  static constexpr int kSmem = kOffScale + (kFp8 ? 2 * 3 * 128 * 4 : 0);
+  static constexpr int kOffScale = kOffF + (kFp8 ? 512 : 0);  // [2][4][128]: ks, what vs does (ValueScale) (e4m3)
+  static constexpr int kSmem = kOffScale + (kFp8 ? 2 * 4 * 128 * 4 : 0);
   static constexpr float kSlack = kFp8 ? 4.f : 8.f;
   static_assert(kSmem <= 232448 && kOffRed % 16 == 0 && sizeof(TreeCursor) <= 40, "shared memory per block");
 };
@@ -253,7 +253,8 @@ __global__ void __launch_bounds__(RowsCfg<kFp8>::kThreads, 1) tree_rows_kernel(c
         // same product, so it costs the softmax nothing.
         if (tt >= 2) ok = warp_wait(bar(kRBarPV + int(b)), ((tt - 2) >> 1) & 1u, budget, status);
         {
-          // A row of zeros (written with scale 1): see tree_tc.cu.
+          uint32_t zeros = 0;  // a bit for each of this lane's keys
+          // A row of zeros is written with scale 1.
           if (__any_sync(0xffffffffu, one)) {
             // The product before is over first, so that the slot's barrier stands at no earlier use.
             if (tt > 0) ok = warp_wait(bar(kRBarPV + int((tt - 1) & 1u)), ((tt - 1) >> 1) & 1u, budget, status) && ok;
@@ -268,22 +269,23 @@ __global__ void __launch_bounds__(RowsCfg<kFp8>::kThreads, 1) tree_rows_kernel(c
                                         uint32_t((i * 32 + lane) % I::kVKeys) * 128u + uint32_t((c & 7) << 4));
                   any |= (v.x | v.y | v.z | v.w) & 0x7f7f7f7fu;
                 }
-                if (any == 0) v_now[i] = 0.f;
+                if (any == 0) zeros |= 1u << i;
               }
             }
             __syncwarp();
           }
-          float* sc = sh_scale + b * 384;
+          float* sc = sh_scale + b * 512 + lane;
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
-            sc[i * 32 + lane] = k_now[i];
-            sc[128 + i * 32 + lane] = v_now[i] == 0.f ? 7.8886090522101181e-31f : v_now[i];  // 2^-100
+            sc[i * 32] = k_now[i];
+            sc[128 + i * 32] = v_now[i];
           }
 #pragma unroll 1
-          for (int i = 128; i < 256; i += 32) {  // one key's code, as with Q
-            const float v = sc[i + lane];
-            sc[i + lane] = log2f(v);
-            sc[128 + i + lane] = 1.f / v;
+          for (int i = 0; i < 4; ++i, sc += 32) {  // one key's code, as with Q
+            const ValueScale s(sc[128], (zeros >> i) & 1u);
+            sc[128] = s.log2;
+            sc[256] = s.inv;
+            sc[384] = s.store;
           }
         }
         if (lane < 4) sh_there[b * 4 + lane] = lane == 0 ? there[0] : lane == 1 ? there[1] : lane == 2 ? there[2] : there[3];
@@ -505,7 +507,7 @@ __global__ void __launch_bounds__(RowsCfg<kFp8>::kThreads, 1) tree_rows_kernel(c
           there = __ballot_sync(0xffffffffu, page >= 0);
           entry = entry_at(tile + 1);
         }
-        const float* scale = sh_scale + sb * 384 + part * 32;
+        const float* scale = sh_scale + sb * 512 + part * 32;
         uint32_t vis = there;
         const bool drafted_tile = j0 + 32 > g.s.ctx && vis != 0;
         if (drafted_tile) {
@@ -615,8 +617,8 @@ __global__ void __launch_bounds__(RowsCfg<kFp8>::kThreads, 1) tree_rows_kernel(c
 #pragma unroll
               for (int k = 0; k < 4; ++k) e[k] = ex2(x[i + k] - m);
               l = fmaf(e[0], inv.x, fmaf(e[1], inv.y, fmaf(e[2], inv.z, fmaf(e[3], inv.w, l))));
-#pragma unroll
-              for (int k = 0; k < 4; ++k) e[k] *= kPScale;
+              const float4 store = *reinterpret_cast<const float4*>(scale + 384 + i);
+              e[0] *= store.x, e[1] *= store.y, e[2] *= store.z, e[3] *= store.w;
               e5m2_pieces4(e, hi[(i - i0) / 4], mid[(i - i0) / 4], lo[(i - i0) / 4]);
             }
             const uint32_t to = lane_addr + 256u + sb * 128u + uint32_t(part * 8 + i0 / 4);
@@ -651,8 +653,8 @@ __global__ void __launch_bounds__(RowsCfg<kFp8>::kThreads, 1) tree_rows_kernel(c
         sync_threads(quarter_bar, 128);
         const float sum = (red(0) + red(1)) + (red(2) + red(3));
         const bool none = !live || sum == 0.f;
-        const float inv = none ? 0.f : (kFp8 ? 1.f / kPScale : 1.f) / sum;
-        const float lse = none ? -INFINITY : (m + log2f(sum)) * kLn2;
+        const float inv = none ? 0.f : 1.f / sum;
+        const float lse = none ? -INFINITY : (m + log2f(sum) - (kFp8 ? kLogSumScale : 0.f)) * kLn2;
         const bool whole = g.whole();
         const int64_t part_row = ((int64_t(worker) * 2 + g.slot()) * p.row_tiles + rt) * kRows;
         const int64_t head = (int64_t(g.b) * p.c.Hkv + g.h) * p.G;
@@ -672,7 +674,7 @@ __global__ void __launch_bounds__(RowsCfg<kFp8>::kThreads, 1) tree_rows_kernel(c
           umma::tmem_ld32(lane_addr + uint32_t(c0), o);
           umma::tmem_wait_ld();
 #pragma unroll
-          for (int i = 0; i < 32; ++i) o[i] = none ? 0.f : o[i] * inv;
+          for (int i = 0; i < 32; ++i) o[i] = none ? 0.f : o[i] * (kFp8 ? kSumScale / kPScale : 1.f) * inv;  // (as in tree_tc.cu)
 #pragma unroll
           for (int i = 0; i < 8; ++i)
             sts16(stage + uint32_t(lane) * 128u + uint32_t((i ^ (lane & 7)) << 4),

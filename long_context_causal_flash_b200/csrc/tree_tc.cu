@@ -261,6 +261,7 @@ __global__ void __launch_bounds__(Cfg<kN, kFp8>::kThreads, 1) tree_tc_kernel(con
   } else {
     // ---------------------------------------------------------------- softmax
     constexpr uint32_t kAll = 32 * F::kSoftWarps;  // threads of barrier 15
+    constexpr float kLogSum = kFp8 ? kLogSumScale : 0.f, kOut = kFp8 ? kSumScale / kPScale : 1.f;
     const int quarter = warp & 3, part = warp >> 2;
     const uint32_t part_bar = 1u + uint32_t(part);
     const int n0 = part * C;              // first row (column of S^T and O^T) of this thread
@@ -374,7 +375,9 @@ __global__ void __launch_bounds__(Cfg<kN, kFp8>::kThreads, 1) tree_tc_kernel(con
                  uint32_t(key % I::kVKeys) * 128u + uint32_t(((c ^ key) & 7) << 4);
         };
         const float ks = kFp8 ? (page < 0 ? 0.f : ks_next) : p.scale_log2;
-        float vs = kFp8 && page >= 0 ? vs_next : 1.f, lvs = 0.f, inv_vs = 1.f;
+        const float vs = kFp8 && page >= 0 ? vs_next : 1.f;
+        float lvs = 0.f, inv_vs = 1.f, store = 1.f;
+        (void)store;
         const int page_now = page;
         page = checked(tile + 1, entry_next);
         scales_at(tile + 1, page, &ks_next, &vs_next);
@@ -394,8 +397,8 @@ __global__ void __launch_bounds__(Cfg<kN, kFp8>::kThreads, 1) tree_tc_kernel(con
         const bool masked = __any_sync(0xffffffffu, vis != 0xffffffffu && (C == 32 || (vis & 0xffffu) != 0xffffu));
         bool fine = ok;
         if constexpr (kFp8) {
-          // A row of zeros (written with scale 1) puts nothing into O: its scale must not set the
-          // maximum, on which P's few bits hang.  2^-100 keeps the row's weight in the sums.
+          // A row of zeros is written with scale 1.
+          bool zeros = false;
           if (__any_sync(0xffffffffu, page_now >= 0 && vs == 1.f)) {
             fine = values_there() && fine;
             uint32_t any = 0;
@@ -405,12 +408,11 @@ __global__ void __launch_bounds__(Cfg<kN, kFp8>::kThreads, 1) tree_tc_kernel(con
                 const uint4 v = lds16(value_unit(c));
                 any |= (v.x | v.y | v.z | v.w) & 0x7f7f7f7fu;
               }
-            if (vs == 1.f && any == 0) vs = 0.f;
+            zeros = vs == 1.f && any == 0;
             __syncwarp();
           }
-          if (vs == 0.f) vs = 7.8886090522101181e-31f;
-          lvs = log2f(vs);
-          inv_vs = 1.f / vs;
+          const ValueScale s(vs, zeros);
+          lvs = s.log2, inv_vs = s.inv, store = s.store;
         }
         // Values that take no part reach a row as 0 x what they are, NaN if that is not finite: those
         // of keys that are not there (a page's rest) are cleared in the tile, and those elements of
@@ -533,7 +535,7 @@ __global__ void __launch_bounds__(Cfg<kN, kFp8>::kThreads, 1) tree_tc_kernel(con
 #pragma unroll
               for (int k = 0; k < 4; ++k) {
                 l[c0 + i + k] = fmaf(x[i + k], inv_vs, l[c0 + i + k]);
-                e[k] = x[i + k] * kPScale;
+                e[k] = x[i + k] * store;
               }
               e5m2_pieces4(e, hi[i / 4], mid[i / 4], lo[i / 4]);
             } else {
@@ -591,9 +593,9 @@ __global__ void __launch_bounds__(Cfg<kN, kFp8>::kThreads, 1) tree_tc_kernel(con
           const int c0 = lane & 16, n = lane & 15;
           const float sum = (get(c0, 0, n) + get(c0, 1, n)) + (get(c0, 2, n) + get(c0, 3, n));
           const bool none = my_t >= d.s.drafted || sum == 0.f;
-          inv = none ? 0.f : (kFp8 ? 1.f / kPScale : 1.f) / sum;
+          inv = none ? 0.f : 1.f / sum;
           if (quarter == 0) {
-            const float lse = none ? -INFINITY : (sh_m[n0 + lane] + log2f(sum)) * kLn2;
+            const float lse = none ? -INFINITY : (sh_m[n0 + lane] + log2f(sum) - kLogSum) * kLn2;
             if (whole)
               p.lse[(head_row + (my_row & (p.G - 1))) * p.T + my_t] = lse;
             else
@@ -626,7 +628,7 @@ __global__ void __launch_bounds__(Cfg<kN, kFp8>::kThreads, 1) tree_tc_kernel(con
             const int64_t at = (whole ? (head_row + (row & (p.G - 1))) * p.T + t : part_at + n0 + c0 + i) * kHeadDim + key;
 #pragma unroll
             for (int half = 0; half < 2; ++half) {
-              float v = f == 0.f ? 0.f : o[half][i] * f;
+              float v = f == 0.f ? 0.f : o[half][i] * kOut * f;  // in this order: a sum may be near either end of fp32
               if (bad && f != 0.f) v += hidden_values<kFp8>(p, d, table, sh_bad, t, half * 128 + key);
               if (row >= rows_all) continue;
               if (whole)

@@ -384,6 +384,25 @@ inline bool encode_pages(CUtensorMap* m, const CacheView& c, bool values) {
   return values ? encode_tokens(m, c, c.v, fp8 ? 64 : 32, fp8 ? 2 : 4, 1) : encode_tokens(m, c, c.k, 128, 1, 1);
 }
 
+// What the scale of a quantised value does to its key: scores get log2 of its magnitude, P
+// is stored times `store`, and a row's sum takes P times `inv`.  A row that puts nothing into O (its
+// scale is zero or subnormal, or `zeros`: so are its codes) is stored as 0, and its score
+// gets kNoValue, so that it does not set the maximum, on which P's bits hang.  kSumScale
+// keeps the sums of values that are tiny throughout within range.  A scale that is not a
+// number reaches the rows that see the key through its score alone.
+constexpr float kNoValue = -60.f;
+constexpr float kLogSumScale = -24.f, kSumScale = 5.9604644775390625e-8f;  // 2^-24
+struct ValueScale {
+  float log2, inv, store;
+  __device__ __forceinline__ ValueScale(float vs, bool zeros) {
+    const float a = fabsf(vs);
+    const bool none = zeros || a < 1.1754943508222875e-38f;  // 2^-126
+    log2 = none ? kNoValue : log2f(a);
+    inv = none ? kSumScale * 1152921504606846976.f /* 2^60 */ : a < INFINITY ? kSumScale / a : 1.f;
+    store = none ? 0.f : copysignf(kPScale, vs);
+  }
+};
+
 // One 16-byte unit of a value in shared memory: cleared whole, or its elements that are not
 // finite (e4m3 has NaN alone); returns whether it had any of the latter.
 template <bool kFp8>

@@ -712,3 +712,62 @@ def test_scores_far_below_zero(cuda_device, dtype, kind, T):
     assert np.all(np.abs(lse[0].double().cpu().numpy() - l) <= np.abs(l) * (8 * 2.0 ** -24 + 2.0 ** -18))
     # weight 1: a probability's rounding (2^-8), the output's (2^-8)
     assert np.all(np.abs(out[0].double().cpu().numpy() - o) <= 2.0 ** -7 * np.abs(o))
+
+
+@pytest.mark.parametrize("T", [1, 5, 12, 24])
+def test_value_scales_of_any_sign_and_size(cuda_device, T):
+    """The value of a row is code x scale for any fp32 scale: of either sign, zero or subnormal,
+    tiny or huge throughout; a scale that is not a number stays behind the mask that hides it."""
+    dev, ctx = cuda_device, [700, 40]
+    p = Problem(dev, 2, 16, 4, T, ctx, 32, BF16, E4M3, seed=130 + T)
+    n, per = p.v.shape[2], p.table.shape[1]
+    at = p.table.cpu().long()
+    place = torch.arange(n)
+    where = [(at[b][place // 32], place % 32) for b in range(2)]
+
+    def scales(fill):  # fill(b, j, head) -> a factor of the scale, for every place
+        kept = p.pool.v_scale.clone()
+        f = torch.ones(2, n, 4)
+        fill(f)
+        s = p.pool.v_scale.cpu()
+        value = p.v.clone()
+        for b in range(2):
+            page, slot = where[b]
+            s[page, :, slot] = s[page, :, slot] * f[b]
+            value[b] = p.v[b] * f[b].double().T[..., None]
+        p.pool.v_scale.copy_(s)
+        got = p.attend()
+        p.pool.v_scale.copy_(kept)
+        return got, value
+
+    def check(fill):
+        (out, lse), value = scales(fill)
+        for b in range(2):
+            o, l, spread = decode.tree_attention(p.q[b], p.k[b], value[b], ctx[b], T)
+            assert np.abs(lse[b].double().cpu().numpy() - l).max() <= 2e-4
+            tol = 2.0 ** -8 * (np.abs(o) + spread) + 4e-4 * spread
+            assert np.all(np.abs(out[b].double().cpu().numpy() - o) <= tol)
+
+    g = torch.Generator().manual_seed(131)
+    sign = torch.where(torch.rand((2, n, 4), generator=g) < 0.5, -1.0, 1.0)
+    check(lambda f: f.copy_(sign))
+    check(lambda f: f[:, ::3].fill_(0.0))
+    check(lambda f: f[:, ::3].fill_(2.0 ** -126))  # subnormal: too little to reach the output
+    for size in (2.0 ** -111, 2.0 ** -40, 2.0 ** 50, 2.0 ** 100):
+        check(lambda f: f.fill_(size))
+
+    def with_zeros(f):  # zero rows as the writer leaves them, beside large ones
+        f.fill_(2.0 ** 50)
+        f[:, 1::2] = 0.0
+
+    check(with_zeros)
+    if T > 1:  # a drafted token whose scale is not a number, hidden from the rows before it
+        good, good_lse = p.attend()
+        for bad in (float("nan"), float("inf"), 1e-42):
+            kept = p.pool.v_scale.clone()
+            for b in range(2):
+                j = ctx[b] + T - 1
+                p.pool.v_scale[at[b][j // 32], :, j % 32] = bad
+            out, lse = p.attend()
+            p.pool.v_scale.copy_(kept)
+            assert torch.equal(out[:, :, :-1], good[:, :, :-1]) and torch.equal(lse[:, :, :-1], good_lse[:, :, :-1])
