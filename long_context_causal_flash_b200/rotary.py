@@ -125,27 +125,33 @@ def rotate(q, k, table, *, positions=None, pos_offset=0, inverse=False, out=None
 
 
 class _Rotate(torch.autograd.Function):
-    """rotate as the forward, the inverse rotation of the gradients as the backward."""
+    """rotate as the forward, the inverse rotation of the gradients as the backward, itself
+    differentiable: the rotation is linear, so that is right to any order."""
 
     @staticmethod
-    def forward(ctx, q, k, table, positions, pos_offset):
-        ctx.table, ctx.pos_offset = table, pos_offset
+    def forward(ctx, q, k, table, positions, pos_offset, inverse):
+        ctx.table, ctx.pos_offset, ctx.inverse = table, pos_offset, inverse
         ctx.save_for_backward(positions)
-        ctx.shapes = (q.shape, None if k is None else k.shape)
-        out, out_k = rotate(q, k, table, positions=positions, pos_offset=pos_offset)
+        out, out_k = rotate(q, k, table, positions=positions, pos_offset=pos_offset, inverse=inverse)
         return out if k is None else (out, out_k)
 
     @staticmethod
     def backward(ctx, dq, dk=None):
         (positions,) = ctx.saved_tensors
-        kw = dict(positions=positions, pos_offset=ctx.pos_offset, inverse=True)
         dq, dk = _dense_rows(dq), _dense_rows(dk)
+
+        def back(a, b):
+            if torch.is_grad_enabled():  # create_graph
+                got = _Rotate.apply(a, b, ctx.table, positions, ctx.pos_offset, not ctx.inverse)
+                return (got, None) if b is None else got
+            return rotate(a, b, ctx.table, positions=positions, pos_offset=ctx.pos_offset, inverse=not ctx.inverse)
+
         if dq is not None and dk is not None and dq.dtype == dk.dtype:
-            dq, dk = rotate(dq, dk, ctx.table, **kw)
+            dq, dk = back(dq, dk)
         else:
-            dq = None if dq is None else rotate(dq, None, ctx.table, **kw)[0]
-            dk = None if dk is None else rotate(dk, None, ctx.table, **kw)[0]
-        return dq, dk, None, None, None
+            dq = None if dq is None else back(dq, None)[0]
+            dk = None if dk is None else back(dk, None)[0]
+        return dq, dk, None, None, None, None
 
 
 def _dense_rows(g):
@@ -158,8 +164,8 @@ def _dense_rows(g):
 
 
 def rotate_autograd(q, k, table, *, positions=None, pos_offset=0):
-    """Differentiable ``rotate`` (new tensors); ``k`` may be ``None``.  The positions carry
-    no gradient."""
+    """Differentiable ``rotate`` (new tensors), to any order; ``k`` may be ``None``.  The
+    positions carry no gradient."""
     if k is None:
-        return _Rotate.apply(q, None, table, positions, int(pos_offset)), None
-    return _Rotate.apply(q, k, table, positions, int(pos_offset))
+        return _Rotate.apply(q, None, table, positions, int(pos_offset), False), None
+    return _Rotate.apply(q, k, table, positions, int(pos_offset), False)

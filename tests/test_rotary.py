@@ -189,3 +189,27 @@ def test_refusals(cuda_device):
     raw = torch.zeros(2 * 3 * 8 * 256 + 1, device=cuda_device)
     with pytest.raises(GqaAttnError):
         rotary.rotate(raw[1:].view(2, 3, 8, 256), None, t)
+
+
+def test_second_derivatives(cuda_device):
+    """The rotation is linear: the gradient's own gradient is the rotation, to any order."""
+    t = rotary.Table(96, layout="interleaved", scaling="yarn", factor=4.0, original_length=64)
+    q, k = _x((2, 3, 9, 256), torch.float32, 20), _x((2, 1, 9, 256), torch.float32, 21)
+    dq, dk, uq, uk = (_x(x.shape, torch.float32, 22 + i) for i, x in enumerate((q, k, q, k)))
+    qd, kd, dqd, dkd = (x.to(cuda_device).requires_grad_() for x in (q, k, dq, dk))
+    pos = torch.tensor([[3, 900_000, 7, 0, 1, 2, 5, 9, 8]] * 2, dtype=torch.int32, device=cuda_device)
+    out = rotary.rotate_autograd(qd, kd, t, positions=pos)
+    gq, gk = torch.autograd.grad(out, (qd, kd), (dqd, dkd), create_graph=True)
+    hq, hk = torch.autograd.grad((gq, gk), (dqd, dkd), (uq.to(cuda_device), uk.to(cuda_device)), create_graph=True)
+    _check(gq.detach(), dq, pos.cpu().numpy(), t, sign=-1.0)
+    _check(hq.detach(), uq, pos.cpu().numpy(), t)
+    _check(hk.detach(), uk, pos.cpu().numpy(), t)
+    # a penalty on the gradient's size, as a user writes it: d / dq of |dL / dq|^2 / 2 with L = |rotated q|^2 / 2
+    m = t.magnitude
+    out, _ = rotary.rotate_autograd(qd, None, t, positions=pos)
+    (g,) = torch.autograd.grad(0.5 * out.square().sum(), qd, create_graph=True)
+    (p,) = torch.autograd.grad(0.5 * g.square().sum(), qd)
+    want = q.double().numpy().copy()
+    want[..., :96] *= m ** 4  # turned and turned back twice, by m each time
+    # four rotations, each off by 8 e m (|x1| + |x2|) (see the module's head), of pairs whose terms are below 12 m^3
+    assert np.abs(p.double().cpu().numpy() - want).max() <= 4 * 8 * E * m * 24 * m ** 3
