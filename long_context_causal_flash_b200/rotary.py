@@ -132,13 +132,15 @@ class _Rotate(torch.autograd.Function):
     def forward(ctx, q, k, table, positions, pos_offset, inverse):
         ctx.table, ctx.pos_offset, ctx.inverse = table, pos_offset, inverse
         ctx.save_for_backward(positions)
+        ctx.set_materialize_grads(False)  # an output that the loss does not use has no gradient, not one of zeros
         out, out_k = rotate(q, k, table, positions=positions, pos_offset=pos_offset, inverse=inverse)
         return out if k is None else (out, out_k)
 
     @staticmethod
     def backward(ctx, dq, dk=None):
         (positions,) = ctx.saved_tensors
-        dq, dk = _dense_rows(dq), _dense_rows(dk)
+        dq = _dense_rows(dq) if ctx.needs_input_grad[0] else None
+        dk = _dense_rows(dk) if ctx.needs_input_grad[1] else None
 
         def back(a, b):
             if torch.is_grad_enabled():  # create_graph
@@ -146,11 +148,10 @@ class _Rotate(torch.autograd.Function):
                 return (got, None) if b is None else got
             return rotate(a, b, ctx.table, positions=positions, pos_offset=ctx.pos_offset, inverse=not ctx.inverse)
 
-        if dq is not None and dk is not None and dq.dtype == dk.dtype:
+        if dq is not None:
             dq, dk = back(dq, dk)
-        else:
-            dq = None if dq is None else back(dq, None)[0]
-            dk = None if dk is None else back(dk, None)[0]
+        elif dk is not None:
+            dk, _ = back(dk, None)
         return dq, dk, None, None, None, None
 
 

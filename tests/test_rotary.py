@@ -213,3 +213,29 @@ def test_second_derivatives(cuda_device):
     want[..., :96] *= m ** 4  # turned and turned back twice, by m each time
     # four rotations, each off by 8 e m (|x1| + |x2|) (see the module's head), of pairs whose terms are below 12 m^3
     assert np.abs(p.double().cpu().numpy() - want).max() <= 4 * 8 * E * m * 24 * m ** 3
+
+
+def test_gradients_that_nobody_asked_for_are_not_computed(cuda_device, monkeypatch):
+    t = rotary.Table(64, device=cuda_device)
+    q, k = (_x((2, h, 7, 256), torch.bfloat16, 30 + h).to(cuda_device) for h in (2, 1))
+    turned = []
+    real = rotary.rotate
+    monkeypatch.setattr(rotary, "rotate", lambda a, b, *args, **kw: (turned.append((a is not None, b is not None)),
+                                                                     real(a, b, *args, **kw))[1])
+
+    def back(need_q, need_k, loss):
+        qd, kd = q.clone().requires_grad_(need_q), k.clone().requires_grad_(need_k)
+        qo, ko = rotary.rotate_autograd(qd, kd, t)
+        turned.clear()
+        loss(qo, ko).backward()
+        return qd.grad, kd.grad
+
+    both = lambda qo, ko: qo.float().square().sum() + ko.float().square().sum()  # noqa: E731
+    gq, gk = back(True, False, both)
+    assert turned == [(True, False)] and gk is None
+    alone, _ = back(True, True, lambda qo, ko: qo.float().square().sum())
+    assert turned == [(True, False)] and torch.equal(alone, gq)
+    _, gk = back(True, True, lambda qo, ko: ko.float().square().sum())
+    assert turned == [(True, False)] and gk is not None  # k's gradient alone, as the launch's first tensor
+    gq2, gk2 = back(True, True, both)
+    assert turned == [(True, True)] and torch.equal(gq2, gq) and torch.equal(gk2, gk)
