@@ -156,12 +156,13 @@ class _Rotate(torch.autograd.Function):
 
 
 def _dense_rows(g):
-    """A gradient as ``rotate`` takes it: autograd may hand in expanded or sliced ones."""
+    """A gradient as ``rotate`` takes it: autograd may hand in expanded or sliced ones, and dense
+    ones that start anywhere (a part of a concatenated tensor's), which are contiguous as they are."""
     if g is None:
         return None
     unit = 16 // g.element_size()
     whole = g.stride(3) == 1 and all(s % unit == 0 for s in g.stride()[:3]) and g.data_ptr() % 16 == 0
-    return g if whole else g.contiguous()
+    return g if whole else g.clone(memory_format=torch.contiguous_format)
 
 
 def rotate_autograd(q, k, table, *, positions=None, pos_offset=0):

@@ -239,3 +239,16 @@ def test_gradients_that_nobody_asked_for_are_not_computed(cuda_device, monkeypat
     assert turned == [(True, False)] and gk is not None  # k's gradient alone, as the launch's first tensor
     gq2, gk2 = back(True, True, both)
     assert turned == [(True, True)] and torch.equal(gq2, gq) and torch.equal(gk2, gk)
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_gradients_off_their_alignment(cuda_device, dtype):
+    """A gradient that starts anywhere in memory, as that of a tensor that was concatenated does."""
+    t = rotary.Table(64, device=cuda_device)
+    q = _x((2, 2, 7, 256), dtype, 33)
+    w = _x((q.numel() + 1,), dtype, 34).to(cuda_device)
+    qd = q.to(cuda_device).requires_grad_()
+    out, _ = rotary.rotate_autograd(qd, None, t)
+    head = torch.zeros(1, dtype=dtype, device=cuda_device, requires_grad=True)
+    torch.cat((head, out.reshape(-1))).backward(w)
+    _check(qd.grad, w[1:].view(q.shape).cpu(), [np.arange(7)], t, sign=-1.0)
