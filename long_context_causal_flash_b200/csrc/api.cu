@@ -106,6 +106,8 @@ TcLayout tc_layout(size_t base, int B, int Hq, int Hkv, int64_t Lq, int64_t Lk) 
 constexpr int kMaxSplits = 16;
 constexpr int kB200Sms = 148;
 
+}  // namespace
+
 // Test hook: GQA_ATTN_TEST_SKIP_FILL=n makes the key/value producer of every CTA
 // skip its fill n (read at every call, so a test can clear it between calls).
 int test_skip_fill() {
@@ -115,8 +117,6 @@ int test_skip_fill() {
   }
   return -1;
 }
-
-}  // namespace
 
 int64_t wait_budget_ns() {
   static int64_t budget = -1;

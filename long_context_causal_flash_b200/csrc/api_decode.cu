@@ -192,6 +192,7 @@ int gqa_attn_fwd_tree(const gqa_rows_t* q, const gqa_cache_t* cache, const int32
   p.out_bf16 = dtype == GQA_BF16;
   p.scale_log2 = float(1.0 / std::sqrt(double(d)) * 1.4426950408889634);
   p.wait_budget_ns = wait_budget_ns();
+  p.test_skip_fill = test_skip_fill();
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   rc = s.tensor ? launch_tree_tc(p, s.rows, st) : launch_tree_f32(p, s.rows, dtype == GQA_BF16, st);
   return rc != GQA_OK ? rc : launch_tree_merge(p, s.rows, st);

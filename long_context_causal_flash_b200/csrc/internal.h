@@ -108,7 +108,9 @@ int launch_cache_write(const CacheView& c, const RowsView& k, const RowsView& v,
 int launch_cache_read(const CacheView& c, const int32_t* table, int64_t max_pages, const int32_t* lens, void* k_out,
                       void* v_out, int B, int64_t max_len, bool bf16, cudaStream_t stream);
 
-// Budget of a bounded device-side wait (GQA_ATTN_WAIT_BUDGET_NS).
+// Budget of a bounded device-side wait (GQA_ATTN_WAIT_BUDGET_NS), and the fill that a test makes
+// the producers skip (-1: none).
 int64_t wait_budget_ns();
+int test_skip_fill();
 
 }  // namespace gqa

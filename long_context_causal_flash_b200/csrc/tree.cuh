@@ -38,6 +38,7 @@ struct TreeParams {
   bool out_bf16;
   float scale_log2;
   int64_t wait_budget_ns;
+  int test_skip_fill;  // test hook (see FwdParams): the keys' producer of every CTA skips this fill of its ring
 };
 
 #if defined(__CUDACC__)

@@ -142,28 +142,29 @@ __device__ __forceinline__ void feed_issue(const TreeParams& p, const CUtensorMa
   const uint32_t n = st.n, j = st.j0 + lane, keys = st.g.s.keys;
   const int left = st.left, b = st.g.b, h = st.g.h;
   if (left == 0) return;
+  const bool skip = !kIsV && int(n) == p.test_skip_fill;  // test hook: neither armed nor copied
   const uint32_t slot = n % kSlots, slot_mask = (1u << p.c.page_shift) - 1, rows = min(1 << p.c.page_shift, kChunk);
   const int page = j < keys ? page_checked(p.c, entry) : -1;
   const uint32_t there = __ballot_sync(0xffffffffu, page >= 0);
-  const bool send = page >= 0 && (lane & (rows - 1)) == 0;
+  const bool send = page >= 0 && (lane & (rows - 1)) == 0 && !skip;
   const uint32_t boxes = __popc(__ballot_sync(0xffffffffu, send));
   if (lane == 0) {
     if (!kIsV) info[slot].there = there;
-    mbar_arrive_expect_tx(full + 8u * slot, boxes * rows * (kHeadDim * kEs));
+    if (!skip) mbar_arrive_expect_tx(full + 8u * slot, boxes * rows * (kHeadDim * kEs));
   }
   __syncwarp();
   if (send)
     tma_load_5d(ring + (slot * kChunk + lane) * uint32_t(kHeadDim * kEs), map, full + 8u * slot, 0, int(j & slot_mask), 0,
                 h, page);
   if constexpr (!kIsV && kCache == GQA_E4M3) {
-    if (page >= 0) {
+    if (page >= 0 && !skip) {
       const int64_t si = ((int64_t(page) * p.c.Hkv + h) << p.c.page_shift) + (j & slot_mask);
       const uint32_t to = smem_u32(info[slot].scale + 2 * lane);
       asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(to), "l"(p.c.ks + si) : "memory");
       asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(to + 4), "l"(p.c.vs + si) : "memory");
     }
     // (a key that is not there has no factors; what stands in their place is not used)
-    asm volatile("cp.async.mbarrier.arrive.noinc.shared.b64 [%0];" ::"r"(full + 8u * slot) : "memory");
+    if (!skip) asm volatile("cp.async.mbarrier.arrive.noinc.shared.b64 [%0];" ::"r"(full + 8u * slot) : "memory");
   }
   __syncwarp();
   if (left > 1) {

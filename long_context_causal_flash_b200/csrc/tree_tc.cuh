@@ -226,6 +226,7 @@ struct Feed {
   int rank = 0;                   // in the pair
   uint32_t slot = 0, parity = 1;  // of the next item; parity: of the wait for the slot to be empty
   int issued = 0;                 // items so far, kSlots at most
+  int fill = 0;                   // items so far (keys: the test hook's count)
   int tile = 0, index = 0, page = -1, page_next = -1;
   bool live = false, whole = false;  // whole: all keys of the tile are there
   // This lane's box: `rows` keys from key `k` of the item on, column block `block`, at `offset` of
@@ -278,7 +279,8 @@ struct Feed {
     const uint32_t full = bar_full + 8u * slot;
     const int at = (kIsV ? index * kKeys : kPair ? rank * kKeys : 0) + k;  // key of the tile
     const int pg = __shfl_sync(0xffffffffu, page, (at >> 3) & 15);
-    const bool send = mine && pg >= 0;
+    const bool skip = !kIsV && fill++ == p.test_skip_fill;  // test hook: neither armed nor copied
+    const bool send = mine && pg >= 0 && !skip;
     uint32_t total = kPair ? 2 * kSlotBytes : kSlotBytes;
     if (!whole) {
       uint32_t boxes = __popc(__ballot_sync(0xffffffffu, send));
@@ -289,7 +291,7 @@ struct Feed {
       }
       total = bytes * boxes;
     }
-    if (lane == 0 && (!kPair || rank == 0)) mbar_arrive_expect_tx(full, total);
+    if (lane == 0 && (!kPair || rank == 0) && !skip) mbar_arrive_expect_tx(full, total);
     __syncwarp();
     if (send) {
       const uint32_t j = uint32_t(tile) * kTreeTile + uint32_t(at), dst = ring + slot * uint32_t(kSlotBytes) + offset;
