@@ -488,7 +488,9 @@ typedef struct {
  *   GQA_ROPE_YARN    by parts: f_i g + f_i / factor (1 - g) with g = clamp((r_i -
  *                    beta_slow) / (beta_fast - beta_slow), 0, 1), r_i = original_length
  *                    f_i / (2 pi) the pair's turns over the length trained on, and
- *                    m = 0.1 ln(factor) + 1 (the YaRN paper, Peng et al. 2023, section 3)
+ *                    m = 0.1 ln(factor) + 1 (the YaRN paper, Peng et al. 2023, section 3; some
+ *                    loaders ramp in i between rounded bounds instead: pass their frequencies to
+ *                    gqa_attn_rope_turns)
  *   m = 1 but for GQA_ROPE_YARN.  GQA_ERR_INVALID_ARG: a null pointer, base <= 1, factor
  *   < 1, original_length < 1 or beta_fast <= beta_slow (GQA_ROPE_YARN), rot of 2 with
  *   GQA_ROPE_NTK, or rot not an even number in 2 .. 256.  Host-only.
@@ -546,7 +548,8 @@ int gqa_attn_cache_read(const gqa_cache_t *cache, const int32_t *page_table, int
                         void *k_out, void *v_out, int B, int64_t max_len, int d, int dtype_out, gqa_stream_t stream);
 
 /*
- * gqa_attn_fwd_tree: attention of T drafted tokens per sequence over the cache.  T = 1 is
+ * gqa_attn_fwd_tree: attention of T drafted tokens per sequence over the cache, B and T at least
+ * 1 as in gqa_attn_fwd (the rotation, the write and the read take 0 and do nothing).  T = 1 is
  * one decoding step.  Sequence b holds context_lens[b] tokens and, behind them, its first
  * tree_lens[b] drafted ones, whose keys and values are in the cache already.  Drafted token
  * t sees the whole context and the drafted tokens u < tree_lens[b] with tree_mask[t][u]:

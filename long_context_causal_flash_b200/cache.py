@@ -165,7 +165,8 @@ def attend(q, pool, page_table, context_lens, *, tree_mask=None, tree_lens=None,
     pool already; ``(out, lse)`` as ``fwd``.  ``tree_mask`` (bool or uint8, [T, T] or [B, T,
     T]): row t sees drafted token u where it is set (its own too has to be); default: a
     chain, u <= t.  ``tree_lens[b]`` < T marks the rows behind it as padding.  A row with no
-    visible key gets 0 and -inf.  Asynchronous on ``stream``."""
+    visible key gets 0 and -inf.  B and T are at least 1, as in ``fwd``: an empty step is an error
+    here, while ``write``, ``read`` and ``rotary.rotate`` do nothing.  Asynchronous on ``stream``."""
     if not (isinstance(q, torch.Tensor) and q.is_cuda and q.dim() == 4):
         raise ValueError("attend takes a 4-d CUDA tensor q")
     dev = pool.device

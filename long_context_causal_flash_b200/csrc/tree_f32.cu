@@ -126,7 +126,7 @@ __device__ __forceinline__ int feed_segment(const TreeParams& p, TreeCursor cur,
     if (live) st.g = g;
     st.j0 = j0;
     st.n = n;
-    st.left = live ? (g.t1 - g.t0)  : 0;
+    st.left = live ? g.t1 - g.t0 : 0;
   }
   __syncwarp();
   return live && j0 + lane < g.s.keys ? page_entry(p.c, p.table + int64_t(g.b) * p.max_pages, p.max_pages, j0 + lane) : -1;
@@ -258,7 +258,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_f32_kernel(const __grid_cons
   bool ok = true;
   TreeSegment g;
   while (tree_next(p, cur, &g)) {
-    const int chunks = (g.t1 - g.t0) ;
+    const int chunks = g.t1 - g.t0;
     // Q's fragments: k = lr of step i of the j-th 16 columns stands for column 4 lr + 2 i of them and
     // k = lr + 4 for the next one, so that a lane has four neighbours of a row in two steps.
     // All loads before their use: one after another they take 9,000 cycles of a cold start.
@@ -357,7 +357,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_f32_kernel(const __grid_cons
       }
       if (c < chunks && srow < kR) {
         float x[2] = {0.f, 0.f};
-  #pragma unroll
+#pragma unroll
         for (int u = 0; u < kParts; ++u) {
           const float2 y = *reinterpret_cast<const float2*>(sh_s + (u * kR + srow) * F::kPitchS + 2 * pair);
           x[0] += y.x, x[1] += y.y;
@@ -367,7 +367,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_f32_kernel(const __grid_cons
         bool vis[2] = {true, true};
         if (masked) {
           uint32_t seen = 0;
-  #pragma unroll
+#pragma unroll
           for (int i = 0; i < 2; ++i) {
             const uint32_t key = 2 * pair + i;
             vis[i] = (there >> key) & 1u;
@@ -377,12 +377,12 @@ __global__ void __launch_bounds__(kThreads, 1) tree_f32_kernel(const __grid_cons
             if (vis[i]) seen |= 1u << key;
             if (!vis[i]) x[i] = -INFINITY;
           }
-  #pragma unroll
+#pragma unroll
           for (int u = 1; u < 16; u <<= 1) seen |= __shfl_xor_sync(0xffffffffu, seen, u);
           if (pair == 0) sh_seen[c & 1][srow] = seen;
         }
         float top = fmaxf(x[0], x[1]);
-  #pragma unroll
+#pragma unroll
         for (int u = 1; u < 16; u <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, u));
         const float m_new = fmaxf(m, top), ref = m_new == -INFINITY ? 0.f : m_new;
         const float alpha = exp2f(m - ref);  // 0 for the first visible key

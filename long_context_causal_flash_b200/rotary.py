@@ -37,7 +37,9 @@ class Table:
     ``"linear"`` (positions divided by ``factor``), ``"ntk"`` (``base`` raised so that the
     slowest pair slows by ``factor``) or ``"yarn"`` (pairs that turn fewer than
     ``beta_slow`` times over ``original_length`` slow by ``factor``, those above
-    ``beta_fast`` do not, and the magnitude is 0.1 ln(factor) + 1).  ``inv_freq`` (a
+    ``beta_fast`` do not, and the magnitude is 0.1 ln(factor) + 1; between the two the
+    ramp is linear in the turns, as in the paper: for a checkpoint whose loader ramps in the pair's
+    index, between bounds rounded to whole pairs, give its frequencies).  ``inv_freq`` (a
     sequence of rot / 2 numbers, with ``magnitude``) replaces all of that by the caller's
     own.  The words the kernels read are copied to ``device`` here, and to another device
     by its first call there: make that call, or ``table.on(device)``, before a capture."""
