@@ -571,8 +571,8 @@ int gqa_attn_cache_read(const gqa_cache_t *cache, const int32_t *page_table, int
  * evenly over the SMs whatever the lengths; partial results are merged in a fixed order, so
  * equal calls give equal bits.
  * Accuracy.  Sums, maxima and the log-sum-exp are fp32.  GQA_BF16 queries over GQA_BF16 pages:
- * products of the numbers as they are; a probability is rounded to bf16 (2^-9 of itself) before it
- * is multiplied with its value, as in gqa_attn_fwd.  Over GQA_E4M3 pages: products of the codes as they
+ * products of the numbers as they are; a probability is off by 2^-15 of itself before it is multiplied
+ * with its value, or, with T Hq / Hkv above 32, rounded to bf16 (2^-8), as in gqa_attn_fwd.  Over GQA_E4M3 pages: products of the codes as they
  * are; a query is off by 2^-10 after its row is scaled to at most 448, and a probability by
  * 2^-8.8 of itself down to 2^-20 of the largest p x scale that the row sees, and by 2^-28 of that
  * below, so many small ones keep what they hold together (2^-10 of the output at most for 2^18 keys).

@@ -20,8 +20,10 @@
 // Softmax: one thread per key and up to 32 rows; the running maximum m of a row is raised
 // only when a score passes it by kSlack (in powers of two), so most tiles need no
 // reduction over the keys and no rescaling of O.  P = 2^(x - m) goes to shared memory as
-// the B operand, over bf16 pages rounded to bf16 (2^-9 of itself: the product then takes the pages as
-// they are, and one of N columns; a second piece would be as many again); the row sum stays with the threads, in fp32, until the end.  For e4m3, x
+// the B operand; the row sum stays with the threads, in fp32, until the end.  Over bf16 pages P is
+// two bf16 pieces up to 32 rows, off by 2^-15 of itself, which memory hides (one token, 60,926
+// keys: 48.4 us with two, 48.0 with one); of more rows it is rounded to one, off by 2^-8 (with two,
+// 64 rows took 3 % longer, and 128 would double the product that bounds them).  For e4m3, x
 // includes log2 of the value's scale, so that m follows the largest product p v rather
 // than the largest p, and P is stored as 2^11 P <= 2^15.
 //
@@ -43,7 +45,7 @@ struct Cfg {
   static constexpr int kParts = kN / kCols;
   static constexpr int kSoftWarps = 4 * kParts;
   static constexpr int kNN = kFp8 ? 2 * kN : kN;  // N of S's products: the query's pieces lie side by side
-  static constexpr int kPieces = kFp8 ? 3 : 1;    // of a probability,
+  static constexpr int kPieces = kFp8 ? 3 : kN > 32 ? 1 : 2;   // of a probability,
   static constexpr int kSide = kFp8 && kN > 32 ? 2 : kPieces;  // of them side by side: a row of P has 128 bytes,
   static constexpr int kNO = kSide * kN;                       // tensor memory 512 columns.  N of O's products
   static constexpr int kQBytes = kN * 512;                     // bf16, or two e4m3 pieces
@@ -526,7 +528,7 @@ __global__ void __launch_bounds__(Cfg<kN, kFp8>::kThreads, 1) tree_tc_kernel(con
           }
           // The row sums, and P.  A wait that ran out here is agreed upon with the next tile.
           if (c0 == 0) ok = last_product() && ok;
-          uint32_t hi[kFp8 ? 4 : 8], mid[4], lo[4];
+          uint32_t hi[kFp8 ? 4 : 8], mid[4], lo[kFp8 ? 4 : 8];
           (void)mid, (void)lo;
 #pragma unroll
           for (int i = 0; i < 16; i += 4) {
@@ -541,8 +543,17 @@ __global__ void __launch_bounds__(Cfg<kN, kFp8>::kThreads, 1) tree_tc_kernel(con
             } else {
 #pragma unroll
               for (int k = 0; k < 4; ++k) l[c0 + i + k] += x[i + k];
-              hi[i / 2] = pack_bf16x2(x[i], x[i + 1]);
-              hi[i / 2 + 1] = pack_bf16x2(x[i + 2], x[i + 3]);
+#pragma unroll
+              for (int k = 0; k < 4; k += 2) {
+                if constexpr (F::kPieces == 1) {
+                  hi[(i + k) / 2] = pack_bf16x2(x[i + k], x[i + k + 1]);
+                } else {
+                  const uint32_t u = __float_as_uint(x[i + k]), v = __float_as_uint(x[i + k + 1]);
+                  hi[(i + k) / 2] = __byte_perm(u, v, 0x7632);  // the upper halves: cut to bf16
+                  lo[(i + k) / 2] = pack_bf16x2(x[i + k] - __uint_as_float(u & 0xffff0000u),
+                                                x[i + k + 1] - __uint_as_float(v & 0xffff0000u));
+                }
+              }
             }
           }
           if constexpr (kFp8) {
@@ -552,6 +563,10 @@ __global__ void __launch_bounds__(Cfg<kN, kFp8>::kThreads, 1) tree_tc_kernel(con
           } else {
             sts16(p_unit(key, c0 / 8, 0), make_uint4(hi[0], hi[1], hi[2], hi[3]));
             sts16(p_unit(key, c0 / 8 + 1, 0), make_uint4(hi[4], hi[5], hi[6], hi[7]));
+            if constexpr (F::kPieces > 1) {
+              sts16(p_unit(key, c0 / 8, 1), make_uint4(lo[0], lo[1], lo[2], lo[3]));
+              sts16(p_unit(key, c0 / 8 + 1, 1), make_uint4(lo[4], lo[5], lo[6], lo[7]));
+            }
           }
         }
         if (stop) {
@@ -610,7 +625,7 @@ __global__ void __launch_bounds__(Cfg<kN, kFp8>::kThreads, 1) tree_tc_kernel(con
           for (int half = 0; half < 2; ++half) {
             const uint32_t a = lane_addr + F::kOffO + uint32_t(half * F::kNO + c0);
             tmem_ld4(a, o[half]);
-            if constexpr (kFp8) {  // the pieces worth least first
+            if constexpr (F::kSide > 1) {  // the pieces worth least first
               float y[F::kSide - 1][4];
 #pragma unroll
               for (int piece = 1; piece < F::kSide; ++piece) tmem_ld4(a + piece * kN, y[piece - 1]);

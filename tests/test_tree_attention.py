@@ -771,3 +771,20 @@ def test_value_scales_of_any_sign_and_size(cuda_device, T):
             out, lse = p.attend()
             p.pool.v_scale.copy_(kept)
             assert torch.equal(out[:, :, :-1], good[:, :, :-1]) and torch.equal(lse[:, :, :-1], good_lse[:, :, :-1])
+
+
+@pytest.mark.parametrize("T,Hq", [(1, 16), (2, 16), (5, 8), (8, 16)])
+def test_probabilities_of_few_rows_are_not_rounded_to_bf16(cuda_device, T, Hq):
+    """Up to 32 rows of a head over bf16 pages: a probability is off by 2^-15 of itself, so an output
+    by its own rounding, 2^-8 of it, and the scores' share.  A score's 255 additions are each off
+    by 2^-24 of at most sum |q k|, below 220 for these inputs: 255 x 220 x 2^-24 / 16 = 2.1e-4, twice
+    that in a probability."""
+    p = Problem(cuda_device, 12, Hq, 4, T, [0, 1, 2, 3, 4, 5, 1, 2, 3, 1, 2, 40], 16, BF16, BF16, seed=150 + T)
+    size = np.abs(p.q.double().numpy()).reshape(12, 4, -1, 256) @ p.k.double().abs().numpy().swapaxes(2, 3)
+    assert size.max() < 220
+    out, lse = p.attend()
+    for b in range(12):
+        o, l, spread = decode.tree_attention(p.q[b], p.k[b], p.v[b], p.ctx[b], T)
+        assert np.abs(lse[b].double().cpu().numpy() - l).max() <= 2.1e-4 + 1e-5
+        tol = 2.0 ** -8 * np.abs(o) + (2.0 ** -15 + 4.2e-4) * spread
+        assert np.all(np.abs(out[b].double().cpu().numpy() - o) <= tol)
