@@ -21,9 +21,10 @@
 // the pair takes 2,850.  64 tokens of 4 heads, 4 sequences of
 // 30,468 bf16 keys (500 MB, 128 GFLOP): 132 us in short runs, 155 - 160 in long ones, whose
 // clock falls (unpaired: 176); 77 for the bytes, as much for the flops.  e4m3 stays
-// single: there the softmax is the bound, 3,700 cycles a tile (128 x 128 exponentials
-// and their conversions to pieces), not the loads.  24 tokens of 4 heads over 8 e4m3 sequences of up
-// to 15,231 keys (159 MB): 73 us against 24.5; 11 pass before the first softmax, 5 per head begun
+// single: there the softmax is the bound within a tile, 3,700 cycles with two pieces (128 x 128
+// exponentials and their conversions; the third costs 2 - 3 %, 77.7 us for 75.3), not the loads.  24
+// tokens of 4 heads over 8 e4m3 sequences of up
+// to 15,231 keys (159 MB): 72 - 81 us against 24.5; 11 pass before the first softmax, 5 per head begun
 // and 4.5 per head written (128 rows of fp32 from every SM at once), 10 in the merge.
 #include <cfloat>
 
