@@ -277,3 +277,32 @@ def test_refusals(cuda_device):
     for kw in (dict(lens=start[:1]), dict(max_len=-1), dict(dtype=E4M3), dict(out=(x, x)), dict(page_table=start)):
         with pytest.raises(ValueError):
             cache.read(pool, **{**dict(page_table=table, lens=start, max_len=4), **kw})
+
+
+@pytest.mark.parametrize("kind", [torch.bfloat16, E4M3], ids=["bf16", "e4m3"])
+@pytest.mark.parametrize("given", [False, True])
+def test_write_of_ragged_lengths_rotates_what_it_writes(cuda_device, kind, given):
+    """lens and rope together, from a projection's view: the first lens[b] tokens turned to their
+    places (or to the positions given), every other slot as it was."""
+    B, L, Hkv, page = 3, 11, 2, 16
+    t = rotary.Table(64, layout="interleaved", device=cuda_device)
+    pool, table = _pool(20, Hkv, page, kind, cuda_device), _table(B, 4, 20, 40, cuda_device)
+    tokens = _x((B, L, 2 * Hkv, 256), torch.bfloat16, 41, False).to(cuda_device)
+    k, v = tokens[:, :, :Hkv].transpose(1, 2), tokens[:, :, Hkv:].transpose(1, 2)
+    lens, start = torch.tensor([11, 0, 4], dtype=torch.int32), torch.tensor([5, 9, 40], dtype=torch.int32)
+    pos = torch.arange(3 * L, dtype=torch.int32).view(B, L) * 7
+    kw = dict(positions=pos.to(cuda_device)) if given else dict(pos_offset=100)
+    cache.write(pool, k, v, table, start.to(cuda_device), lens=lens.to(cuda_device), rope=t, **kw)
+    whole = _pool(20, Hkv, page, kind, cuda_device)
+    places = start.to(cuda_device)[:, None] + 100 + torch.arange(L, dtype=torch.int32, device=cuda_device)
+    # the same rows as one call for each sequence writes, which the tests above hold against the definition
+    for b in range(B):
+        n = int(lens[b])
+        at = pos[b:b + 1, :n].to(cuda_device) if given else places[b:b + 1, :n]
+        cache.write(whole, k[b:b + 1, :, :n], v[b:b + 1, :, :n], table[b:b + 1], start[b:b + 1].to(cuda_device), rope=t,
+                    positions=at.contiguous())
+    for a, w in ((pool.k, whole.k), (pool.v, whole.v)):
+        assert torch.equal(a.view(torch.uint8), w.view(torch.uint8))
+    if kind == E4M3:
+        assert torch.equal(pool.k_scale, whole.k_scale) and torch.equal(pool.v_scale, whole.v_scale)
+    assert cache.status(pool) == 0

@@ -788,3 +788,29 @@ def test_probabilities_of_few_rows_are_not_rounded_to_bf16(cuda_device, T, Hq):
         assert np.abs(lse[b].double().cpu().numpy() - l).max() <= 2.1e-4 + 1e-5
         tol = 2.0 ** -8 * np.abs(o) + (2.0 ** -15 + 4.2e-4) * spread
         assert np.all(np.abs(out[b].double().cpu().numpy() - o) <= tol)
+
+
+@pytest.mark.parametrize("dtype,kind", PAIRS, ids=IDS)
+@pytest.mark.parametrize("T,page", [(1, 256), (12, 1024), (40, 512)])
+def test_large_pages_and_one_page_pools(cuda_device, dtype, kind, T, page):
+    """Pages of more keys than a tile, and a pool of a single page of one head, whose strides
+    of the dimensions of one mean nothing."""
+    p = Problem(cuda_device, 2, 8, 2, T, [1500, 255], page, dtype, kind, seed=160 + T)
+    p.check(*p.attend())
+    p = Problem(cuda_device, 1, 4, 1, T, [100], page, dtype, kind, seed=161)
+    only = int(p.table[0, 0])
+    first = lambda t: None if t is None else t[only:only + 1].contiguous()  # noqa: E731
+    pool = cache.PagedCache(*(first(t) for t in (p.pool.k, p.pool.v, p.pool.k_scale, p.pool.v_scale)))
+    out, lse = cache.attend(p.q.to(cuda_device), pool, torch.zeros_like(p.table), p.ctx_dev)
+    p.check(out, lse)
+
+
+def test_a_thousand_sequences(cuda_device):
+    """More sequences than a warp's lanes many times over, most of them short, some empty."""
+    B = 1000
+    rng = np.random.default_rng(5)
+    ctx = [int(c) for c in rng.integers(0, 40, B)]
+    drafted = [int(d) for d in rng.integers(0, 3, B)]
+    p = Problem(cuda_device, B, 4, 2, 2, ctx, 8, BF16, BF16, seed=170, drafted=drafted)
+    p.check(*p.attend(), rows=list(range(0, B, 7)) + [B - 1])
+    assert cache.status(p.pool) == 0
