@@ -571,14 +571,14 @@ int gqa_attn_cache_read(const gqa_cache_t *cache, const int32_t *page_table, int
  * evenly over the SMs whatever the lengths; partial results are merged in a fixed order, so
  * equal calls give equal bits.
  * Accuracy.  Sums, maxima and the log-sum-exp are fp32.  GQA_BF16 queries over GQA_BF16 pages:
- * products of the numbers as they are; a probability is off by 2^-15 of itself before it is multiplied
- * with its value, or, with T Hq / Hkv above 32, rounded to bf16 (2^-8), as in gqa_attn_fwd.  Over GQA_E4M3 pages: products of the codes as they
- * are; a query is off by 2^-10 after its row is scaled to at most 448, and a probability by
- * 2^-8.8 of itself down to 2^-20 of the largest p x scale that the row sees, and by 2^-28 of that
- * below, so many small ones keep what they hold together (2^-10 of the output at most for 2^18 keys).
- * That holds for value scales, among the keys of a row, of 2^-100 .. 2^100 in magnitude that lie
- * within 2^100 of one another, beside values of zeros (whose scale does not matter) of 2^-60 .. 2^60;
- * a subnormal scale counts as zero.
+ * products of the numbers as they are; a probability is off by 2^-15 of itself before it is
+ * multiplied with its value, or, with T Hq / Hkv above 32, rounded to bf16 (2^-8), as in
+ * gqa_attn_fwd.  Over GQA_E4M3 pages: products of the codes as they are; a query is off by 2^-10
+ * after its row is scaled to at most 448, and a probability by 2^-8.8 of itself down to 2^-20 of
+ * the largest p x scale that the row sees, and by 2^-28 of that below, so many small ones keep what
+ * they hold together (2^18 of them lose 2^-10 of the largest).  That holds for value scales, among the
+ * keys of a row, of 2^-100 .. 2^100 in magnitude that lie within 2^100 of one another, beside values of
+ * zeros (whose scale does not matter) of 2^-60 .. 2^60; a subnormal scale counts as zero.
  * The other pairs of types are multiplied to fp32 accuracy (two tf32 pieces of each fp32 number):
  * there an infinite key makes the rows that see it NaN, and an infinite value their column.
  * Errors: as gqa_attn_cache_write, GQA_ERR_UNSUPPORTED (d, Hq / Hkv, T > 1024,
